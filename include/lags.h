@@ -365,6 +365,143 @@ int lags_trace_read(lags_layout *layout, double *ms, int64_t *launches,
 int32_t lags_num_kernels(void);
 const char *lags_kernel_name(int32_t id);
 
+/*
+ * Activation operators: what a worker's backward pass needs to fill the flat
+ * gradient that lags_sparsify_layers reads, with the activations it keeps held
+ * in 8 bits.  Error compensation costs a worker four bytes a parameter, and
+ * messages and workspace more; 8-bit checkpoints of the activations give that
+ * memory back.  Group normalisation takes its statistics from one sample, so
+ * replicas that exchange only sparse gradients have no running statistics of
+ * the batch to keep alike.
+ *
+ * A matrix is rows x columns, columns (channels) contiguous, `ld` elements
+ * from one row to the next (ld >= columns): a tensor with channels last, or a
+ * slice of its channels.  dtype is LAGS_F32, LAGS_BF16 or LAGS_F16.  Matrices,
+ * parameters and gradients need their element's alignment only (a layer's
+ * slice of a flat buffer starts anywhere); checkpoints and workspaces are
+ * 16-byte aligned.  Conventions are those above; workspaces of these calls
+ * need no initialisation, and one must not be used by two calls that may
+ * overlap in time.  Every sum has a fixed order: results repeat bit for bit.
+ * Sums, statistics and matrix products are held in fp32.
+ */
+#define LAGS_F32 0
+#define LAGS_BF16 1
+#define LAGS_F16 2
+#define LAGS_ACT_NONE 0
+#define LAGS_ACT_RELU 1 /* max(z, 0); gradient 0 at 0 */
+#define LAGS_ACT_SILU 2 /* z / (1 + exp(-z)) */
+#define LAGS_GRAD_ADD 1u /* add to the gradient buffer instead of overwriting it */
+#define LAGS_CKPT_RUN 32 /* columns of a row that share a scale */
+#define LAGS_SLAB_MAX 4096 /* see lags_gn */
+
+/*
+ * 8-bit checkpoint of a [rows, cols] matrix.  Each run of 32 columns of a row
+ * (the last one shorter) is held as signed bytes q and one scale byte s, and
+ * stands for q * 2^(s - 127): s - 127 is the smallest exponent, -126 at least,
+ * for which every value of the run divided by 2^(s - 127), rounded to the
+ * nearest integer with ties to even, is at most 127 in magnitude.  So a value
+ * is off by at most half of 2^(s - 127), 1/128 of the run's largest magnitude,
+ * and is exact in bf16.  A run that holds an infinity or NaN has s = 255 and
+ * q = 0 and reads back as NaN throughout.
+ * Buffer: codes [rows][pitch], pitch = cols rounded up to 16 (pad codes are
+ * 0), then scales [rows][ceil(cols / 32)]; the size is rounded up to 16.
+ * rows >= 0 (0: nothing is launched); 1 <= cols < 2^31.
+ */
+
+/* Bytes of a checkpoint; 0 for rows < 0, cols outside its range, or a size above 2^62. */
+size_t lags_ckpt_bytes(int64_t rows, int64_t cols);
+
+/* Pack x (device, ld = ldx) into ckpt (device, ckpt_bytes >= lags_ckpt_bytes).
+ * Returns LAGS_OK, LAGS_EINVAL (null or misaligned pointer, dtype, ldx < cols,
+ * overlap of x and ckpt), LAGS_ERANGE (rows, cols), LAGS_EWORKSPACE (ckpt null,
+ * misaligned or small), LAGS_EHIP. */
+int lags_ckpt_pack(int64_t rows, int64_t cols, const void *x, int64_t ldx, int32_t dtype,
+                   void *ckpt, size_t ckpt_bytes, void *stream);
+
+/* The values of ckpt, rounded to dtype, into x.  Returns as lags_ckpt_pack. */
+int lags_ckpt_unpack(int64_t rows, int64_t cols, const void *ckpt, size_t ckpt_bytes, void *x,
+                     int64_t ldx, int32_t dtype, void *stream);
+
+/*
+ * Group normalisation with an activation over `samples` blocks of `spatial`
+ * rows, each row `channels` long, channels cut into `groups` equal groups:
+ *   mean, rstd: per sample and group over its spatial * (channels / groups)
+ *               values; rstd = 1 / sqrt(variance + eps), variance over the count;
+ *   xh = (x - mean) * rstd;  z = xh * gamma + beta;  y = act(z)
+ * in fp32, each operation of xh and z rounded by itself.  (spatial = 1 and
+ * groups = 1 is a layer normalisation.)
+ * Limits: samples, spatial in [0, 2^31), channels in [1, 2^31) a multiple of
+ * groups, eps >= 0 and finite.  The smallest number of channels that is both
+ * whole groups and a multiple of 32, or all channels if that is less, is at
+ * most LAGS_SLAB_MAX (else LAGS_ERANGE).
+ */
+typedef struct lags_gn {
+    int64_t samples, spatial, channels, groups;
+    int32_t dtype; /* of x, y, dy and dx */
+    int32_t act;
+    float eps;
+} lags_gn;
+
+/* Bytes of workspace that lags_gn_forward and lags_gn_backward of this shape
+ * need (at least 16); 0 for an invalid shape. */
+size_t lags_gn_workspace_bytes(const lags_gn *gn);
+
+/*
+ * y = act(groupnorm(x)).
+ *   x, y:        device matrices of samples * spatial rows (ldx, ldy); y may
+ *                be x itself (same pointer and ld);
+ *   gamma, beta: device fp32[channels]; both null stand for 1 and 0;
+ *   mean, rstd:  device fp32[samples][groups], out; each may be null;
+ *   ckpt:        null, or a checkpoint buffer of x (samples * spatial rows,
+ *                `channels` columns) that this call packs in the same pass.
+ * With samples or spatial 0 nothing is launched and nothing written.
+ * Returns LAGS_OK, LAGS_EINVAL (null or misaligned pointer, bad shape or ld,
+ * one of gamma and beta null, buffers that overlap), LAGS_ERANGE,
+ * LAGS_EWORKSPACE (ws or ckpt misaligned or small, ws null), LAGS_EHIP.
+ */
+int lags_gn_forward(const lags_gn *gn, const void *x, int64_t ldx, const float *gamma,
+                    const float *beta, void *y, int64_t ldy, float *mean, float *rstd,
+                    void *ckpt, size_t ckpt_bytes, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradients of the forward call for the gradient dy of y:
+ *   dz = dy * act'(z);  dbeta = sum dz;  dgamma = sum dz * xh  (over all rows);
+ *   dx = rstd * (gamma dz - <gamma dz> - xh <gamma dz xh>), < > the mean over
+ *   a sample's group.
+ *   x or ckpt:     the forward's input, or its checkpoint: exactly one is not
+ *                  null; with a checkpoint xh, z and the activation's mask
+ *                  are those of the values it holds;
+ *   mean, rstd:    as the forward left them;
+ *   dx:            device matrix out (lddx); may be dy itself;
+ *   dgamma, dbeta: device fp32[channels], out; each may be null;
+ *   flags:         0 or LAGS_GRAD_ADD (dgamma and dbeta are added to).
+ * With samples or spatial 0 dgamma and dbeta become 0 (unless added to).
+ * Returns as lags_gn_forward.
+ */
+int lags_gn_backward(const lags_gn *gn, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                     const void *ckpt, size_t ckpt_bytes, const float *gamma, const float *beta,
+                     const float *mean, const float *rstd, void *dx, int64_t lddx, float *dgamma,
+                     float *dbeta, uint32_t flags, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace of lags_ckpt_wgrad (at least 16); 0 for invalid sizes. */
+size_t lags_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols, int32_t dtype);
+
+/*
+ * Weight gradient of a linear layer (or 1x1 convolution) from its input's
+ * checkpoint: dw[o][c] = sum over rows of dy[row][o] * X[row][c], X the values
+ * of ckpt ([rows, cols]).  The operands are multiplied exactly and summed in
+ * fp32.
+ *   dy:  device matrix [rows, outs] (lddy);
+ *   dw:  device fp32[outs][cols], out, contiguous: the layer's slice of the
+ *        flat gradient;
+ *   flags: 0 or LAGS_GRAD_ADD.
+ * rows >= 0 (0: dw becomes 0 unless added to); outs, cols in [1, 2^31).
+ * Returns LAGS_OK, LAGS_EINVAL, LAGS_ERANGE, LAGS_EWORKSPACE (ws or ckpt), LAGS_EHIP.
+ */
+int lags_ckpt_wgrad(int64_t rows, int64_t outs, int64_t cols, const void *dy, int64_t lddy,
+                    int32_t dtype, const void *ckpt, size_t ckpt_bytes, float *dw, uint32_t flags,
+                    void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

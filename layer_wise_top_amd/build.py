@@ -11,7 +11,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "liblags.so")
 SOURCES = [os.path.join(CSRC, "lags_host.cpp"), os.path.join(CSRC, "lags_schedule.cpp"),
-           os.path.join(CSRC, "lags_kernels.hip")]
+           os.path.join(CSRC, "lags_kernels.hip"), os.path.join(CSRC, "lags_act.cpp"),
+           os.path.join(CSRC, "lags_ckpt.hip"), os.path.join(CSRC, "lags_gn.hip"),
+           os.path.join(CSRC, "lags_wgrad.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -21,6 +23,7 @@ FLAGS = [
     # no packed fp32 instructions (v_pk_*_f32)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-result",
+    "-parallel-jobs=8",
 ]
 
 

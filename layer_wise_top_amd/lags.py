@@ -29,8 +29,16 @@ EXPORTED = (
     "lags_aggregate_apply", "lags_workspace_report", "lags_trace_enable",
     "lags_trace_read", "lags_num_kernels", "lags_kernel_name", "lags_sparsify_range",
     "lags_aggregate_range", "lags_merge_schedule", "lags_schedule_finish", "lags_adaptive_k",
-    "lags_workspace_init", "lags_sparsify_layers_static",
+    "lags_workspace_init", "lags_sparsify_layers_static", "lags_ckpt_bytes", "lags_ckpt_pack",
+    "lags_ckpt_unpack", "lags_gn_workspace_bytes", "lags_gn_forward", "lags_gn_backward",
+    "lags_ckpt_wgrad_workspace_bytes", "lags_ckpt_wgrad",
 )
+
+LAGS_F32, LAGS_BF16, LAGS_F16 = 0, 1, 2
+LAGS_GRAD_ADD = 1
+LAGS_CKPT_RUN = 32
+LAGS_SLAB_MAX = 4096
+ACTS = {"none": 0, "relu": 1, "silu": 2}
 
 
 class LagsError(RuntimeError):
@@ -43,6 +51,13 @@ class Report(ctypes.Structure):
     _fields_ = [("layers_sampled", ctypes.c_int32), ("layers_exact", ctypes.c_int32),
                 ("bad_entries", ctypes.c_uint32), ("slow_chunks", ctypes.c_uint32),
                 ("layers_wide_bin", ctypes.c_int32), ("fix_timeouts", ctypes.c_uint32)]
+
+
+class GnShape(ctypes.Structure):
+    """lags_gn"""
+    _fields_ = [("samples", ctypes.c_int64), ("spatial", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -113,6 +128,24 @@ def lib():
     L.lags_num_kernels.argtypes = []
     L.lags_kernel_name.restype = ctypes.c_char_p
     L.lags_kernel_name.argtypes = [i32]
+    gn = ctypes.POINTER(GnShape)
+    L.lags_ckpt_bytes.restype = sz
+    L.lags_ckpt_bytes.argtypes = [i64, i64]
+    L.lags_ckpt_pack.restype = ctypes.c_int
+    L.lags_ckpt_pack.argtypes = [i64, i64, vp, i64, i32, vp, sz, vp]
+    L.lags_ckpt_unpack.restype = ctypes.c_int
+    L.lags_ckpt_unpack.argtypes = [i64, i64, vp, sz, vp, i64, i32, vp]
+    L.lags_gn_workspace_bytes.restype = sz
+    L.lags_gn_workspace_bytes.argtypes = [gn]
+    L.lags_gn_forward.restype = ctypes.c_int
+    L.lags_gn_forward.argtypes = [gn, vp, i64, vp, vp, vp, i64, vp, vp, vp, sz, vp, sz, vp]
+    L.lags_gn_backward.restype = ctypes.c_int
+    L.lags_gn_backward.argtypes = [gn, vp, i64, vp, i64, vp, sz, vp, vp, vp, vp, vp, i64, vp, vp,
+                                   u32, vp, sz, vp]
+    L.lags_ckpt_wgrad_workspace_bytes.restype = sz
+    L.lags_ckpt_wgrad_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    L.lags_ckpt_wgrad.restype = ctypes.c_int
+    L.lags_ckpt_wgrad.argtypes = [i64, i64, i64, vp, i64, i32, vp, sz, vp, u32, vp, sz, vp]
     _lib = L
     return L
 
@@ -362,3 +395,179 @@ def lags_trace_read(layout: Layout) -> dict:
 
 def kernel_names():
     return [lib().lags_kernel_name(i).decode() for i in range(int(lib().lags_num_kernels()))]
+
+
+# ---- activation operators ---------------------------------------------------
+
+def _dtype_code(dtype) -> int:
+    import torch
+    codes = {torch.float32: LAGS_F32, torch.bfloat16: LAGS_BF16, torch.float16: LAGS_F16}
+    if dtype not in codes:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    return codes[dtype]
+
+
+def _matrix(t, name: str, dtype=None, rows=None, cols=None):
+    """A device tensor as a matrix: the last dimension is the columns, the others are rows that
+    one pitch separates (a contiguous tensor, or a slice of its last dimension).  Returns
+    (pointer, rows, cols, ld)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have at least two dimensions, channels last")
+    c, r = t.shape[-1], t.numel() // t.shape[-1] if t.shape[-1] else 0
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} must hold {rows} rows of {cols} channels, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        # an empty tensor's address may be null, which the library refuses
+        return t.data_ptr() or (0 if r and c else 16), r, c, c
+    if c > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have its channels last and contiguous")
+    ld, span = None, 0
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = span = stride
+        elif stride != span:
+            raise ValueError(f"{name}: its rows are not one pitch apart")
+        span *= size
+    ld = c if ld is None else ld
+    if ld < c:
+        raise ValueError(f"{name}: its rows overlap")
+    return t.data_ptr(), r, c, ld
+
+
+def _vector(t, numel: int, name: str):
+    """A contiguous fp32 device tensor, or None."""
+    import torch
+    if t is None:
+        return None
+    p = _dev_tensor(t, torch.float32, numel, name)
+    return p if p.value else ctypes.c_void_p(16)
+
+
+def _buffer(t, name: str):
+    import torch
+    return _dev_tensor(t, torch.uint8, 0, name), t.numel()
+
+
+def lags_ckpt_bytes(rows: int, cols: int) -> int:
+    return int(lib().lags_ckpt_bytes(int(rows), int(cols)))
+
+
+def checkpoint(rows: int, cols: int, device=None):
+    """Allocate the 8-bit checkpoint buffer of a [rows, cols] matrix (uint8 device tensor)."""
+    import torch
+    nbytes = lags_ckpt_bytes(rows, cols)
+    if nbytes == 0 and rows != 0:
+        raise ValueError("invalid checkpoint shape")
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def lags_ckpt_pack(x, ckpt, stream=None):
+    """Pack x (channels last) into ckpt."""
+    p, rows, cols, ld = _matrix(x, "x")
+    c, nb = _buffer(ckpt, "ckpt")
+    rc = lib().lags_ckpt_pack(rows, cols, p, ld, _dtype_code(x.dtype), c, nb, _stream_handle(stream))
+    _check("lags_ckpt_pack", rc)
+
+
+def lags_ckpt_unpack(ckpt, x, stream=None):
+    """The values ckpt holds, into x (channels last, of the shape that was packed)."""
+    p, rows, cols, ld = _matrix(x, "x")
+    c, nb = _buffer(ckpt, "ckpt")
+    rc = lib().lags_ckpt_unpack(rows, cols, c, nb, p, ld, _dtype_code(x.dtype), _stream_handle(stream))
+    _check("lags_ckpt_unpack", rc)
+
+
+class GroupNorm:
+    """A group normalisation's shape (lags_gn): `samples` blocks of `spatial` rows of `channels`."""
+
+    def __init__(self, samples: int, spatial: int, channels: int, groups: int, dtype=None,
+                 act: str = "none", eps: float = 1e-5):
+        import torch
+        if act not in ACTS:
+            raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+        self.dtype = dtype if dtype is not None else torch.float32
+        self.shape = GnShape(int(samples), int(spatial), int(channels), int(groups),
+                             _dtype_code(self.dtype), ACTS[act], float(eps))
+
+    @property
+    def rows(self) -> int:
+        return int(self.shape.samples) * int(self.shape.spatial)
+
+    def workspace_bytes(self) -> int:
+        return int(lib().lags_gn_workspace_bytes(ctypes.byref(self.shape)))
+
+
+def gn_workspace(gn: GroupNorm, device=None):
+    """Allocate a workspace for lags_gn_forward and lags_gn_backward of this shape."""
+    import torch
+    nbytes = gn.workspace_bytes()
+    if nbytes == 0:
+        raise ValueError("invalid or unsupported group normalisation shape")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def lags_gn_forward(gn: GroupNorm, x, gamma, beta, y, mean, rstd, ws, ckpt=None, stream=None):
+    """y = act(groupnorm(x)); mean, rstd [samples, groups] (or None); ckpt: a checkpoint buffer that
+    receives x in the same pass."""
+    s = gn.shape
+    px, _, _, ldx = _matrix(x, "x", gn.dtype, gn.rows, s.channels)
+    py, _, _, ldy = _matrix(y, "y", gn.dtype, gn.rows, s.channels)
+    w, nw = _buffer(ws, "ws")
+    c, nc = _buffer(ckpt, "ckpt") if ckpt is not None else (None, 0)
+    rc = lib().lags_gn_forward(
+        ctypes.byref(s), px, ldx, _vector(gamma, s.channels, "gamma"), _vector(beta, s.channels, "beta"),
+        py, ldy, _vector(mean, s.samples * s.groups, "mean"), _vector(rstd, s.samples * s.groups, "rstd"),
+        c, nc, w, nw, _stream_handle(stream))
+    _check("lags_gn_forward", rc)
+
+
+def lags_gn_backward(gn: GroupNorm, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta, ws, x=None,
+                     ckpt=None, add: bool = False, stream=None):
+    """dx, and dgamma and dbeta (each may be None), from dy and the forward's x or its checkpoint."""
+    s = gn.shape
+    pdy, _, _, lddy = _matrix(dy, "dy", gn.dtype, gn.rows, s.channels)
+    pdx, _, _, lddx = _matrix(dx, "dx", gn.dtype, gn.rows, s.channels)
+    px, ldx = None, 0
+    if x is not None:
+        px, _, _, ldx = _matrix(x, "x", gn.dtype, gn.rows, s.channels)
+    w, nw = _buffer(ws, "ws")
+    c, nc = _buffer(ckpt, "ckpt") if ckpt is not None else (None, 0)
+    rc = lib().lags_gn_backward(
+        ctypes.byref(s), pdy, lddy, px, ldx, c, nc, _vector(gamma, s.channels, "gamma"),
+        _vector(beta, s.channels, "beta"), _vector(mean, s.samples * s.groups, "mean"),
+        _vector(rstd, s.samples * s.groups, "rstd"), pdx, lddx, _vector(dgamma, s.channels, "dgamma"),
+        _vector(dbeta, s.channels, "dbeta"), LAGS_GRAD_ADD if add else 0, w, nw, _stream_handle(stream))
+    _check("lags_gn_backward", rc)
+
+
+def wgrad_workspace(rows: int, outs: int, cols: int, dtype, device=None):
+    """Allocate a workspace for lags_ckpt_wgrad of these sizes and dY's dtype."""
+    import torch
+    nbytes = int(lib().lags_ckpt_wgrad_workspace_bytes(int(rows), int(outs), int(cols), _dtype_code(dtype)))
+    if nbytes == 0:
+        raise ValueError("invalid weight gradient sizes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def lags_ckpt_wgrad(dy, ckpt, dw, ws, add: bool = False, stream=None):
+    """dw [outs, cols] (fp32, contiguous: a layer's slice of the flat gradient) = dy^T X, X the
+    [rows, cols] matrix whose checkpoint is ckpt."""
+    import torch
+    pdy, rows, outs, lddy = _matrix(dy, "dy")
+    if not isinstance(dw, torch.Tensor) or dw.dim() != 2 or dw.shape[0] != outs:
+        raise ValueError(f"dw must be a [{outs}, cols] tensor")
+    w, nw = _buffer(ws, "ws")
+    c, nc = _buffer(ckpt, "ckpt")
+    rc = lib().lags_ckpt_wgrad(rows, outs, dw.shape[1], pdy, lddy, _dtype_code(dy.dtype), c, nc,
+                               _dev_tensor(dw, torch.float32, dw.numel(), "dw"),
+                               LAGS_GRAD_ADD if add else 0, w, nw, _stream_handle(stream))
+    _check("lags_ckpt_wgrad", rc)

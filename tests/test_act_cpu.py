@@ -1,0 +1,178 @@
+"""The activation operators' host side: sizes and refusals, all before any HIP call."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import act_reference as R
+from layer_wise_top_amd import lags
+
+OK, EINVAL, ERANGE, EWS = 0, -1, -2, -3
+BASE = 1 << 40                                  # never dereferenced
+
+
+def P(i):
+    return BASE + (i << 32)
+
+
+def test_checkpoint_sizes():
+    for rows, cols in ((1, 1), (3, 16), (3, 17), (7, 32), (7, 33), (0, 5), (1 << 20, 4096)):
+        want = rows * (-(-cols // 16) * 16 + -(-cols // 32))
+        assert lags.lags_ckpt_bytes(rows, cols) == -(-want // 16) * 16
+    assert lags.lags_ckpt_bytes(-1, 4) == 0 and lags.lags_ckpt_bytes(4, 0) == 0
+    assert lags.lags_ckpt_bytes(4, 1 << 31) == 0 and lags.lags_ckpt_bytes(1 << 60, 1 << 20) == 0
+    assert R.codes(np.zeros((3, 17)))[1] == 3 * (32 + 1)
+
+
+def test_pack_refusals():
+    L = lags.lib()
+    need = lags.lags_ckpt_bytes(100, 50)
+    for f, mk in ((L.lags_ckpt_pack, lambda r, c, x, ld, d, k, n: (r, c, x, ld, d, k, n, None)),
+                  (L.lags_ckpt_unpack, lambda r, c, x, ld, d, k, n: (r, c, k, n, x, ld, d, None))):
+        def call(rows=100, cols=50, x=P(0), ld=50, dtype=1, ck=P(1), n=need):
+            return f(*mk(rows, cols, x, ld, dtype, ck, n))
+        assert call(dtype=3) == EINVAL and call(dtype=-1) == EINVAL
+        assert call(rows=-1) == ERANGE and call(cols=0) == ERANGE and call(cols=1 << 31) == ERANGE
+        assert call(x=None) == EINVAL and call(x=P(0) + 1) == EINVAL and call(ld=49) == EINVAL
+        assert call(dtype=0, x=P(0) + 2) == EINVAL            # fp32 needs 4-byte alignment
+        assert call(ld=1 << 61) == ERANGE
+        assert call(ck=None) == EWS and call(ck=P(1) + 8) == EWS and call(n=need - 1) == EWS
+        assert call(ck=P(0) + 16) == EINVAL                   # overlap
+        assert call(rows=0, n=0) == OK                        # nothing to do, nothing launched
+
+
+def _gn(n=4, s=10, c=64, g=8, dtype=1, act=2, eps=1e-5):
+    return lags.GnShape(n, s, c, g, dtype, act, eps)
+
+
+BAD_SHAPES = [(dict(g=7), EINVAL), (dict(g=0), EINVAL), (dict(c=0), EINVAL), (dict(n=-1), EINVAL),
+              (dict(s=-1), EINVAL), (dict(dtype=9), EINVAL), (dict(act=3), EINVAL), (dict(act=-1), EINVAL),
+              (dict(eps=-1.0), EINVAL), (dict(eps=float("nan")), EINVAL), (dict(eps=float("inf")), EINVAL),
+              (dict(n=1 << 31), ERANGE), (dict(s=1 << 31), ERANGE), (dict(c=1 << 31, g=1), ERANGE),
+              (dict(c=5000, g=1), ERANGE),                    # one group of more than 4096 channels
+              (dict(c=301 * 20, g=20), ERANGE),               # 301 channels a group, runs of 32: 9632 > 4096
+              (dict(n=(1 << 31) - 1, s=(1 << 31) - 1, c=4096, g=4096), ERANGE)]
+
+
+def test_group_norm_workspace():
+    L = lags.lib()
+    assert L.lags_gn_workspace_bytes(ctypes.byref(_gn())) >= 16
+    assert L.lags_gn_workspace_bytes(None) == 0
+    for kw, _ in BAD_SHAPES:
+        assert L.lags_gn_workspace_bytes(ctypes.byref(_gn(**kw))) == 0, kw
+    # wide shapes that are supported: many groups, and one group of the most channels
+    for kw in (dict(c=8192, g=32), dict(c=4096, g=1), dict(c=1 << 20, g=1 << 20), dict(n=0), dict(s=0)):
+        assert L.lags_gn_workspace_bytes(ctypes.byref(_gn(**kw))) >= 16, kw
+    # the workspace stays far below the data it serves
+    big = L.lags_gn_workspace_bytes(ctypes.byref(_gn(n=64, s=12544, c=64, g=32)))
+    assert big < 64 * 12544 * 64 * 2 // 8
+
+
+def test_group_norm_forward_refusals():
+    L = lags.lib()
+    gn = _gn()
+    need = L.lags_gn_workspace_bytes(ctypes.byref(gn))
+    cb = lags.lags_ckpt_bytes(40, 64)
+
+    def call(g=gn, x=P(0), ldx=64, gamma=P(1), beta=P(2), y=P(3), ldy=64, mean=P(4), rstd=P(5), ck=None, ckn=0,
+             ws=P(6), wsn=need):
+        return L.lags_gn_forward(ctypes.byref(g) if g is not None else None, x, ldx, gamma, beta, y, ldy, mean, rstd,
+                                 ck, ckn, ws, wsn, None)
+    assert call(g=None) == EINVAL
+    for kw, rc in BAD_SHAPES:
+        assert call(g=_gn(**kw), ldx=1 << 32, ldy=1 << 32) == rc, kw
+    assert call(x=None) == EINVAL and call(y=None) == EINVAL and call(ldx=63) == EINVAL and call(ldy=0) == EINVAL
+    assert call(x=P(0) + 1) == EINVAL
+    assert call(gamma=None) == EINVAL and call(beta=None) == EINVAL        # both or neither
+    assert call(gamma=P(1) + 2) == EINVAL and call(mean=P(4) + 1) == EINVAL
+    assert call(ws=None) == EWS and call(ws=P(6) + 4) == EWS and call(wsn=need - 1) == EWS
+    assert call(ck=P(7), ckn=cb - 1) == EWS and call(ck=P(7) + 8, ckn=cb) == EWS
+    assert call(y=P(0) + 64) == EINVAL                        # overlaps x, not the same matrix
+    assert call(y=P(0), ldy=65) == EINVAL                     # in place needs the same pitch
+    assert call(mean=P(5)) == EINVAL and call(mean=P(0)) == EINVAL and call(rstd=P(3)) == EINVAL
+    assert call(ck=P(0), ckn=cb) == EINVAL and call(ws=P(3)) == EINVAL and call(y=P(1), ldy=64) == EINVAL
+    # columns of one wide buffer meet only where their channels do
+    assert call(x=P(0), ldx=128, y=P(0) + 126, ldy=128) == EINVAL
+    empty = _gn(n=0)
+    assert call(g=empty) == OK and call(g=_gn(s=0)) == OK
+
+
+def test_group_norm_backward_refusals():
+    L = lags.lib()
+    gn = _gn()
+    need = L.lags_gn_workspace_bytes(ctypes.byref(gn))
+    cb = lags.lags_ckpt_bytes(40, 64)
+
+    def call(g=gn, dy=P(0), lddy=64, x=P(1), ldx=64, ck=None, ckn=0, gamma=P(2), beta=P(3), mean=P(4), rstd=P(5),
+             dx=P(6), lddx=64, dg=P(7), db=P(8), flags=0, ws=P(9), wsn=need):
+        return L.lags_gn_backward(ctypes.byref(g) if g is not None else None, dy, lddy, x, ldx, ck, ckn, gamma, beta,
+                                  mean, rstd, dx, lddx, dg, db, flags, ws, wsn, None)
+    assert call(g=None) == EINVAL
+    for kw, rc in BAD_SHAPES:
+        assert call(g=_gn(**kw), lddy=1 << 32, ldx=1 << 32, lddx=1 << 32) == rc, kw
+    assert call(flags=2) == EINVAL
+    assert call(x=None) == EINVAL and call(ck=P(10), ckn=cb) == EINVAL     # one source, not none or two
+    assert call(x=None, ck=P(10), ckn=cb - 1) == EWS and call(x=None, ck=P(10) + 4, ckn=cb) == EWS
+    assert call(dy=None) == EINVAL and call(dx=None) == EINVAL and call(lddy=1) == EINVAL and call(lddx=1) == EINVAL
+    assert call(ldx=63) == EINVAL and call(mean=None) == EINVAL and call(rstd=None) == EINVAL
+    assert call(gamma=None) == EINVAL and call(dg=P(7) + 2) == EINVAL
+    assert call(ws=None) == EWS and call(wsn=need - 1) == EWS and call(ws=P(9) + 8) == EWS
+    assert call(dx=P(1)) == EINVAL and call(dx=P(0) + 2) == EINVAL and call(dg=P(8)) == EINVAL
+    assert call(dg=P(6)) == EINVAL and call(db=P(2)) == EINVAL and call(ws=P(1)) == EINVAL
+    assert call(x=None, ck=P(6), ckn=cb) == EINVAL
+    # nothing to compute and no gradient asked for: nothing launched
+    assert call(g=_gn(n=0), dg=None, db=None) == OK
+
+
+def test_wgrad_refusals():
+    L = lags.lib()
+    bytes_ = L.lags_ckpt_wgrad_workspace_bytes
+    assert bytes_(-1, 4, 4, 0) == 0 and bytes_(4, 0, 4, 0) == 0 and bytes_(4, 4, 0, 0) == 0 and bytes_(4, 4, 4, 5) == 0
+    need, cb = bytes_(5000, 100, 60, 1), lags.lags_ckpt_bytes(5000, 60)
+    assert need >= 16 and bytes_(0, 100, 60, 1) >= 16
+
+    def call(rows=5000, outs=100, cols=60, dy=P(0), ld=100, dtype=1, ck=P(1), ckn=cb, dw=P(2), flags=0, ws=P(3),
+             wsn=need):
+        return L.lags_ckpt_wgrad(rows, outs, cols, dy, ld, dtype, ck, ckn, dw, flags, ws, wsn, None)
+    assert call(dtype=4) == EINVAL and call(flags=4) == EINVAL
+    assert call(rows=-1) == ERANGE and call(outs=0) == ERANGE and call(cols=0) == ERANGE and call(outs=1 << 31) == ERANGE
+    assert call(dy=None) == EINVAL and call(ld=99) == EINVAL and call(dy=P(0) + 1) == EINVAL
+    assert call(dw=None) == EINVAL and call(dw=P(2) + 2) == EINVAL
+    assert call(ck=None) == EWS and call(ckn=cb - 1) == EWS and call(ck=P(1) + 8) == EWS
+    assert call(ws=None) == EWS and call(wsn=need - 1) == EWS and call(ws=P(3) + 8) == EWS
+    assert call(dw=P(0)) == EINVAL and call(dw=P(1)) == EINVAL and call(ws=P(0)) == EINVAL and call(ws=P(2)) == EINVAL
+
+
+def test_binding_refuses_what_is_no_device_matrix():
+    import torch
+    for bad in (torch.zeros(3, 4), np.zeros((3, 4))):
+        with pytest.raises(TypeError):
+            lags.lags_ckpt_pack(bad, None)
+    with pytest.raises(ValueError):
+        lags.GroupNorm(1, 1, 8, 2, act="tanh")
+    with pytest.raises(TypeError):
+        lags.GroupNorm(1, 1, 8, 2, dtype=torch.float64)
+    with pytest.raises(ValueError):
+        lags.gn_workspace(lags.GroupNorm(1, 1, 8, 3))
+    with pytest.raises(ValueError):
+        lags.wgrad_workspace(1, 0, 4, torch.float32)
+    with pytest.raises(ValueError):
+        lags.checkpoint(-1, 4)
+
+
+def test_reference_formats_agree():
+    """The test oracle's two descriptions of the format, and the definition's bound: off by at most
+    1/128 of the run's largest magnitude, exact in bf16."""
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((20, 70)) * np.exp(3 * rng.standard_normal((20, 1)))
+    buf, n = R.codes(x)
+    pitch, nrun = 80, 3
+    q = buf[:20 * pitch].view(np.int8).reshape(20, pitch)[:, :70].astype(np.float64)
+    s = buf[20 * pitch:n].reshape(20, nrun).astype(int)
+    val = q * np.ldexp(1.0, np.repeat(s - 127, 32, axis=1)[:, :70])
+    assert np.array_equal(val, R.held(x))
+    for b in range(nrun):
+        v = slice(32 * b, 32 * b + 32)
+        assert (np.abs(val[:, v] - x[:, v]).max(axis=1) <= np.abs(x[:, v]).max(axis=1) / 128).all()
+    f = val.astype(np.float32).view(np.uint32)
+    assert not (f & 0xFFFF).any()

@@ -1,0 +1,296 @@
+"""Group normalisation with an activation on the GPU, both directions, from
+the input and from its checkpoint, against float64."""
+import numpy as np
+import pytest
+
+import act_reference as R
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": "float32", "bf16": "bfloat16", "f16": "float16"}
+EPS = 1e-5
+
+
+class Case:
+    """Inputs of one shape on the device and in float64."""
+
+    def __init__(self, n, s, c, groups, dtype, act, seed=0, offset=0.0, affine=True, x=None):
+        import torch
+        from layer_wise_top_amd import lags
+        rng = np.random.default_rng(seed)
+        self.n, self.s, self.c, self.groups, self.dtype, self.act = n, s, c, groups, dtype, act
+        dt = getattr(torch, DT[dtype])
+        if x is None:
+            x = rng.standard_normal((n, s, c)) * np.exp(0.5 * rng.standard_normal(c)) + rng.standard_normal(c) + offset
+        self.x = torch.from_numpy(x).to(dt).cuda()
+        self.dy = torch.from_numpy(rng.standard_normal((n, s, c))).to(dt).cuda()
+        self.gamma = torch.from_numpy(1 + 0.3 * rng.standard_normal(c)).float().cuda() if affine else None
+        self.beta = torch.from_numpy(0.5 * rng.standard_normal(c)).float().cuda() if affine else None
+        self.g64 = self.gamma.double().cpu().numpy() if affine else np.ones(c)
+        self.b64 = self.beta.double().cpu().numpy() if affine else np.zeros(c)
+        self.gn = lags.GroupNorm(n, s, c, groups, dtype=dt, act=act, eps=EPS)
+        self.ws = lags.gn_workspace(self.gn)
+        self.ws.fill_(0xFF)
+        self.tag = f"n{n} s{s} c{c} g{groups} {dtype} {act}"
+
+    def x64(self):
+        return self.x.double().cpu().numpy()
+
+    def forward(self, ckpt=None, y=None):
+        import torch
+        from layer_wise_top_amd import lags
+        y = torch.full_like(self.x, 9.0, memory_format=torch.contiguous_format) if y is None else y
+        mean = torch.full((self.n, self.groups), 9.0, device="cuda")
+        rstd = torch.full_like(mean, 9.0)
+        print("forward", self.tag, "ckpt" if ckpt is not None else "", flush=True)
+        lags.lags_gn_forward(self.gn, self.x, self.gamma, self.beta, y, mean, rstd, self.ws, ckpt=ckpt)
+        torch.cuda.synchronize()
+        return y, mean, rstd
+
+    def check_forward(self, ckpt=None):
+        y, mean, rstd = self.forward(ckpt)
+        want, err = R.forward(self.x64(), self.g64, self.b64, self.groups, EPS, self.act)
+        for name, got, w, e in zip(("y", "mean", "rstd"), (y, mean, rstd), want, err):
+            R.check(f"{name} {self.tag}", got.double().cpu().numpy(), w, e, self.dtype if name == "y" else "f32")
+        return mean, rstd
+
+    def backward(self, mean, rstd, x=None, ckpt=None, dx=None, add=None):
+        import torch
+        from layer_wise_top_amd import lags
+        dx = torch.full_like(self.dy, 9.0, memory_format=torch.contiguous_format) if dx is None else dx
+        dg = torch.full((self.c,), 9.0, device="cuda") if add is None else add[0].clone()
+        db = torch.full((self.c,), 9.0, device="cuda") if add is None else add[1].clone()
+        print("backward", self.tag, "ckpt" if ckpt is not None else "", flush=True)
+        lags.lags_gn_backward(self.gn, self.dy, self.gamma, self.beta, mean, rstd, dx, dg, db, self.ws,
+                              x=x, ckpt=ckpt, add=add is not None)
+        torch.cuda.synchronize()
+        return dx, dg, db
+
+    def check_backward(self, mean, rstd, ckpt=None, x64=None):
+        got = self.backward(mean, rstd, x=None if ckpt is not None else self.x, ckpt=ckpt)
+        x64 = self.x64() if x64 is None else x64
+        want, err = R.backward(self.dy.double().cpu().numpy(), x64, self.g64, self.b64,
+                               mean.double().cpu().numpy(), rstd.double().cpu().numpy(), self.act)
+        for name, g, w, e in zip(("dx", "dgamma", "dbeta"), got, want, err):
+            R.check(f"{name} {self.tag}", g.double().cpu().numpy(), w, e, self.dtype if name == "dx" else "f32")
+
+    def check_all(self):
+        """Forward without and with a checkpoint, the checkpoint's bytes, both backwards."""
+        import torch
+        from layer_wise_top_amd import lags
+        self.check_forward()
+        rows = self.n * self.s
+        ck, ref = lags.checkpoint(rows, self.c), lags.checkpoint(rows, self.c)
+        ck.fill_(0x77)
+        mean, rstd = self.check_forward(ck)
+        lags.lags_ckpt_pack(self.x, ref)
+        used = R.codes(np.zeros((1, self.c)))[1] * rows
+        assert torch.equal(ck[:used], ref[:used]), "checkpoint of " + self.tag
+        self.check_backward(mean, rstd)
+        self.check_backward(mean, rstd, ck, R.held(self.x64().reshape(rows, self.c)).reshape(self.x.shape))
+
+
+SHAPES = [
+    # n, s, c, groups: one launch, tiny to wide
+    (1, 1, 1, 1), (1, 1, 32, 1), (2, 1, 6, 3), (3, 5, 12, 3), (2, 49, 64, 8), (4, 64, 64, 8), (1, 7, 33, 11),
+    (2, 9, 96, 2), (2, 16, 100, 5), (3, 33, 40, 40), (1, 100, 2048, 32), (2, 3, 4096, 1), (2, 4, 301 * 13, 13),
+    (130, 1, 64, 32), (300, 2, 24, 4),
+    # a workgroup's rows by the dozen; chunked forms; ragged ends
+    (64, 600, 64, 8), (1, 3000, 32, 4), (2, 1500, 48, 6), (1, 1025, 160, 5), (1, 513, 512, 2), (2, 257, 2048, 1),
+    (1, 20000, 8, 2), (9, 1551, 36, 3),
+]
+
+
+@pytest.mark.parametrize("dtype,act", [("f32", "silu"), ("bf16", "relu"), ("f16", "silu"), ("f32", "none"),
+                                       ("bf16", "silu"), ("f32", "relu")])
+@pytest.mark.parametrize("n,s,c,groups", SHAPES)
+def test_shapes(n, s, c, groups, dtype, act):
+    Case(n, s, c, groups, dtype, act, seed=n + s + c).check_all()
+
+
+@pytest.mark.parametrize("n,s", [(2, 100), (1, 6000)])
+def test_no_affine(n, s):
+    Case(n, s, 64, 8, "f32", "silu", affine=False).check_all()
+
+
+@pytest.mark.parametrize("n,s", [(2, 60), (1, 5000)])
+@pytest.mark.parametrize("dtype,offset", [("f32", 1e4), ("bf16", 100.0)])
+def test_large_common_offset(n, s, dtype, offset):
+    """A mean far larger than the spread: the variance keeps its digits."""
+    Case(n, s, 64, 8, dtype, "none", offset=offset).check_forward()
+
+
+@pytest.mark.parametrize("n,s", [(2, 10), (1, 9000)])
+def test_constant_groups(n, s):
+    """Variance zero: rstd = 1 / sqrt(eps), y = act(beta), dx finite."""
+    x = np.broadcast_to(np.repeat([0.0, 1.0, -3.5, 1e-3], 8), (n, s, 32)).copy()
+    k = Case(n, s, 32, 4, "f32", "silu", x=x)
+    y, mean, rstd = k.forward()
+    assert torch_all_close(mean, np.repeat([[0.0, 1.0, -3.5, 1e-3]], n, 0), 1e-6)
+    # a constant that is not exact in the mean's rounding leaves a distance of an ulp, squared
+    assert torch_all_close(rstd, np.full((n, 4), EPS ** -0.5), 1e-3)
+    want = R.act(k.b64, "silu")
+    assert np.abs(y.double().cpu().numpy() - want).max() < 1e-4
+    dx, dg, db = k.backward(mean, rstd, x=k.x)
+    assert np.isfinite(dx.cpu().numpy()).all() and np.isfinite(dg.cpu().numpy()).all()
+
+
+def torch_all_close(t, want, rel):
+    t = t.double().cpu().numpy()
+    return bool((np.abs(t - want) <= rel * np.abs(want) + 1e-7).all())
+
+
+@pytest.mark.parametrize("n,s", [(3, 20), (2, 6000)])
+@pytest.mark.parametrize("act", ["none", "relu", "silu"])
+def test_non_finite_stays_in_its_group(n, s, act):
+    k = Case(n, s, 64, 8, "f32", act, seed=3)
+    clean = k.forward()
+    k.x[0, 1, 9], k.x[1, 2, 30] = float("nan"), float("inf")
+    y, mean, rstd = k.forward()
+    bad = np.zeros((n, 8), bool)
+    bad[0, 1] = bad[1, 3] = True
+    assert np.array_equal(np.isnan(rstd.cpu().numpy()), bad)
+    ny = np.isnan(y.cpu().numpy()).reshape(n, s, 8, 8)
+    assert ny[0, :, 1].all() and ny[1, :, 3].all()
+    ok = ~np.broadcast_to(bad[:, None, :, None], ny.shape)
+    assert np.array_equal(y.cpu().numpy().reshape(ny.shape)[ok], clean[0].cpu().numpy().reshape(ny.shape)[ok])
+    dx, dg, db = k.backward(mean, rstd, x=k.x)
+    nd = np.isnan(dx.cpu().numpy()).reshape(n, s, 8, 8)
+    # relu sees no z above zero in such a group, so it passes no gradient and only the NaN statistics show
+    assert nd[0, :, 1].all() and nd[1, :, 3].all() and not nd[ok].any()
+    assert not np.isnan(dg.cpu().numpy().reshape(8, 8)[[0, 2, 4, 5, 6, 7]]).any()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n,s", [(2, 30), (1, 4000)])
+def test_slices_in_place_and_neighbours(n, s, dtype):
+    """x, y, dy, dx as slices of wider tensors at odd offsets; what lies around y and dx is left
+    alone; y over x and dx over dy give the same bits as separate buffers."""
+    import torch
+    k = Case(n, s, 40, 5, dtype, "silu", seed=8)
+    y0, mean, rstd = k.forward()
+    d0 = k.backward(mean, rstd, x=k.x)
+    wide = torch.full((n, s, 99), 3.0, dtype=k.x.dtype, device="cuda")
+    wide[..., 7:47] = k.x
+    x_plain, dy_plain = k.x, k.dy
+    k.x = wide[..., 7:47]
+    y, m2, r2 = k.forward(y=wide[..., 53:93])
+    assert torch.equal(y, y0) and torch.equal(m2, mean) and torch.equal(r2, rstd)
+    assert (wide[..., :7] == 3).all() and (wide[..., 47:53] == 3).all() and (wide[..., 93:] == 3).all()
+    assert torch.equal(wide[..., 7:47], x_plain)
+    y, m2, r2 = k.forward(y=k.x)                               # in place
+    assert torch.equal(y, y0) and torch.equal(m2, mean)
+    k.x = x_plain
+    wd = torch.full((n, s, 81), 3.0, dtype=k.x.dtype, device="cuda")
+    wd[..., 1:41] = dy_plain
+    k.dy = wd[..., 1:41]
+    got = k.backward(mean, rstd, x=k.x, dx=k.dy)               # in place, in a slice
+    for a, b in zip(got, d0):
+        assert torch.equal(a, b)
+    assert (wd[..., :1] == 3).all() and (wd[..., 41:] == 3).all()
+
+
+@pytest.mark.parametrize("n,s", [(2, 30), (1, 4000)])
+def test_add_and_partial_outputs(n, s):
+    """LAGS_GRAD_ADD adds one rounding; null dgamma, dbeta, mean and rstd are left out."""
+    import torch
+    from layer_wise_top_amd import lags
+    k = Case(n, s, 48, 6, "f32", "relu", seed=4)
+    _, mean, rstd = k.forward()
+    dx, dg, db = k.backward(mean, rstd, x=k.x)
+    flat = torch.randn(97, generator=torch.Generator().manual_seed(1)).cuda()   # a flat gradient, odd offsets
+    a0, a1 = flat[1:49], flat[49:97]
+    got = k.backward(mean, rstd, x=k.x, add=(a0, a1))
+    assert torch.equal(got[1], a0 + dg) and torch.equal(got[2], a1 + db)
+    only = torch.zeros_like(dg)
+    lags.lags_gn_backward(k.gn, k.dy, k.gamma, k.beta, mean, rstd, dx.zero_(), only, None, k.ws, x=k.x)
+    assert torch.equal(only, dg)
+    lags.lags_gn_backward(k.gn, k.dy, k.gamma, k.beta, mean, rstd, dx.zero_(), None, None, k.ws, x=k.x)
+    y = torch.zeros_like(k.x)
+    lags.lags_gn_forward(k.gn, k.x, k.gamma, k.beta, y, None, None, k.ws)
+    assert torch.equal(y, k.forward()[0])
+
+
+def test_empty():
+    """No samples, or no positions: gradients of the parameters become zero, or stay when added to."""
+    import torch
+    for n, s in ((0, 5), (3, 0)):
+        k = Case(n, s, 16, 2, "f32", "relu")
+        y, mean, rstd = k.forward()
+        assert (mean == 9).all() and (rstd == 9).all()
+        dx, dg, db = k.backward(mean, rstd, x=k.x)
+        assert not dg.any() and not db.any()
+        one = torch.ones(16, device="cuda")
+        dx, dg, db = k.backward(mean, rstd, x=k.x, add=(one, one))
+        assert torch.equal(dg, one) and torch.equal(db, one)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu"])
+@pytest.mark.parametrize("s", [6, 5000])
+def test_gradient_by_differences(act, s):
+    """dx and dgamma, dbeta against central differences of sum(dy * y) through the forward itself.
+    Step h = 2^-6: the difference is off by h^2/6 times a third derivative (about 10 at most for
+    these sizes, dy ~ 1, rstd ~ 1), and by fp32's rounding of y over h; 1e-2 covers both.  relu's
+    kink: inputs whose z comes within 0.1 of zero get a dy of zero."""
+    import torch
+    k = Case(1, s, 8, 2, "f32", act, seed=21)
+    y, mean, rstd = k.forward()
+    z = R.z_fp32(k.x64().astype(np.float32), k.g64, k.b64, mean.double().cpu().numpy(), rstd.double().cpu().numpy())
+    if act == "relu":
+        k.dy *= torch.from_numpy((np.abs(z) > 0.1).astype(np.float32)).cuda()
+    dx, dg, db = k.backward(mean, rstd, x=k.x)
+    h = 2.0 ** -6
+
+    def loss():
+        return float((k.dy.double() * k.forward()[0].double()).sum())
+
+    for t, g, at in ((k.x, dx, [(0, 0, 0), (0, 3, 2), (0, s - 1, 7), (0, 2, 5)]), (k.gamma, dg, [(0,), (5,)]),
+                     (k.beta, db, [(1,), (6,)])):
+        for i in at:
+            old = float(t[i])
+            t[i] = old + h
+            up = loss()
+            t[i] = old - h
+            down = loss()
+            t[i] = old
+            want = (up - down) / (2 * h)
+            got = float(g[i])
+            scale = max(1.0, abs(want)) if t is k.x else max(1.0, float(k.dy.abs().sum()) * 1e-4, abs(want))
+            assert abs(got - want) <= 1e-2 * scale, (act, i, got, want)
+
+
+@pytest.mark.parametrize("n,s", [(64, 100), (2, 7000)])
+def test_repeats_bit_for_bit_on_streams_and_in_graphs(n, s):
+    import torch
+    from layer_wise_top_amd import lags
+    k = Case(n, s, 64, 32, "bf16", "silu", seed=2)
+    ck = lags.checkpoint(n * s, 64)
+    y0, m0, r0 = k.forward(ck)
+    d0 = k.backward(m0, r0, ckpt=ck)
+    y, m, r = torch.empty_like(y0), torch.empty_like(m0), torch.empty_like(r0)
+    dx, dg, db = (torch.empty_like(t) for t in d0)
+
+    def step(stream=None):
+        lags.lags_gn_forward(k.gn, k.x, k.gamma, k.beta, y, m, r, k.ws, ckpt=ck, stream=stream)
+        lags.lags_gn_backward(k.gn, k.dy, k.gamma, k.beta, m, r, dx, dg, db, k.ws, ckpt=ck, stream=stream)
+
+    def same(tag):
+        torch.cuda.synchronize()
+        for a, b in zip((y, m, r, dx, dg, db), (y0, m0, r0) + tuple(d0)):
+            assert torch.equal(a, b), tag
+            a.zero_()
+        torch.cuda.synchronize()
+
+    for i in range(3):
+        step()
+        same(f"again {i}")
+    s1 = torch.cuda.Stream()
+    step(s1)
+    same("other stream")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(4):
+        g.replay()
+        same(f"replay {i}")
+        step()
+        same(f"eager {i}")
