@@ -393,6 +393,7 @@ const char *lags_kernel_name(int32_t id);
 #define LAGS_GRAD_ADD 1u /* add to the gradient buffer instead of overwriting it */
 #define LAGS_CKPT_RUN 32 /* columns of a row that share a scale */
 #define LAGS_SLAB_MAX 4096 /* see lags_gn */
+#define LAGS_WGRAD_MAX (1 << 22) /* outs, cols and lddy of lags_ckpt_wgrad */
 
 /*
  * 8-bit checkpoint of a [rows, cols] matrix.  Each run of 32 columns of a row
@@ -495,7 +496,8 @@ size_t lags_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols,
  *   dw:  device fp32[outs][cols], out, contiguous: the layer's slice of the
  *        flat gradient;
  *   flags: 0 or LAGS_GRAD_ADD.
- * rows >= 0 (0: dw becomes 0 unless added to); outs, cols in [1, 2^31).
+ * rows >= 0 (0: dw becomes 0 unless added to); outs and cols in [1, LAGS_WGRAD_MAX],
+ * lddy <= LAGS_WGRAD_MAX.
  * Returns LAGS_OK, LAGS_EINVAL, LAGS_ERANGE, LAGS_EWORKSPACE (ws or ckpt), LAGS_EHIP.
  */
 int lags_ckpt_wgrad(int64_t rows, int64_t outs, int64_t cols, const void *dy, int64_t lddy,

@@ -59,6 +59,11 @@ bool ckpt_dims(int64_t rows, int64_t cols)
     return rows >= 0 && cols >= 1 && cols <= kMaxDim && (u128)rows * (u128)(cols + 64) * 2 <= kMaxBytes;
 }
 
+bool wgrad_dims(int64_t rows, int64_t outs, int64_t cols)
+{
+    return ckpt_dims(rows, cols) && cols <= LAGS_WGRAD_MAX && outs >= 1 && outs <= LAGS_WGRAD_MAX;
+}
+
 int hip(hipError_t e) { return e == hipSuccess ? LAGS_OK : LAGS_EHIP; }
 
 int check_pack(int64_t rows, int64_t cols, const void *x, int64_t ldx, int32_t dtype, const void *ckpt,
@@ -246,7 +251,7 @@ int lags_gn_backward(const lags_gn *gn, const void *dy, int64_t lddy, const void
 
 size_t lags_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols, int32_t dtype)
 {
-    if (!known_dtype(dtype) || !ckpt_dims(rows, cols) || outs < 1 || outs > kMaxDim) return 0;
+    if (!known_dtype(dtype) || !wgrad_dims(rows, outs, cols)) return 0;
     const WgradPlan p = wgrad_plan(dtype, rows, outs, cols);
     const u128 n = p.split > 1 ? (u128)p.split * (u128)outs * (u128)cols * 4 : 16;
     return n > kMaxBytes ? 0 : (size_t)((n + 15) / 16 * 16);
@@ -257,9 +262,10 @@ int lags_ckpt_wgrad(int64_t rows, int64_t outs, int64_t cols, const void *dy, in
                     void *stream)
 {
     if (!known_dtype(dtype) || (flags & ~LAGS_GRAD_ADD)) return LAGS_EINVAL;
-    if (!ckpt_dims(rows, cols) || outs < 1 || outs > kMaxDim) return LAGS_ERANGE;
+    if (!wgrad_dims(rows, outs, cols)) return LAGS_ERANGE;
     Region r[4];
     if (int rc = matrix(dy, rows, outs, lddy, dtype, r[0]); rc != LAGS_OK) return rc;
+    if (lddy > LAGS_WGRAD_MAX) return LAGS_ERANGE;
     if (!dw || !aligned(dw, 4)) return LAGS_EINVAL;
     const size_t need_ck = ckpt_size(ckpt_shape(rows, cols));
     if (!ckpt || !aligned(ckpt, 16) || ckpt_bytes < need_ck) return LAGS_EWORKSPACE;

@@ -12,6 +12,7 @@
 // the LDS transpose reads that feed the matrix instructions.
 #include "lags_act.h"
 
+#include <cmath>
 #include <type_traits>
 
 namespace lags {
@@ -19,19 +20,17 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-constexpr int kThreads = 256;
-constexpr int kStep = 32;            // rows staged at a time
 
 template <int D> constexpr int kTerms = D == kBF16 ? 1 : D == kF16 ? 2 : 3;
 
-// Byte offset in a staged [kStep][B] bf16 tile.  A transpose read of 16 lanes
+// Byte offset in a staged [32][B] bf16 tile.  A transpose read of 16 lanes
 // takes 32 bytes from each of four consecutive rows: the 64-byte blocks of a
 // row are exchanged by its number so that those rows fall into different banks.
 template <int B> __device__ inline int tile_at(int k, int c)
 {
-    const int x = B >= 128 ? k & 3 : (k >> 1) & 1;
+    const int x = B % 128 == 0 ? k & 3 : (k >> 1) & 1;
     return k * B * 2 + (((c >> 5) ^ x) << 6) + (c & 31) * 2;
 }
 
@@ -80,15 +79,26 @@ __device__ inline uint32_t deal(uint32_t b, uint32_t n)
     return b < main ? (b & 7) * per + (b >> 3) : b;
 }
 
-// A workgroup: a BO x BC tile of dW over one slice of the rows; WR x WC waves.
-template <int D, int BO, int BC, int WR, int WC>
-__global__ __launch_bounds__(kThreads) void k_wgrad(WgradArgs a)
+// A buffer descriptor for `left` bytes at p: reads past them give zeros.
+__device__ inline __amdgpu_buffer_rsrc_t window(const void *p, int64_t left)
 {
+    const int n = left > 0x7ffffffc ? 0x7ffffffc : left < 0 ? 0 : (int)left;
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, n, 0x00020000);
+}
+
+// A workgroup: a BO x BC tile of dW over one slice of the rows; WR x WC waves,
+// K rows staged at a time.  ODD: rows of 16-bit values that may start inside a
+// word (odd pitch, odd slice): five words are read for each vector's four and
+// shifted into place.
+template <int D, int BO, int BC, int WR, int WC, int K, bool ODD>
+__global__ __launch_bounds__(64 * WR * WC) void k_wgrad(WgradArgs a)
+{
+    constexpr int kThreads = 64 * WR * WC;
     constexpr int V = Elem<D>::V, E = Elem<D>::E, T = kTerms<D>;
-    constexpr int VO = BO / V, RA = kThreads / VO, PA = kStep / RA;      // dY: vectors a row, rows a pass, passes
-    constexpr int VC = BC / 16, RX = kThreads / VC, PX = RX >= kStep ? 1 : kStep / RX;
+    constexpr int VO = BO / V, NA = VO * K, PA = (NA + kThreads - 1) / kThreads;   // dY: vectors a row, in all, passes
+    constexpr int VC = BC / 16, RX = kThreads / VC, PX = RX >= K ? 1 : K / RX;
     constexpr int NI = BO / WR / 32, NJ = BC / WC / 32;
-    constexpr int TA = kStep * BO * 2, TX = kStep * BC * 2, BUF = T * TA + TX;
+    constexpr int TA = K * BO * 2, TX = K * BC * 2, BUF = T * TA + TX;
     extern __shared__ __attribute__((aligned(128))) char lds[];
 
     uint32_t b = deal(blockIdx.x, gridDim.x);
@@ -96,46 +106,74 @@ __global__ __launch_bounds__(kThreads) void k_wgrad(WgradArgs a)
     const uint32_t o0 = tile / a.tc * BO, c0 = tile % a.tc * BC;
     const int64_t lo = slice * a.rows_per, hi = min(a.M, lo + a.rows_per);
     const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
-    const int ar = t / VO, ac = t % VO * V, xr = t / VC, xc = t % VC * 16;
-    const int an = (int)a.O - (int)(o0 + ac);
-    const bool xin = c0 + xc < a.pitch && xr < kStep;
-    const char *pa = (const char *)a.dy + ((lo + ar) * a.lddy + o0 + ac) * E;
-    const uint8_t *px = a.codes + (lo + xr) * a.pitch + c0 + xc;
-    const uint8_t *ps = a.scales + (lo + xr) * a.nrun + (c0 + xc) / kRun;
+    const int xr = t / VC, xc = t % VC * 16;
 
+    // What is staged next; the windows move with it and end with the slice's last value, so rows
+    // past it read as zeros.  dY's window starts and ends on whole words: what else those hold is
+    // shifted out, lies in columns past O, which are not stored, or (ODD) in the row after the
+    // slice, which stage() clears.
+    const char *pa = (const char *)a.dy + (lo * a.lddy + o0) * E;
+    const uint8_t *px = a.codes + lo * a.pitch + c0, *ps = a.scales + lo * a.nrun + c0 / kRun;
+    int64_t la = hi > lo ? ((hi - lo - 1) * a.lddy + (a.O - o0)) * E : 0;
+    int64_t lx = (hi - lo) * a.pitch - c0, ls = (hi - lo) * a.nrun - c0 / kRun;
+    const int into = (int)((uintptr_t)pa & 3);
+    pa -= into;
+    la = (la + into + 3) & ~(int64_t)3;
+    // dY's vectors go to the threads in turn (the last pass may not need all); a thread's place in a
+    // word is the same every step, K being even
+    int vx_at[PX], vs_at[PX];
+    uint32_t va_at[PA];
+    static_assert(K % 2 == 0, "");
+    for (int p = 0; p < PA; ++p) {
+        const int id = t + p * kThreads;
+        va_at[p] = into + (uint32_t)((id / VO * a.lddy + id % VO * V) * E);
+    }
+    for (int p = 0; p < PX; ++p) {
+        vx_at[p] = (xr + p * RX) * (int)a.pitch + xc;
+        vs_at[p] = (xr + p * RX) * (int)a.nrun + xc / (int)kRun;
+    }
     u32x4 va[PA], vx[PX];
-    uint32_t sx[PX];
-    auto load = [&](int64_t m) {
+    uint32_t ve[PA], sx[PX];
+    int64_t m = lo - K;                  // the row that the registers start with
+    auto load = [&] {
+        m += K;
+        const auto ra = window(pa, la), rx = window(px, lx), rs = window(ps, ls);
 #pragma unroll
-        for (int p = 0; p < PA; ++p)
-            va[p] = load_vec<D>(pa + p * RA * a.lddy * E, m + ar + p * RA < hi ? an : 0);
+        for (int p = 0; p < PA; ++p) {
+            va[p] = __builtin_amdgcn_raw_buffer_load_b128(ra, va_at[p] & ~3u, 0, 0);
+            if constexpr (ODD) ve[p] = __builtin_amdgcn_raw_buffer_load_b32(ra, (va_at[p] & ~3u) + 16, 0, 0);
+        }
 #pragma unroll
         for (int p = 0; p < PX; ++p) {
-            vx[p] = u32x4{0, 0, 0, 0};
-            sx[p] = 0;
-            if (xin && m + xr + p * RX < hi) {
-                vx[p] = *(const u32x4 *)(px + (int64_t)p * RX * a.pitch);
-                sx[p] = ps[(int64_t)p * RX * a.nrun];
-            }
+            vx[p] = __builtin_amdgcn_raw_buffer_load_b128(rx, vx_at[p], 0, 0);
+            sx[p] = __builtin_amdgcn_raw_buffer_load_b8(rs, vs_at[p], 0, 0);
         }
-        pa += kStep * a.lddy * E;
-        px += (int64_t)kStep * a.pitch;
-        ps += (int64_t)kStep * a.nrun;
+        pa += K * a.lddy * E, la -= K * a.lddy * E;
+        px += (int64_t)K * a.pitch, lx -= (int64_t)K * a.pitch;
+        ps += (int64_t)K * a.nrun, ls -= (int64_t)K * a.nrun;
     };
     auto stage = [&](char *buf) {
 #pragma unroll
         for (int p = 0; p < PA; ++p) {
+            const int id = t + p * kThreads;
+            if (NA % kThreads && id >= NA) break;
             uint32_t w[T][V / 2];
+            if constexpr (ODD) {
+                const uint32_t shift = (va_at[p] & 2) * 8;
+                for (int i = 0; i < 3; ++i) va[p][i] = __builtin_amdgcn_alignbit(va[p][i + 1], va[p][i], shift);
+                va[p][3] = __builtin_amdgcn_alignbit(ve[p], va[p][3], shift);
+                if (m + id / VO >= hi) va[p] = u32x4{0, 0, 0, 0};
+            }
             terms<D, T>(va[p], w);
             for (int k = 0; k < T; ++k) {
-                char *q = buf + k * TA + tile_at<BO>(ar + p * RA, ac);
+                char *q = buf + k * TA + tile_at<BO>(id / VO, id % VO * V);
                 if constexpr (V == 8)
                     *(u32x4 *)q = u32x4{w[k][0], w[k][1], w[k][V / 2 - 2], w[k][V / 2 - 1]};
                 else
                     *(u32x2 *)q = u32x2{w[k][0], w[k][1]};
             }
         }
-        if (xr < kStep) {
+        if (RX <= K || xr < K) {
 #pragma unroll
             for (int p = 0; p < PX; ++p) {
                 uint32_t w[8];
@@ -155,30 +193,35 @@ __global__ __launch_bounds__(kThreads) void k_wgrad(WgradArgs a)
 
     const int oi = wave / WC * (BO / WR), cj = wave % WC * (BC / WC);
     f32x16 acc[NI][NJ] = {};
-    int cur = 0;
-    if (lo < hi) {
-        load(lo);
-        stage(lds);
-    }
-    for (int64_t m = lo; m < hi; m += kStep) {
-        __syncthreads();
-        const bool more = m + kStep < hi;
-        if (more) load(m + kStep);
-        const char *buf = lds + cur * BUF;
+    auto multiply = [&](const char *buf, int k) {
+        bf16x8 fx[NJ];
 #pragma unroll
-        for (int k = 0; k < kStep; k += 16) {
-            bf16x8 fx[NJ];
-            for (int j = 0; j < NJ; ++j) fx[j] = fragment<BC>(buf + T * TA, k, cj + 32 * j);
-            // the smallest terms first
-            for (int q = T - 1; q >= 0; --q)
-                for (int i = 0; i < NI; ++i) {
-                    const bf16x8 fa = fragment<BO>(buf + q * TA, k, oi + 32 * i);
-                    for (int j = 0; j < NJ; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fx[j], acc[i][j], 0, 0, 0);
-                }
-        }
+        for (int j = 0; j < NJ; ++j) fx[j] = fragment<BC>(buf + T * TA, k, cj + 32 * j);
+        // the smallest terms first
+#pragma unroll
+        for (int q = T - 1; q >= 0; --q)
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const bf16x8 fa = fragment<BO>(buf + q * TA, k, oi + 32 * i);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fx[j], acc[i][j], 0, 0, 0);
+            }
+    };
+    int cur = 0;
+    load();
+    stage(lds);
+    load();
+    for (int64_t step = lo; step < hi; step += K) {
+        __syncthreads();
+        const char *buf = lds + cur * BUF;
         cur ^= 1;
-        if (more) stage(lds + cur * BUF);
+        multiply(buf, 0);
+        stage(lds + cur * BUF);          // loaded while the last step ran
+        load();
+        __builtin_amdgcn_sched_barrier(0);   // not later: they have this step's products to arrive in
+#pragma unroll
+        for (int k = 16; k < K; k += 16) multiply(buf, k);
     }
 
     float *out = a.split > 1 ? a.part + (size_t)slice * a.O * a.C : a.dw;
@@ -199,56 +242,114 @@ __global__ __launch_bounds__(kThreads) void k_wgrad(WgradArgs a)
         }
 }
 
-// Sum of the slices, in order.
-__global__ __launch_bounds__(256) void k_wgrad_sum(WgradArgs a)
+// Sum of the slices, in a fixed order: a workgroup takes 256 values of dW, its
+// W waves each a run of the slices.
+template <int W> __global__ __launch_bounds__(64 * W) void k_wgrad_sum(WgradArgs a)
 {
-    const size_t n = (size_t)a.O * a.C;
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
-        float s = 0;
+    __shared__ f32x4 sh[W][64];
+    const size_t n = (size_t)a.O * a.C, i = ((size_t)blockIdx.x * 64 + (threadIdx.x & 63)) * 4;
+    const uint32_t w = threadIdx.x >> 6;
+    const uint32_t k0 = w * a.split / W, k1 = (w + 1) * a.split / W;
+    f32x4 s = {0, 0, 0, 0};
+    if (i + 4 <= n) {
 #pragma unroll 8
-        for (uint32_t k = 0; k < a.split; ++k) s += a.part[k * n + i];
-        a.dw[i] = a.add ? a.dw[i] + s : s;
+        for (uint32_t k = k0; k < k1; ++k) s += *(const f32x4_u4 *)(a.part + k * n + i);
+    } else {
+        for (uint32_t k = k0; k < k1; ++k)
+            for (int j = 0; j < 3; ++j)
+                if (i + j < n) s[j] += a.part[k * n + i + j];
+    }
+    sh[w][threadIdx.x & 63] = s;
+    __syncthreads();
+    if (w) return;
+    for (int k = 1; k < W; ++k) s += sh[k][threadIdx.x];
+    if (i + 4 <= n) {
+        f32x4_u4 *p = (f32x4_u4 *)(a.dw + i);
+        *p = a.add ? *p + s : s;
+    } else {
+        for (int j = 0; j < 3; ++j)
+            if (i + j < n) a.dw[i + j] = a.add ? a.dw[i + j] + s[j] : s[j];
     }
 }
 
-template <int D, int BO, int BC, int WR, int WC> hipError_t run(const WgradArgs &a, hipStream_t s)
+template <int D, int BO, int BC, int WR, int WC, int K> hipError_t run(const WgradArgs &a, hipStream_t s)
 {
     constexpr int T = kTerms<D>;
-    constexpr int lds = 2 * (T * kStep * BO * 2 + kStep * BC * 2);
-    const auto k = k_wgrad<D, BO, BC, WR, WC>;
+    constexpr int lds = 2 * (T * K * BO * 2 + K * BC * 2);
+    bool odd = false;
+    if constexpr (D != kF32) odd = (((uintptr_t)a.dy | (uint64_t)a.lddy * Elem<D>::E) & 3) != 0;
+    auto k = k_wgrad<D, BO, BC, WR, WC, K, false>;
+    if constexpr (D != kF32)
+        if (odd) k = k_wgrad<D, BO, BC, WR, WC, K, true>;
     if (lds > 65536)
         if (hipError_t e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
             e != hipSuccess)
             return e;
-    k<<<a.to * a.tc * a.split, kThreads, lds, s>>>(a);
+    k<<<a.to * a.tc * a.split, 64 * WR * WC, lds, s>>>(a);
     return hipGetLastError();
 }
 
+// The tiles, and the time (ns) that one takes a row on a compute unit that is
+// full of them, for one, two and three terms; `alone`: when it is the only one.
+// Measured with 8192 x 2048 outputs over 4096 to 16384 rows, and with one
+// workgroup a unit over 200704 rows.
+struct Tile {
+    int bo, bc;
+    float full[3], alone[3];
+};
+constexpr Tile kTiles[] = {
+    {256, 256, {32.0f, 58.0f, 91.0f}, {31.0f, 50.0f, 80.0f}},
+    {192, 256, {25.0f, 45.0f, 70.0f}, {25.0f, 40.0f, 62.0f}},
+    {128, 128, {10.4f, 20.0f, 27.5f}, {20.0f, 25.0f, 35.0f}},
+    {256, 64, {11.0f, 27.0f, 57.0f}, {20.0f, 40.0f, 57.0f}},
+    {64, 256, {11.5f, 20.0f, 26.0f}, {20.0f, 25.0f, 31.0f}},
+    {64, 64, {4.3f, 7.4f, 11.0f}, {8.5f, 12.0f, 17.0f}},
+};
 template <int D> hipError_t run_tile(uint32_t tile, const WgradArgs &a, hipStream_t s)
 {
-    if (tile == 128) return run<D, 128, 128, 2, 2>(a, s);
-    return run<D, 64, 64, 2, 2>(a, s);
+    constexpr int K = D == kBF16 ? 64 : 32;
+    switch (tile) {
+    case 0: return run<D, 256, 256, 2, 4, K>(a, s);
+    case 1: return run<D, 192, 256, 2, 4, K>(a, s);
+    case 2: return run<D, 128, 128, 2, 2, K>(a, s);
+    case 3: return run<D, 256, 64, 4, 1, K>(a, s);
+    case 4: return run<D, 64, 256, 1, 4, K>(a, s);
+    default: return run<D, 64, 64, 2, 2, 64>(a, s);
+    }
 }
 
 }  // namespace
 
+// The tile and the number of row slices with the least time by a model of it:
+// the rounds of workgroups on 256 compute units, or the bytes of the operands,
+// then dW once, or the slices' sums written and read again.
 WgradPlan wgrad_plan(int dtype, int64_t M, int64_t O, int64_t C)
 {
-    WgradPlan p = {};
-    p.tile = O <= 64 || C <= 64 ? 64 : 128;
-    p.to = (uint32_t)((O + p.tile - 1) / p.tile);
-    p.tc = (uint32_t)((C + p.tile - 1) / p.tile);
-    int64_t split = 512 / ((int64_t)p.to * p.tc);
-    const int64_t most = (M + 255) / 256;
-    if (split > most) split = most;
-    if (split < 1) split = 1;
-    int64_t per = (M + split - 1) / split;
-    per = (per + kStep - 1) / kStep * kStep;
-    if (per < kStep) per = kStep;
-    p.rows_per = per;
-    p.split = (uint32_t)((M + per - 1) / per);
-    if (p.split < 1) p.split = 1;
-    return p;
+    const int terms = dtype == kBF16 ? 0 : dtype == kF16 ? 1 : 2;
+    const double in = (double)M * (O * elem_bytes(dtype) + C * 1.04) / 4800, out = (double)O * C * 4;
+    WgradPlan best = {};
+    double least = 0;
+    for (uint32_t t = 0; t < sizeof(kTiles) / sizeof(kTiles[0]); ++t) {
+        WgradPlan p = {};
+        p.tile = t;
+        p.to = (uint32_t)((O + kTiles[t].bo - 1) / kTiles[t].bo);
+        p.tc = (uint32_t)((C + kTiles[t].bc - 1) / kTiles[t].bc);
+        const double tiles = (double)p.to * p.tc;
+        for (int64_t want = 1; want <= 512; want = want < 4 ? want + 1 : want % 3 ? want + want / 2 : want / 3 * 4) {
+            int64_t per = ((M + want - 1) / want + 63) / 64 * 64;
+            if (per < 64) per = 64;
+            p.rows_per = per;
+            p.split = (uint32_t)((M + per - 1) / per);
+            if (p.split < 1) p.split = 1;
+            const double n = std::ceil(tiles * p.split / 256);
+            const double rows = (double)(p.split > 1 ? per : M);
+            double ns = std::fmax(rows * std::fmax(n * kTiles[t].full[terms], kTiles[t].alone[terms]), in);
+            ns += p.split > 1 ? 3500 + out * (2 * p.split + 1) / 7500 : out / 5000;
+            if (!least || ns < least) least = ns, best = p;
+            if (want > 1 && (per == 64 || tiles * want > 4096)) break;
+        }
+    }
+    return best;
 }
 
 hipError_t launch_wgrad(const WgradPlan &p, WgradArgs a, int dtype, hipStream_t s)
@@ -258,8 +359,13 @@ hipError_t launch_wgrad(const WgradPlan &p, WgradArgs a, int dtype, hipStream_t 
                    : dtype == kBF16 ? run_tile<kBF16>(p.tile, a, s)
                                     : run_tile<kF16>(p.tile, a, s);
     if (e != hipSuccess || p.split == 1) return e;
-    const size_t n = (size_t)a.O * a.C, g = (n + 255) / 256;
-    k_wgrad_sum<<<(uint32_t)(g < 65536 ? g : 65536), 256, 0, s>>>(a);
+    const uint32_t g = (uint32_t)(((size_t)a.O * a.C + 255) / 256);
+    if (p.split >= 32)
+        k_wgrad_sum<16><<<g, 1024, 0, s>>>(a);
+    else if (p.split >= 4)
+        k_wgrad_sum<4><<<g, 256, 0, s>>>(a);
+    else
+        k_wgrad_sum<2><<<g, 128, 0, s>>>(a);
     return hipGetLastError();
 }
 

@@ -136,6 +136,8 @@ def test_wgrad_refusals():
         return L.lags_ckpt_wgrad(rows, outs, cols, dy, ld, dtype, ck, ckn, dw, flags, ws, wsn, None)
     assert call(dtype=4) == EINVAL and call(flags=4) == EINVAL
     assert call(rows=-1) == ERANGE and call(outs=0) == ERANGE and call(cols=0) == ERANGE and call(outs=1 << 31) == ERANGE
+    assert call(outs=(1 << 22) + 1, ld=1 << 23) == ERANGE and call(ld=(1 << 22) + 1) == ERANGE
+    assert bytes_(64, 1 << 22, 1, 1) >= 16 and bytes_(64, 1, (1 << 22) + 1, 1) == 0
     assert call(dy=None) == EINVAL and call(ld=99) == EINVAL and call(dy=P(0) + 1) == EINVAL
     assert call(dw=None) == EINVAL and call(dw=P(2) + 2) == EINVAL
     assert call(ck=None) == EWS and call(ckn=cb - 1) == EWS and call(ck=P(1) + 8) == EWS

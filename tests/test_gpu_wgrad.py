@@ -47,7 +47,8 @@ def _check(tag, dw, dy, val):
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("m,o,c", [(1, 1, 1), (1, 64, 64), (3, 5, 17), (31, 64, 64), (32, 65, 63), (33, 128, 128),
                                    (64, 1, 300), (100, 300, 1), (257, 129, 200), (1000, 70, 33), (513, 256, 256),
-                                   (2048, 64, 32), (5000, 256, 64), (700, 1000, 500), (300, 513, 777)])
+                                   (2048, 64, 32), (5000, 256, 64), (700, 1000, 500), (300, 513, 777),
+                                   (900, 190, 250), (130, 383, 700), (64, 6000, 31), (2000, 63, 1000)])
 def test_shapes(m, o, c, dtype):
     dy, ck, val = _inputs(m, o, c, dtype, m + o + c)
     _check(f"{m}x{o}x{c} {dtype}", _run(dy, ck, o, c), dy, val)
@@ -120,6 +121,30 @@ def test_non_finite(dtype):
         assert np.array_equal(rest[row], want, equal_nan=True)
     keep = [i for i in range(o) if i not in (3, 60, 64)]
     assert np.isfinite(rest[keep]).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_odd_rows_past_the_slice(dtype):
+    """Rows of odd length start inside a word; what follows the matrix there, and the first value of
+    the next slice of the rows, stay out of the sums, infinities and NaN too."""
+    import torch
+    m, o, c = 5000, 67, 64
+    dy, ck, val = _inputs(m, o, c, dtype, 12)
+    base = _run(dy, ck, o, c)
+    big = torch.full((m * o + 70,), float("nan"), dtype=dy.dtype, device="cuda")
+    for off in (0, 1, 3):
+        big[off:off + m * o] = dy.reshape(-1)
+        view = torch.as_strided(big, (m, o), (o, 1), off)
+        assert torch.equal(_run(view, ck, o, c), base), off
+        big.fill_(float("nan"))
+    dy[::64, 0] = float("inf")
+    with np.errstate(invalid="ignore"):
+        want = (np.inf * val[::64]).sum(axis=0)
+    got = _run(dy, ck, o, c).cpu().numpy()
+    assert np.array_equal(np.isnan(got[0]), np.isnan(want)) and np.isfinite(got[1:]).all()
+    one = np.sign(val[::64])
+    same = (one == one[0]).all(axis=0) & (one[0] != 0)        # infinities of one sign: no NaN
+    assert np.array_equal(got[0][same], np.inf * one[0][same])
 
 
 def test_fp32_keeps_its_digits():
