@@ -393,6 +393,7 @@ const char *lags_kernel_name(int32_t id);
 #define LAGS_GRAD_ADD 1u /* add to the gradient buffer instead of overwriting it */
 #define LAGS_CKPT_RUN 32 /* columns of a row that share a scale */
 #define LAGS_SLAB_MAX 4096 /* see lags_gn */
+#define LAGS_GN_MAX (1 << 18) /* channels and pitches of lags_gn */
 #define LAGS_WGRAD_MAX (1 << 22) /* outs, cols and lddy of lags_ckpt_wgrad */
 
 /*
@@ -431,8 +432,8 @@ int lags_ckpt_unpack(int64_t rows, int64_t cols, const void *ckpt, size_t ckpt_b
  *   xh = (x - mean) * rstd;  z = xh * gamma + beta;  y = act(z)
  * in fp32, each operation of xh and z rounded by itself.  (spatial = 1 and
  * groups = 1 is a layer normalisation.)
- * Limits: samples, spatial in [0, 2^31), channels in [1, 2^31) a multiple of
- * groups, eps >= 0 and finite.  The smallest number of channels that is both
+ * Limits: samples, spatial in [0, 2^31), channels in [1, LAGS_GN_MAX] a multiple
+ * of groups, every ld <= LAGS_GN_MAX, eps >= 0 and finite.  The smallest number of channels that is both
  * whole groups and a multiple of 32, or all channels if that is less, is at
  * most LAGS_SLAB_MAX (else LAGS_ERANGE).
  */

@@ -13,6 +13,8 @@ LIB = os.path.join(HERE, "liblags.so")
 SOURCES = [os.path.join(CSRC, "lags_host.cpp"), os.path.join(CSRC, "lags_schedule.cpp"),
            os.path.join(CSRC, "lags_kernels.hip"), os.path.join(CSRC, "lags_act.cpp"),
            os.path.join(CSRC, "lags_ckpt.hip"), os.path.join(CSRC, "lags_gn.hip"),
+           os.path.join(CSRC, "lags_gn_f32.hip"), os.path.join(CSRC, "lags_gn_bf16.hip"),
+           os.path.join(CSRC, "lags_gn_f16.hip"),
            os.path.join(CSRC, "lags_wgrad.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

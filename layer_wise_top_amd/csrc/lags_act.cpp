@@ -1,9 +1,10 @@
 // Host side of the activation operators: argument validation, workspace sizes
 // and launches.  The entry points are declared in include/lags.h.
 #include "lags.h"
-#include "lags_act.h"
+#include "lags_gn.h"
 
 #include <cmath>
+#include <initializer_list>
 
 using namespace lags;
 
@@ -11,6 +12,92 @@ static_assert(kF32 == LAGS_F32 && kBF16 == LAGS_BF16 && kF16 == LAGS_F16, "one n
 static_assert(kActNone == LAGS_ACT_NONE && kActRelu == LAGS_ACT_RELU && kActSilu == LAGS_ACT_SILU,
               "one numbering");
 static_assert(kRun == LAGS_CKPT_RUN && kSlabMax == LAGS_SLAB_MAX, "one size");
+
+namespace {
+uint32_t gcd(uint32_t a, uint32_t b) { return b ? gcd(b, a % b) : a; }
+}  // namespace
+
+namespace lags {
+// Register rows a thread of a resident workgroup aims at.  Forward 13: 28 x 28
+// positions by 64 bf16 channels in 512 threads, two workgroups a compute unit
+// (26 us for 64 x 784 x 512; 8 rows in 1024 threads: 28 us).  Backward 8, which
+// leaves the registers for two workgroups (41 us; 13: 46 us), but 13 with silu,
+// whose own registers 8 rows would spill (51 us; 8: 56 us).
+static uint32_t rows_aimed_at(bool backward, int act) { return backward && act != kActSilu ? 8 : kMostRows; }
+
+GnPlan gn_plan(int dtype, int act, bool backward, bool split, uint64_t N, uint64_t S, uint32_t C, uint32_t G)
+{
+    GnPlan p = {};
+    const uint32_t E = elem_bytes(dtype), V = 16 / E, cg = C / G;
+    // a slab is whole groups and whole runs
+    const uint64_t whole = (uint64_t)(cg / gcd(cg, kRun)) * kRun;
+    const uint32_t unit = whole < C ? (uint32_t)whole : C;
+    if (unit > kSlabMax) return p;
+    auto slab = [&](uint32_t bytes) {
+        uint32_t w = unit;
+        while (w < C && w * E < bytes && w + unit <= kSlabMax) w += unit;
+        if (w > C) w = C;
+        p.tcl = 0;
+        while ((V << p.tcl) < w || (V << p.tcl) < kRun) ++p.tcl;
+        p.w = w;
+        p.nslab = (C + w - 1) / w;
+        return S << p.tcl;                         // vectors of a slab's lanes
+    };
+    const uint32_t most = backward ? kResidentBwd : kResident;
+    const uint64_t room = (uint64_t)most * kMostRows;
+    if (!split) {
+        // the widest slab, up to 256 bytes of a row (forward: 128), that the registers aimed at hold and
+        // that leaves two workgroups a compute unit; else 64 bytes, as long as they fit at all.
+        // 64 x 196 x 1024 backward: 256 bytes 20 us, 64 bytes 23 us.
+        uint64_t vecs = 0;
+        for (uint32_t bytes = backward ? 256 : 128; bytes >= 64; bytes /= 2) {
+            vecs = slab(bytes);
+            if (vecs <= (uint64_t)most * (backward ? 8 : kMostRows) && N * p.nslab >= 512) break;
+        }
+        // too few slabs to fill the GPU: split, unless the work is so small that one launch is what counts
+        p.resident = (1u << p.tcl) <= most && (vecs <= 2048 || (vecs <= room && N * p.nslab >= 128));
+        if (p.resident) {
+            const uint32_t rows = rows_aimed_at(backward, act);
+            p.threads = 1u << p.tcl;
+            if (p.threads < 64) p.threads = 64;
+            while (p.threads < 256 && (uint64_t)p.threads * 2 < vecs) p.threads *= 2;
+            while (p.threads < most && (uint64_t)p.threads * rows < vecs) p.threads *= 2;
+            p.rows = (uint32_t)((vecs + p.threads - 1) / p.threads);
+            // backward: several samples a workgroup where there are far more than fill the GPU
+            uint64_t nper = 1;
+            while (backward && N * p.nslab / nper > 4096 && nper < N) nper *= 2;
+            p.nper = (uint32_t)nper;
+            p.nparts = (uint32_t)((N + nper - 1) / nper);
+        }
+    }
+    if (!p.resident) {
+        // whole rows of up to 256 bytes: 64 x 3136 x 256 backward 94 us (64 bytes: 97, 1024: 99)
+        slab(256);
+        p.threads = 1u << p.tcl;
+        if (p.threads < 512) p.threads = 512;
+        // chunks: about 2048 workgroups (1024: 95 us, 4096: 96 us), whole sweeps each
+        const uint64_t sweep = (uint64_t)(p.threads >> p.tcl) * kSweep;
+        uint64_t want = 2048 / (N * p.nslab);
+        if (want < 1) want = 1;
+        uint64_t chunk = (S + want - 1) / want;
+        chunk = (chunk + sweep - 1) / sweep * sweep;
+        if (chunk > S) chunk = S;
+        p.chunk = (uint32_t)chunk;
+        p.nchunk = (uint32_t)((S + chunk - 1) / chunk);
+        if (N * p.nchunk > 0x7fffffffull) return GnPlan{};
+        p.nparts = (uint32_t)(N * p.nchunk);
+    }
+    const uint64_t grid = (p.resident ? N : N * p.nchunk) * p.nslab;
+    return grid <= 0x7fffffffull ? p : GnPlan{};
+}
+
+size_t gn_part_floats(const GnPlan &p, bool backward, uint64_t N, uint32_t C, uint32_t G)
+{
+    if (backward) return (size_t)p.nparts * 2 * C;
+    return p.resident ? 0 : (size_t)N * G * p.nchunk * 2;
+}
+
+}  // namespace lags
 
 namespace {
 
@@ -49,7 +136,7 @@ int matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
 {
     const uint32_t e = elem_bytes(dtype);
     if (!p || !aligned(p, e) || ld < cols) return LAGS_EINVAL;
-    if ((u128)rows * (u128)ld * e > kMaxBytes) return LAGS_ERANGE;
+    if (ld > kMaxDim || (u128)rows * (u128)ld * e > kMaxBytes) return LAGS_ERANGE;
     r = {p, (u128)rows, (u128)cols * e, (u128)ld * e};
     return LAGS_OK;
 }
@@ -79,8 +166,8 @@ int check_pack(int64_t rows, int64_t cols, const void *x, int64_t ldx, int32_t d
 }
 
 struct GnCall {
-    GnPlan fwd, bwd;
-    size_t need;                     // workspace, of both directions
+    GnPlan fwd[2], bwd[2];           // as the shape asks for, and split
+    size_t need;                     // workspace, of all of them
     int64_t rows;
 };
 
@@ -90,7 +177,7 @@ int check_shape(const lags_gn *gn)
     if (gn->act != LAGS_ACT_NONE && gn->act != LAGS_ACT_RELU && gn->act != LAGS_ACT_SILU) return LAGS_EINVAL;
     if (!(gn->eps >= 0) || !std::isfinite(gn->eps)) return LAGS_EINVAL;
     if (gn->samples < 0 || gn->spatial < 0 || gn->channels < 1 || gn->groups < 1) return LAGS_EINVAL;
-    if (gn->samples > kMaxDim || gn->spatial > kMaxDim || gn->channels > kMaxDim) return LAGS_ERANGE;
+    if (gn->samples > kMaxDim || gn->spatial > kMaxDim || gn->channels > LAGS_GN_MAX) return LAGS_ERANGE;
     if (gn->channels % gn->groups) return LAGS_EINVAL;
     return LAGS_OK;
 }
@@ -102,22 +189,40 @@ int plan(const lags_gn *gn, GnCall &c)
     // an empty call is planned as one of one row, whose limits are the same
     const uint64_t N = gn->samples ? gn->samples : 1, S = gn->spatial ? gn->spatial : 1;
     const uint32_t C = (uint32_t)gn->channels, G = (uint32_t)gn->groups;
-    c.fwd = gn_plan(gn->dtype, false, N, S, C, G);
-    c.bwd = gn_plan(gn->dtype, true, N, S, C, G);
-    if (!c.fwd.threads || !c.bwd.threads) return LAGS_ERANGE;
-    const size_t f = gn_part_floats(c.fwd, false, N, C, G) * 4, b = gn_part_floats(c.bwd, true, N, C, G) * 4;
-    c.need = c.rows ? ((f > b ? f : b) + 15) / 16 * 16 : 0;
+    size_t floats = 0;
+    for (int split = 0; split < 2; ++split) {
+        c.fwd[split] = gn_plan(gn->dtype, gn->act, false, split, N, S, C, G);
+        c.bwd[split] = gn_plan(gn->dtype, gn->act, true, split, N, S, C, G);
+        if (!c.fwd[split].threads || !c.bwd[split].threads) return LAGS_ERANGE;
+        const size_t f = gn_part_floats(c.fwd[split], false, N, C, G), b = gn_part_floats(c.bwd[split], true, N, C, G);
+        floats = floats > f ? floats : f;
+        floats = floats > b ? floats : b;
+    }
+    c.need = c.rows ? (floats * 4 + 15) / 16 * 16 : 0;
     if (c.need < 16) c.need = 16;
     return LAGS_OK;
 }
 
-void fill(const lags_gn *gn, GnArgs &a)
+void fill(const lags_gn *gn, const GnPlan &p, GnArgs &a)
 {
     const CkptShape cs = ckpt_shape(0, gn->channels);
     a.eps = gn->eps;
     a.N = (uint32_t)gn->samples, a.S = (uint32_t)gn->spatial;
     a.C = (uint32_t)gn->channels, a.G = (uint32_t)gn->groups, a.cg = a.C / a.G;
     a.pitch = cs.pitch, a.nrun = cs.nrun;
+    a.act = gn->act, a.inv_cg = 1.0f / (float)a.cg;
+    a.w = p.w, a.nslab = p.nslab, a.tcl = p.tcl, a.nchunk = p.nchunk, a.chunk = p.chunk;
+    a.nper = p.nper, a.nparts = p.nparts;
+}
+
+// A resident workgroup reaches its rows by 32-bit offsets; where a pitch is too
+// large for that the split form runs (its offsets span one sweep of rows).
+bool split_only(const GnPlan &p, int dtype, std::initializer_list<int64_t> lds)
+{
+    for (int64_t ld : lds)
+        if (p.resident && (uint64_t)(p.threads >> p.tcl) * kMostRows * ld * elem_bytes(dtype) >= 0x7fffffffull)
+            return true;
+    return false;
 }
 
 // `out` must not overlap any of the n regions of `all` but itself.
@@ -180,6 +285,7 @@ int lags_gn_forward(const lags_gn *gn, const void *x, int64_t ldx, const float *
     Region r[8];
     if (int rc = matrix(x, c.rows, gn->channels, ldx, gn->dtype, r[0]); rc != LAGS_OK) return rc;
     if (int rc = matrix(y, c.rows, gn->channels, ldy, gn->dtype, r[1]); rc != LAGS_OK) return rc;
+    if (ldx > LAGS_GN_MAX || ldy > LAGS_GN_MAX) return LAGS_ERANGE;
     if (!gamma != !beta || !aligned(gamma, 4) || !aligned(beta, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
         return LAGS_EINVAL;
     const size_t cb = (size_t)gn->channels * 4, sb = (size_t)gn->samples * gn->groups * 4;
@@ -197,12 +303,13 @@ int lags_gn_forward(const lags_gn *gn, const void *x, int64_t ldx, const float *
     if (overlap(r[1], r[2]) || overlap(r[1], r[3]) || (overlap(r[0], r[1]) && !same(r[0], r[1]))) return LAGS_EINVAL;
     if (!c.rows) return LAGS_OK;
     GnArgs a = {};
-    fill(gn, a);
+    const GnPlan &p = c.fwd[split_only(c.fwd[0], gn->dtype, {ldx, ldy})];
+    fill(gn, p, a);
     a.x = x, a.ldx = ldx, a.y = y, a.ldy = ldy;
     a.gamma = gamma, a.beta = beta, a.mean = mean, a.rstd = rstd;
     if (ckpt) a.wcodes = (uint8_t *)ckpt, a.wscales = (uint8_t *)ckpt + (size_t)c.rows * a.pitch;
     a.part = (float *)ws;
-    return hip(launch_gn_forward(c.fwd, a, gn->dtype, gn->act, (hipStream_t)stream));
+    return hip(launch_gn_forward(p, a, gn->dtype, (hipStream_t)stream));
 }
 
 int lags_gn_backward(const lags_gn *gn, const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *ckpt,
@@ -226,6 +333,7 @@ int lags_gn_backward(const lags_gn *gn, const void *dy, int64_t lddy, const void
         need_ck = ckpt_size(ckpt_shape(c.rows, gn->channels));
         if (!aligned(ckpt, 16) || ckpt_bytes < need_ck) return LAGS_EWORKSPACE;
     }
+    if (lddy > LAGS_GN_MAX || lddx > LAGS_GN_MAX || (x && ldx > LAGS_GN_MAX)) return LAGS_ERANGE;
     if (!gamma != !beta || !mean || !rstd || !aligned(gamma, 4) || !aligned(beta, 4) || !aligned(mean, 4) ||
         !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(dbeta, 4))
         return LAGS_EINVAL;
@@ -240,13 +348,14 @@ int lags_gn_backward(const lags_gn *gn, const void *dy, int64_t lddy, const void
         if (overlap(r[1], r[in])) return LAGS_EINVAL;
     if (overlap(r[0], r[1]) && !same(r[0], r[1])) return LAGS_EINVAL;
     GnArgs a = {};
-    fill(gn, a);
+    const GnPlan &p = c.bwd[split_only(c.bwd[0], gn->dtype, {lddy, lddx, x ? ldx : 0})];
+    fill(gn, p, a);
     a.dy = dy, a.lddy = lddy, a.dx = dx, a.lddx = lddx, a.x = x, a.ldx = ldx;
     if (ckpt) a.rcodes = (const uint8_t *)ckpt, a.rscales = (const uint8_t *)ckpt + (size_t)c.rows * a.pitch;
     a.gamma = gamma, a.beta = beta, a.mean = (float *)mean, a.rstd = (float *)rstd;
     a.dgamma = dgamma, a.dbeta = dbeta, a.add = flags & LAGS_GRAD_ADD;
     a.part = (float *)ws;
-    return hip(launch_gn_backward(c.bwd, a, gn->dtype, gn->act, (hipStream_t)stream));
+    return hip(launch_gn_backward(p, a, gn->dtype, (hipStream_t)stream));
 }
 
 size_t lags_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols, int32_t dtype)

@@ -51,7 +51,8 @@ struct GnArgs {
     float *mean, *rstd;              // forward: written where not null; backward: read
     float *dgamma, *dbeta;
     float *part;                     // workspace
-    float eps;
+    float eps, inv_cg;
+    int act;
     uint32_t add;                    // dgamma, dbeta are added to
     uint32_t N, S, C, G, cg;         // samples, positions, channels, groups, channels per group
     uint32_t pitch, nrun;
@@ -86,10 +87,13 @@ struct GnPlan {
 };
 constexpr uint32_t kSlabMax = 4096;  // channels a workgroup spans, at most
 // .threads == 0: the shape is not supported
-GnPlan gn_plan(int dtype, bool backward, uint64_t N, uint64_t S, uint32_t C, uint32_t G);
+GnPlan gn_plan(int dtype, int act, bool backward, bool split, uint64_t N, uint64_t S, uint32_t C, uint32_t G);
 size_t gn_part_floats(const GnPlan &p, bool backward, uint64_t N, uint32_t C, uint32_t G);
-hipError_t launch_gn_forward(const GnPlan &p, GnArgs a, int dtype, int act, hipStream_t s);
-hipError_t launch_gn_backward(const GnPlan &p, GnArgs a, int dtype, int act, hipStream_t s);
+template <int D> hipError_t launch_gn_forward(const GnPlan &p, const GnArgs &a, hipStream_t s);
+template <int D> hipError_t launch_gn_backward(const GnPlan &p, const GnArgs &a, hipStream_t s);
+hipError_t launch_gn_forward(const GnPlan &p, const GnArgs &a, int dtype, hipStream_t s);
+hipError_t launch_gn_backward(const GnPlan &p, const GnArgs &a, int dtype, hipStream_t s);
+constexpr int kSweep = 4;          // rows a thread requests at a time (split form)
 
 struct WgradPlan {
     uint32_t tile, to, tc, split;
@@ -167,12 +171,18 @@ template <> struct Elem<kF16> {
             f[2 * i + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(v[i] >> 16));
         }
     }
+    // rounded to fp32 first, then to fp16: the compiler joins some conversions
+    // with the operation before them, which rounds once, and which ones it joins
+    // differs between kernels that are to agree bit for bit
     __device__ static u32x4 pack(const float (&f)[8])
     {
         u32x4 r;
-        for (int i = 0; i < 4; ++i)
-            r[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f[2 * i]) |
-                   (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f[2 * i + 1]) << 16;
+        for (int i = 0; i < 4; ++i) {
+            float a = f[2 * i], b = f[2 * i + 1];
+            asm("" : "+v"(a), "+v"(b));
+            r[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)a) |
+                   (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)b) << 16;
+        }
         return r;
     }
     __device__ static uint32_t top(u32x4 v)
@@ -205,14 +215,65 @@ template <int D> __device__ inline void store_vec(void *p, u32x4 v, int n)
         *(u32x4_u2 *)p = v;
         return;
     }
-    for (int i = 0; i < V - 1; ++i)
-        if (i < n) {
-            if constexpr (Elem<D>::E == 4)
-                ((uint32_t *)p)[i] = v[i];
-            else
-                ((uint16_t *)p)[i] = (uint16_t)(v[i / 2] >> (i % 2 * 16));
+    if (n <= 0) return;
+    if constexpr (V == 8) {
+        typedef uint32_t u32_u2 __attribute__((aligned(2)));
+        typedef uint32_t u32x2_u2 __attribute__((ext_vector_type(2), aligned(2)));
+        uint16_t *q = (uint16_t *)p;
+        if (n & 4) {
+            *(u32x2_u2 *)q = u32x2_u2{v[0], v[1]};
+            q += 4, v[0] = v[2], v[1] = v[3];
         }
+        if (n & 2) {
+            *(u32_u2 *)q = v[0];
+            q += 2, v[0] = v[1];
+        }
+        if (n & 1) *q = (uint16_t)v[0];
+    } else {
+        for (int i = 0; i < V - 1; ++i)
+            if (i < n) ((uint32_t *)p)[i] = v[i];
+    }
 }
+
+// A buffer descriptor for `left` bytes at p: reads past them give zeros, so a
+// loop needs no branch between its loads.
+__device__ inline __amdgpu_buffer_rsrc_t window(const void *p, int64_t left)
+{
+    const int n = left > 0x7ffffffc ? 0x7ffffffc : left < 0 ? 0 : (int)left;
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, n, 0x00020000);
+}
+
+// One column of vectors over `rows` rows of a matrix, through a window of
+// them.  Values of columns past the window's width are whatever lies there;
+// rows past its end read as zeros.  ODD: 16-bit rows that may start inside a
+// word (odd pitch, odd slice): five words are read for a vector's four and
+// shifted into place.
+template <int D, bool ODD> struct Reader {
+    __amdgpu_buffer_rsrc_t r;
+    uint32_t at, pitch, rows;
+    __device__ Reader(const void *base, int64_t row0, uint32_t n, int64_t ld, uint32_t c0, uint32_t w, uint32_t col)
+    {
+        constexpr int V = Elem<D>::V, E = Elem<D>::E;
+        const char *p = (const char *)base + (row0 * ld + c0) * E;
+        const uint32_t into = ODD ? (uint32_t)((uintptr_t)p & 3) : 0;
+        // whole words: what a last one holds beside the last value is a column past the width or
+        // (ODD) the next row's first, which load() drops
+        r = window(p - into, n ? (((int64_t)(n - 1) * ld + w) * E + into + 3) & ~(int64_t)3 : 0);
+        at = col * V < w ? into + col * V * E : 0x80000000u;       // idle lanes read nothing
+        pitch = (uint32_t)(ld * E);
+        rows = n;
+    }
+    __device__ u32x4 load(uint32_t row) const
+    {
+        const uint32_t o = at + row * pitch;
+        if constexpr (!ODD) return __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0);
+        u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, o & ~3u, 0, 0);
+        const uint32_t e = __builtin_amdgcn_raw_buffer_load_b32(r, (o & ~3u) + 16, 0, 0), sh = (o & 2) * 8;
+        for (int i = 0; i < 3; ++i) v[i] = __builtin_amdgcn_alignbit(v[i + 1], v[i], sh);
+        v[3] = __builtin_amdgcn_alignbit(e, v[3], sh);
+        return row < rows ? v : u32x4{0, 0, 0, 0};
+    }
+};
 
 // ---- the 8-bit format ------------------------------------------------------
 // Largest magnitude of a run of 32 columns from each lane's vector: the run is
@@ -250,12 +311,90 @@ template <int V> __device__ inline void run_codes(const float (&f)[V], uint32_t 
         q[i] = s == 255 ? 0u : lo | hi << 16;
     }
 }
+// The four codes of a word as numbers.  One instruction each: written out
+// because the compiler extracts the byte first where the word comes out of a
+// vector.
+__device__ inline void code_values(uint32_t q, float *f)
+{
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(f[0]) : "v"(q));
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(f[1]) : "v"(q));
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(f[2]) : "v"(q));
+    asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(f[3]) : "v"(q));
+}
 // The four values that a word of codes stands for.
 __device__ inline void run_values(uint32_t q, float step, float *f)
 {
-    for (int j = 0; j < 4; ++j) f[j] = (float)(int8_t)(q >> (8 * j)) * step;
+    code_values(q, f);
+    for (int j = 0; j < 4; ++j) f[j] *= step;
 }
 __device__ inline float run_step(uint32_t s) { return asf(s << 23); }
+
+// ---- output ----------------------------------------------------------------
+// One column of vectors over `rows` rows of a matrix.  Whole vectors go
+// through a window that ends with the last row, so rows past it are dropped
+// by the hardware; the last vector of a row of odd length, and rows that
+// start inside a word (ODD), are stored piece by piece.
+template <int D, bool ODD> struct Writer {
+    __amdgpu_buffer_rsrc_t r;
+    char *p;
+    uint32_t at, pitch, rows;
+    int nv;
+    __device__ Writer(void *base, int64_t row0, uint32_t n, int64_t ld, uint32_t c0, uint32_t w, uint32_t col)
+    {
+        constexpr int V = Elem<D>::V, E = Elem<D>::E;
+        p = (char *)base + (row0 * ld + c0) * E;
+        r = window(p, n ? ((int64_t)(n - 1) * ld + w) * E : 0);
+        at = col * V * E, pitch = (uint32_t)(ld * E), rows = n;
+        nv = (int)w - (int)(col * V);
+    }
+    __device__ void store(uint32_t row, u32x4 v) const
+    {
+        constexpr int V = Elem<D>::V;
+        const uint32_t o = at + row * pitch;
+        if constexpr (!ODD) {
+            __builtin_amdgcn_raw_buffer_store_b128(v, r, nv >= V ? o : 0x80000000u, 0, 0);
+            if (nv > 0 && nv < V && row < rows) store_vec<D>(p + o, v, nv);
+        } else {
+            if (row < rows) store_vec<D>(p + o, v, nv);
+        }
+    }
+};
+
+// The same of a checkpoint: codes of whole vectors (a row's pad up to its
+// pitch gets zeros), and a scale byte for each run.
+template <int D> struct CodeWriter {
+    __amdgpu_buffer_rsrc_t rq, rs;
+    uint32_t q_at, s_at, pitch, nrun;
+    __device__ CodeWriter(uint8_t *codes, uint8_t *scales, int64_t row0, uint32_t n, uint32_t pitch_, uint32_t nrun_,
+                          uint32_t C, uint32_t c0, uint32_t w, uint32_t col)
+    {
+        constexpr uint32_t V = Elem<D>::V;
+        pitch = pitch_, nrun = nrun_;
+        rq = window(codes + row0 * pitch + c0, (int64_t)n * pitch - c0);
+        rs = window(scales + row0 * nrun + c0 / kRun, (int64_t)n * nrun - c0 / kRun);
+        const uint32_t c = c0 + col * V;
+        // lanes past the slab write nothing unless they are past the last channel too
+        q_at = c < pitch && (col * V < w || c >= C) ? col * V : 0x80000000u;
+        s_at = col * V < w && c % kRun == 0 ? col * V / kRun : 0x80000000u;
+    }
+    // f: the values of `raw`, of which nv count
+    __device__ void store(uint32_t row, u32x4 raw, float (&f)[Elem<D>::V], int nv) const
+    {
+        constexpr int V = Elem<D>::V;
+        if (nv < V) {
+            for (int j = 0; j < V; ++j) f[j] = j < nv ? f[j] : 0.0f;
+            raw = Elem<D>::pack(f);
+        }
+        const uint32_t s = run_scale(run_top<V>(Elem<D>::top(raw)));
+        uint32_t q[V / 4];
+        run_codes<V>(f, s, q);
+        if constexpr (V == 8)
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{q[0], q[V / 4 - 1]}, rq, q_at + row * pitch, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(q[0], rq, q_at + row * pitch, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)s, rs, s_at + row * nrun, 0, 0);
+    }
+};
 #endif
 
 }  // namespace lags

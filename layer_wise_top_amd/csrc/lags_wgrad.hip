@@ -79,13 +79,6 @@ __device__ inline uint32_t deal(uint32_t b, uint32_t n)
     return b < main ? (b & 7) * per + (b >> 3) : b;
 }
 
-// A buffer descriptor for `left` bytes at p: reads past them give zeros.
-__device__ inline __amdgpu_buffer_rsrc_t window(const void *p, int64_t left)
-{
-    const int n = left > 0x7ffffffc ? 0x7ffffffc : left < 0 ? 0 : (int)left;
-    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, n, 0x00020000);
-}
-
 // A workgroup: a BO x BC tile of dW over one slice of the rows; WR x WC waves,
 // K rows staged at a time.  ODD: rows of 16-bit values that may start inside a
 // word (odd pitch, odd slice): five words are read for each vector's four and

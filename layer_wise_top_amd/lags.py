@@ -398,38 +398,64 @@ def kernel_names():
 
 
 # ---- activation operators ---------------------------------------------------
+# These calls are short: at a few thousand values a call, checking the
+# arguments costs more than the kernels.  Each check asks torch once, and
+# pointers go to ctypes as plain integers.
+
+_DTYPES = {}
+
 
 def _dtype_code(dtype) -> int:
-    import torch
-    codes = {torch.float32: LAGS_F32, torch.bfloat16: LAGS_BF16, torch.float16: LAGS_F16}
-    if dtype not in codes:
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: LAGS_F32, torch.bfloat16: LAGS_BF16, torch.float16: LAGS_F16})
+    if dtype not in _DTYPES:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    return codes[dtype]
+    return _DTYPES[dtype]
 
 
-def _matrix(t, name: str, dtype=None, rows=None, cols=None):
-    """A device tensor as a matrix: the last dimension is the columns, the others are rows that
-    one pitch separates (a contiguous tensor, or a slice of its last dimension).  Returns
-    (pointer, rows, cols, ld)."""
+def _place(first, name: str, stream):
+    """(current device, raw stream): `stream`, or the current one.  `first`: a tensor of the call,
+    checked before the device is asked for, so that this raises the same without one."""
+    import torch
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    dev = torch.cuda.current_device()
+    if stream is not None:
+        return dev, stream.cuda_stream
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _on(t, dev: int, name: str):
+    """t must be a tensor on device `dev`."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
-    if dtype is not None and t.dtype != dtype:
+
+
+def _matrix(t, dev: int, name: str, dtype=None, rows=None, cols=None):
+    """A device tensor as a matrix: the last dimension is the columns, the others are rows that
+    one pitch separates (a contiguous tensor, or a slice of its last dimension).  Returns
+    (pointer, rows, cols, ld)."""
+    _on(t, dev, name)
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() < 2:
+    shape = t.shape
+    if len(shape) < 2:
         raise ValueError(f"{name} must have at least two dimensions, channels last")
-    c, r = t.shape[-1], t.numel() // t.shape[-1] if t.shape[-1] else 0
+    c = shape[-1]
+    r = t.numel() // c if c else 0
     if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{name} must hold {rows} rows of {cols} channels, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must hold {rows} rows of {cols} channels, got {tuple(shape)}")
     if t.is_contiguous():
         # an empty tensor's address may be null, which the library refuses
         return t.data_ptr() or (0 if r and c else 16), r, c, c
     if c > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have its channels last and contiguous")
     ld, span = None, 0
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
             continue
         if ld is None:
@@ -443,18 +469,30 @@ def _matrix(t, name: str, dtype=None, rows=None, cols=None):
     return t.data_ptr(), r, c, ld
 
 
-def _vector(t, numel: int, name: str):
-    """A contiguous fp32 device tensor, or None."""
-    import torch
+def _vector(t, dev: int, numel: int, name: str):
+    """A contiguous fp32 device tensor of at least `numel` values, or None."""
     if t is None:
         return None
-    p = _dev_tensor(t, torch.float32, numel, name)
-    return p if p.value else ctypes.c_void_p(16)
-
-
-def _buffer(t, name: str):
     import torch
-    return _dev_tensor(t, torch.uint8, 0, name), t.numel()
+    _on(t, dev, name)
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
+    if t.numel() < numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with at least {numel} elements")
+    return t.data_ptr() or 16
+
+
+def _buffer(t, dev: int, name: str):
+    """A uint8 device tensor (checkpoint or workspace), or None."""
+    if t is None:
+        return None, 0
+    import torch
+    _on(t, dev, name)
+    if t.dtype is not torch.uint8:
+        raise TypeError(f"{name} must be {torch.uint8}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), t.numel()
 
 
 def lags_ckpt_bytes(rows: int, cols: int) -> int:
@@ -472,17 +510,19 @@ def checkpoint(rows: int, cols: int, device=None):
 
 def lags_ckpt_pack(x, ckpt, stream=None):
     """Pack x (channels last) into ckpt."""
-    p, rows, cols, ld = _matrix(x, "x")
-    c, nb = _buffer(ckpt, "ckpt")
-    rc = lib().lags_ckpt_pack(rows, cols, p, ld, _dtype_code(x.dtype), c, nb, _stream_handle(stream))
+    dev, s = _place(x, "x", stream)
+    p, rows, cols, ld = _matrix(x, dev, "x")
+    c, nb = _buffer(ckpt, dev, "ckpt")
+    rc = lib().lags_ckpt_pack(rows, cols, p, ld, _dtype_code(x.dtype), c, nb, s)
     _check("lags_ckpt_pack", rc)
 
 
 def lags_ckpt_unpack(ckpt, x, stream=None):
     """The values ckpt holds, into x (channels last, of the shape that was packed)."""
-    p, rows, cols, ld = _matrix(x, "x")
-    c, nb = _buffer(ckpt, "ckpt")
-    rc = lib().lags_ckpt_unpack(rows, cols, c, nb, p, ld, _dtype_code(x.dtype), _stream_handle(stream))
+    dev, s = _place(x, "x", stream)
+    p, rows, cols, ld = _matrix(x, dev, "x")
+    c, nb = _buffer(ckpt, dev, "ckpt")
+    rc = lib().lags_ckpt_unpack(rows, cols, c, nb, p, ld, _dtype_code(x.dtype), s)
     _check("lags_ckpt_unpack", rc)
 
 
@@ -497,13 +537,12 @@ class GroupNorm:
         self.dtype = dtype if dtype is not None else torch.float32
         self.shape = GnShape(int(samples), int(spatial), int(channels), int(groups),
                              _dtype_code(self.dtype), ACTS[act], float(eps))
-
-    @property
-    def rows(self) -> int:
-        return int(self.shape.samples) * int(self.shape.spatial)
+        self.ref = ctypes.byref(self.shape)
+        self.rows, self.channels = int(samples) * int(spatial), int(channels)
+        self.stats = int(samples) * int(groups)
 
     def workspace_bytes(self) -> int:
-        return int(lib().lags_gn_workspace_bytes(ctypes.byref(self.shape)))
+        return int(lib().lags_gn_workspace_bytes(self.ref))
 
 
 def gn_workspace(gn: GroupNorm, device=None):
@@ -518,34 +557,35 @@ def gn_workspace(gn: GroupNorm, device=None):
 def lags_gn_forward(gn: GroupNorm, x, gamma, beta, y, mean, rstd, ws, ckpt=None, stream=None):
     """y = act(groupnorm(x)); mean, rstd [samples, groups] (or None); ckpt: a checkpoint buffer that
     receives x in the same pass."""
-    s = gn.shape
-    px, _, _, ldx = _matrix(x, "x", gn.dtype, gn.rows, s.channels)
-    py, _, _, ldy = _matrix(y, "y", gn.dtype, gn.rows, s.channels)
-    w, nw = _buffer(ws, "ws")
-    c, nc = _buffer(ckpt, "ckpt") if ckpt is not None else (None, 0)
+    dev, s = _place(x, "x", stream)
+    c = gn.channels
+    px, _, _, ldx = _matrix(x, dev, "x", gn.dtype, gn.rows, c)
+    py, _, _, ldy = _matrix(y, dev, "y", gn.dtype, gn.rows, c)
+    pw, nw = _buffer(ws, dev, "ws")
+    pc, nc = _buffer(ckpt, dev, "ckpt")
     rc = lib().lags_gn_forward(
-        ctypes.byref(s), px, ldx, _vector(gamma, s.channels, "gamma"), _vector(beta, s.channels, "beta"),
-        py, ldy, _vector(mean, s.samples * s.groups, "mean"), _vector(rstd, s.samples * s.groups, "rstd"),
-        c, nc, w, nw, _stream_handle(stream))
+        gn.ref, px, ldx, _vector(gamma, dev, c, "gamma"), _vector(beta, dev, c, "beta"), py, ldy,
+        _vector(mean, dev, gn.stats, "mean"), _vector(rstd, dev, gn.stats, "rstd"), pc, nc, pw, nw, s)
     _check("lags_gn_forward", rc)
 
 
 def lags_gn_backward(gn: GroupNorm, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta, ws, x=None,
                      ckpt=None, add: bool = False, stream=None):
     """dx, and dgamma and dbeta (each may be None), from dy and the forward's x or its checkpoint."""
-    s = gn.shape
-    pdy, _, _, lddy = _matrix(dy, "dy", gn.dtype, gn.rows, s.channels)
-    pdx, _, _, lddx = _matrix(dx, "dx", gn.dtype, gn.rows, s.channels)
+    dev, s = _place(dy, "dy", stream)
+    c = gn.channels
+    pdy, _, _, lddy = _matrix(dy, dev, "dy", gn.dtype, gn.rows, c)
+    pdx, _, _, lddx = _matrix(dx, dev, "dx", gn.dtype, gn.rows, c)
     px, ldx = None, 0
     if x is not None:
-        px, _, _, ldx = _matrix(x, "x", gn.dtype, gn.rows, s.channels)
-    w, nw = _buffer(ws, "ws")
-    c, nc = _buffer(ckpt, "ckpt") if ckpt is not None else (None, 0)
+        px, _, _, ldx = _matrix(x, dev, "x", gn.dtype, gn.rows, c)
+    pw, nw = _buffer(ws, dev, "ws")
+    pc, nc = _buffer(ckpt, dev, "ckpt")
     rc = lib().lags_gn_backward(
-        ctypes.byref(s), pdy, lddy, px, ldx, c, nc, _vector(gamma, s.channels, "gamma"),
-        _vector(beta, s.channels, "beta"), _vector(mean, s.samples * s.groups, "mean"),
-        _vector(rstd, s.samples * s.groups, "rstd"), pdx, lddx, _vector(dgamma, s.channels, "dgamma"),
-        _vector(dbeta, s.channels, "dbeta"), LAGS_GRAD_ADD if add else 0, w, nw, _stream_handle(stream))
+        gn.ref, pdy, lddy, px, ldx, pc, nc, _vector(gamma, dev, c, "gamma"),
+        _vector(beta, dev, c, "beta"), _vector(mean, dev, gn.stats, "mean"),
+        _vector(rstd, dev, gn.stats, "rstd"), pdx, lddx, _vector(dgamma, dev, c, "dgamma"),
+        _vector(dbeta, dev, c, "dbeta"), LAGS_GRAD_ADD if add else 0, pw, nw, s)
     _check("lags_gn_backward", rc)
 
 
@@ -561,13 +601,13 @@ def wgrad_workspace(rows: int, outs: int, cols: int, dtype, device=None):
 def lags_ckpt_wgrad(dy, ckpt, dw, ws, add: bool = False, stream=None):
     """dw [outs, cols] (fp32, contiguous: a layer's slice of the flat gradient) = dy^T X, X the
     [rows, cols] matrix whose checkpoint is ckpt."""
-    import torch
-    pdy, rows, outs, lddy = _matrix(dy, "dy")
-    if not isinstance(dw, torch.Tensor) or dw.dim() != 2 or dw.shape[0] != outs:
+    dev, s = _place(dy, "dy", stream)
+    pdy, rows, outs, lddy = _matrix(dy, dev, "dy")
+    _on(dw, dev, "dw")
+    if dw.dim() != 2 or dw.shape[0] != outs:
         raise ValueError(f"dw must be a [{outs}, cols] tensor")
-    w, nw = _buffer(ws, "ws")
-    c, nc = _buffer(ckpt, "ckpt")
-    rc = lib().lags_ckpt_wgrad(rows, outs, dw.shape[1], pdy, lddy, _dtype_code(dy.dtype), c, nc,
-                               _dev_tensor(dw, torch.float32, dw.numel(), "dw"),
-                               LAGS_GRAD_ADD if add else 0, w, nw, _stream_handle(stream))
+    pw, nw = _buffer(ws, dev, "ws")
+    pc, nc = _buffer(ckpt, dev, "ckpt")
+    rc = lib().lags_ckpt_wgrad(rows, outs, dw.shape[1], pdy, lddy, _dtype_code(dy.dtype), pc, nc,
+                               _vector(dw, dev, 0, "dw"), LAGS_GRAD_ADD if add else 0, pw, nw, s)
     _check("lags_ckpt_wgrad", rc)

@@ -13,50 +13,47 @@ TINY = {"f32": 0.0, "bf16": 0.0, "f16": 2.0 ** -24}            # fp16's subnorma
 RUN = 32
 
 
+def quantise(x):
+    """Codes [rows, cols] and exponents [rows, runs] of a float64 array; a run that is not finite has
+    codes 0 and exponent 128 (scale byte 255)."""
+    rows, cols = x.shape
+    nrun = -(-cols // RUN)
+    v = np.zeros((rows, nrun * RUN))
+    v[:, :cols] = x
+    v = v.reshape(rows, nrun, RUN)
+    bad = ~np.isfinite(v).all(axis=2)
+    v = np.where(bad[:, :, None], 0.0, v)
+    top = np.abs(v).max(axis=2)
+    p = np.full(top.shape, -126)
+    some = top > 0
+    p[some] = np.maximum(-126, np.floor(np.log2(top[some])).astype(int) - 8)
+    while True:                                # the smallest exponent that keeps every code within 127
+        over = np.abs(np.rint(np.ldexp(top, -p))) > 127
+        if not over.any():
+            break
+        p[over] += 1
+    q = np.rint(np.ldexp(v, -p[:, :, None])).reshape(rows, nrun * RUN)[:, :cols]
+    return q, np.where(bad, 128, p)
+
+
 def held(x):
     """What the 8-bit format holds of a float64 [rows, cols] array (NaN runs where not finite)."""
-    out = np.empty_like(x)
-    for lo in range(0, x.shape[1], RUN):
-        v = x[:, lo:lo + RUN]
-        for r in range(x.shape[0]):
-            row = v[r]
-            if not np.isfinite(row).all():
-                out[r, lo:lo + RUN] = np.nan
-                continue
-            p = -126
-            top = np.abs(row).max()
-            if top > 0:
-                p = max(-126, int(np.floor(np.log2(top))) - 8)
-                while np.abs(np.rint(np.ldexp(row, -p))).max() > 127:
-                    p += 1
-            out[r, lo:lo + RUN] = np.ldexp(np.rint(np.ldexp(row, -p)), p)
-    return out
+    q, p = quantise(x)
+    e = np.repeat(p, RUN, axis=1)[:, :x.shape[1]]
+    return np.where(e == 128, np.nan, np.ldexp(q, np.where(e == 128, 0, e)))
 
 
 def codes(x):
-    """The checkpoint buffer (uint8) of a float64 [rows, cols] array."""
+    """The checkpoint buffer (uint8) of a float64 [rows, cols] array, and its bytes in use."""
     rows, cols = x.shape
     pitch, nrun = -(-cols // 16) * 16, -(-cols // RUN)
-    q = np.zeros((rows, pitch), np.int8)
-    s = np.zeros((rows, nrun), np.uint8)
-    for r in range(rows):
-        for b in range(nrun):
-            v = x[r, b * RUN:(b + 1) * RUN]
-            if not np.isfinite(v).all():
-                s[r, b] = 255
-                continue
-            p = -126
-            top = np.abs(v).max()
-            if top > 0:
-                p = max(-126, int(np.floor(np.log2(top))) - 8)
-                while np.abs(np.rint(np.ldexp(v, -p))).max() > 127:
-                    p += 1
-            q[r, b * RUN:b * RUN + v.size] = np.rint(np.ldexp(v, -p))
-            s[r, b] = p + 127
+    q, p = quantise(x)
+    padded = np.zeros((rows, pitch), np.int8)
+    padded[:, :cols] = q
     n = rows * (pitch + nrun)
     buf = np.zeros(-(-n // 16) * 16, np.uint8)
-    buf[:rows * pitch] = q.view(np.uint8).reshape(-1)
-    buf[rows * pitch:n] = s.reshape(-1)
+    buf[:rows * pitch] = padded.view(np.uint8).reshape(-1)
+    buf[rows * pitch:n] = (p + 127).astype(np.uint8).reshape(-1)
     return buf, n
 
 

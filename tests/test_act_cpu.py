@@ -49,6 +49,7 @@ BAD_SHAPES = [(dict(g=7), EINVAL), (dict(g=0), EINVAL), (dict(c=0), EINVAL), (di
               (dict(s=-1), EINVAL), (dict(dtype=9), EINVAL), (dict(act=3), EINVAL), (dict(act=-1), EINVAL),
               (dict(eps=-1.0), EINVAL), (dict(eps=float("nan")), EINVAL), (dict(eps=float("inf")), EINVAL),
               (dict(n=1 << 31), ERANGE), (dict(s=1 << 31), ERANGE), (dict(c=1 << 31, g=1), ERANGE),
+              (dict(c=(1 << 18) + 2, g=(1 << 18) + 2), ERANGE),
               (dict(c=5000, g=1), ERANGE),                    # one group of more than 4096 channels
               (dict(c=301 * 20, g=20), ERANGE),               # 301 channels a group, runs of 32: 9632 > 4096
               (dict(n=(1 << 31) - 1, s=(1 << 31) - 1, c=4096, g=4096), ERANGE)]
@@ -61,7 +62,7 @@ def test_group_norm_workspace():
     for kw, _ in BAD_SHAPES:
         assert L.lags_gn_workspace_bytes(ctypes.byref(_gn(**kw))) == 0, kw
     # wide shapes that are supported: many groups, and one group of the most channels
-    for kw in (dict(c=8192, g=32), dict(c=4096, g=1), dict(c=1 << 20, g=1 << 20), dict(n=0), dict(s=0)):
+    for kw in (dict(c=8192, g=32), dict(c=4096, g=1), dict(c=1 << 18, g=1 << 18), dict(n=0), dict(s=0)):
         assert L.lags_gn_workspace_bytes(ctypes.byref(_gn(**kw))) >= 16, kw
     # the workspace stays far below the data it serves
     big = L.lags_gn_workspace_bytes(ctypes.byref(_gn(n=64, s=12544, c=64, g=32)))
@@ -80,9 +81,10 @@ def test_group_norm_forward_refusals():
                                  ck, ckn, ws, wsn, None)
     assert call(g=None) == EINVAL
     for kw, rc in BAD_SHAPES:
-        assert call(g=_gn(**kw), ldx=1 << 32, ldy=1 << 32) == rc, kw
+        assert call(g=_gn(**kw), ldx=1 << 18, ldy=1 << 18) == rc, kw
     assert call(x=None) == EINVAL and call(y=None) == EINVAL and call(ldx=63) == EINVAL and call(ldy=0) == EINVAL
     assert call(x=P(0) + 1) == EINVAL
+    assert call(ldx=(1 << 18) + 1) == ERANGE and call(ldy=(1 << 18) + 1) == ERANGE
     assert call(gamma=None) == EINVAL and call(beta=None) == EINVAL        # both or neither
     assert call(gamma=P(1) + 2) == EINVAL and call(mean=P(4) + 1) == EINVAL
     assert call(ws=None) == EWS and call(ws=P(6) + 4) == EWS and call(wsn=need - 1) == EWS
@@ -109,11 +111,13 @@ def test_group_norm_backward_refusals():
                                   mean, rstd, dx, lddx, dg, db, flags, ws, wsn, None)
     assert call(g=None) == EINVAL
     for kw, rc in BAD_SHAPES:
-        assert call(g=_gn(**kw), lddy=1 << 32, ldx=1 << 32, lddx=1 << 32) == rc, kw
+        assert call(g=_gn(**kw), lddy=1 << 18, ldx=1 << 18, lddx=1 << 18) == rc, kw
     assert call(flags=2) == EINVAL
     assert call(x=None) == EINVAL and call(ck=P(10), ckn=cb) == EINVAL     # one source, not none or two
     assert call(x=None, ck=P(10), ckn=cb - 1) == EWS and call(x=None, ck=P(10) + 4, ckn=cb) == EWS
     assert call(dy=None) == EINVAL and call(dx=None) == EINVAL and call(lddy=1) == EINVAL and call(lddx=1) == EINVAL
+    for k in ("lddy", "ldx", "lddx"):
+        assert call(**{k: (1 << 18) + 1}) == ERANGE, k
     assert call(ldx=63) == EINVAL and call(mean=None) == EINVAL and call(rstd=None) == EINVAL
     assert call(gamma=None) == EINVAL and call(dg=P(7) + 2) == EINVAL
     assert call(ws=None) == EWS and call(wsn=need - 1) == EWS and call(ws=P(9) + 8) == EWS

@@ -96,7 +96,9 @@ SHAPES = [
     (130, 1, 64, 32), (300, 2, 24, 4),
     # a workgroup's rows by the dozen; chunked forms; ragged ends
     (64, 600, 64, 8), (1, 3000, 32, 4), (2, 1500, 48, 6), (1, 1025, 160, 5), (1, 513, 512, 2), (2, 257, 2048, 1),
-    (1, 20000, 8, 2), (9, 1551, 36, 3),
+    (1, 20000, 8, 2), (9, 1551, 36, 3), (1, 200000, 8, 2),
+    # resident workgroups of 8 and 13 rows a thread; several samples a workgroup
+    (130, 420, 32, 4), (256, 200, 64, 32), (128, 830, 32, 2), (4200, 3, 32, 4), (600, 20, 256, 8),
 ]
 
 
