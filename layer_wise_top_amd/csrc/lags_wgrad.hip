@@ -336,7 +336,8 @@ WgradPlan wgrad_plan(int dtype, int64_t M, int64_t O, int64_t C)
             if (p.split < 1) p.split = 1;
             const double n = std::ceil(tiles * p.split / 256);
             const double rows = (double)(p.split > 1 ? per : M);
-            double ns = std::fmax(rows * std::fmax(n * kTiles[t].full[terms], kTiles[t].alone[terms]), in);
+            const double uneven = tiles * p.split > 256 ? n * 256 / (tiles * p.split) : 1;
+            double ns = std::fmax(rows * std::fmax(n * kTiles[t].full[terms], kTiles[t].alone[terms]), in * uneven);
             ns += p.split > 1 ? 3500 + out * (2 * p.split + 1) / 7500 : out / 5000;
             if (!least || ns < least) least = ns, best = p;
             if (want > 1 && (per == 64 || tiles * want > 4096)) break;
