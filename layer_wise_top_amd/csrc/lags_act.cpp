@@ -71,16 +71,16 @@ GnPlan gn_plan(int dtype, int act, bool backward, bool split, uint64_t N, uint64
         }
     }
     if (!p.resident) {
-        // whole rows of up to 256 bytes: 64 x 3136 x 256 backward 94 us (64 bytes: 97, 1024: 99)
-        slab(256);
+        // 64 channels: 64 x 3136 x 256 backward 92 us (32: 97, 128: 95, 512: 99)
+        slab(64 * E);
         p.threads = 1u << p.tcl;
         if (p.threads < 512) p.threads = 512;
-        // chunks: about 2048 workgroups (1024: 95 us, 4096: 96 us), whole sweeps each
-        const uint64_t sweep = (uint64_t)(p.threads >> p.tcl) * kSweep;
-        uint64_t want = 2048 / (N * p.nslab);
+        // chunks: about 1024 workgroups (256 to 4096 differ by 3 %)
+        const uint64_t rows = p.threads >> p.tcl;
+        uint64_t want = 1024 / (N * p.nslab);
         if (want < 1) want = 1;
         uint64_t chunk = (S + want - 1) / want;
-        chunk = (chunk + sweep - 1) / sweep * sweep;
+        chunk = (chunk + rows - 1) / rows * rows;
         if (chunk > S) chunk = S;
         p.chunk = (uint32_t)chunk;
         p.nchunk = (uint32_t)((S + chunk - 1) / chunk);
@@ -308,6 +308,10 @@ int lags_gn_forward(const lags_gn *gn, const void *x, int64_t ldx, const float *
     a.x = x, a.ldx = ldx, a.y = y, a.ldy = ldy;
     a.gamma = gamma, a.beta = beta, a.mean = mean, a.rstd = rstd;
     if (ckpt) a.wcodes = (uint8_t *)ckpt, a.wscales = (uint8_t *)ckpt + (size_t)c.rows * a.pitch;
+    // A large y is stored past the caches: it would not stay there until it is read, and drives out x,
+    // which a split forward reads twice.  With the operation before and after it in the loop: 103 MB 118
+    // -> 107 us, 206 MB 219 -> 216, 51 MB 56.5 -> 57.7 (and no gain at any size for the backward's dx).
+    a.past = (u128)c.rows * gn->channels * elem_bytes(gn->dtype) > ((u128)64 << 20);
     a.part = (float *)ws;
     return hip(launch_gn_forward(p, a, gn->dtype, (hipStream_t)stream));
 }

@@ -54,6 +54,7 @@ struct GnArgs {
     float eps, inv_cg;
     int act;
     uint32_t add;                    // dgamma, dbeta are added to
+    uint32_t past;                   // y is stored past the caches
     uint32_t N, S, C, G, cg;         // samples, positions, channels, groups, channels per group
     uint32_t pitch, nrun;
     // geometry: a workgroup takes `w` channels (whole groups, whole runs) of
@@ -334,12 +335,16 @@ __device__ inline float run_step(uint32_t s) { return asf(s << 23); }
 // through a window that ends with the last row, so rows past it are dropped
 // by the hardware; the last vector of a row of odd length, and rows that
 // start inside a word (ODD), are stored piece by piece.
+// `past`: whole vectors are stored past the caches.
 template <int D, bool ODD> struct Writer {
     __amdgpu_buffer_rsrc_t r;
     char *p;
     uint32_t at, pitch, rows;
     int nv;
-    __device__ Writer(void *base, int64_t row0, uint32_t n, int64_t ld, uint32_t c0, uint32_t w, uint32_t col)
+    bool past;
+    __device__ Writer(void *base, int64_t row0, uint32_t n, int64_t ld, uint32_t c0, uint32_t w, uint32_t col,
+                      bool past_caches = false)
+        : past(past_caches)
     {
         constexpr int V = Elem<D>::V, E = Elem<D>::E;
         p = (char *)base + (row0 * ld + c0) * E;
@@ -352,7 +357,10 @@ template <int D, bool ODD> struct Writer {
         constexpr int V = Elem<D>::V;
         const uint32_t o = at + row * pitch;
         if constexpr (!ODD) {
-            __builtin_amdgcn_raw_buffer_store_b128(v, r, nv >= V ? o : 0x80000000u, 0, 0);
+            if (past)
+                __builtin_amdgcn_raw_buffer_store_b128(v, r, nv >= V ? o : 0x80000000u, 0, 2);
+            else
+                __builtin_amdgcn_raw_buffer_store_b128(v, r, nv >= V ? o : 0x80000000u, 0, 0);
             if (nv > 0 && nv < V && row < rows) store_vec<D>(p + o, v, nv);
         } else {
             if (row < rows) store_vec<D>(p + o, v, nv);

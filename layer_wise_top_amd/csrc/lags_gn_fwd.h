@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kResident) void k_gn_fwd(GnArgs a)
     });
     __syncthreads();
     nm.rs.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return gs[g.ng + i]; });
-    const Writer<D, ODD> wy(a.y, row0, a.S, a.ldy, g.c0, g.wc, g.col);
+    const Writer<D, ODD> wy(a.y, row0, a.S, a.ldy, g.c0, g.wc, g.col, a.past);
     const CodeWriter<D> wq(a.wcodes, a.wscales, row0, a.S, a.pitch, a.nrun, a.C, g.c0, g.wc, g.col);
     float last = nm.rs[0];
 #pragma unroll
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(1024) void k_gn_apply(GnArgs a)
     for (uint32_t s0 = 0; s0 < rows; s0 += U * g.tr) {
         const int64_t r0 = (int64_t)g.n * a.S + lo + s0;
         const Reader<D, ODD> rx(a.x, r0, rows - s0, a.ldx, g.c0, g.wc, g.col);
-        const Writer<D, ODD> wy(a.y, r0, rows - s0, a.ldy, g.c0, g.wc, g.col);
+        const Writer<D, ODD> wy(a.y, r0, rows - s0, a.ldy, g.c0, g.wc, g.col, a.past);
         const CodeWriter<D> wq(a.wcodes, a.wscales, r0, rows - s0, a.pitch, a.nrun, a.C, g.c0, g.wc, g.col);
         u32x4 raw[U];
 #pragma unroll

@@ -109,6 +109,24 @@ def test_shapes(n, s, c, groups, dtype, act):
     Case(n, s, c, groups, dtype, act, seed=n + s + c).check_all()
 
 
+@pytest.mark.parametrize("n,s", [(600, 784), (40, 12544)])
+def test_large_outputs(n, s):
+    """Outputs above 64 MB, whose stores pass the caches, resident and split: some samples in full."""
+    import torch
+    from layer_wise_top_amd import lags
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(n, s, 96, generator=g, device="cuda").bfloat16()
+    gamma, beta = torch.randn(96, generator=g, device="cuda"), torch.randn(96, generator=g, device="cuda")
+    gn = lags.GroupNorm(n, s, 96, 12, dtype=x.dtype, act="relu", eps=EPS)
+    y, mean, rstd = torch.full_like(x, 9.0), torch.empty(n, 12, device="cuda"), torch.empty(n, 12, device="cuda")
+    lags.lags_gn_forward(gn, x, gamma, beta, y, mean, rstd, lags.gn_workspace(gn))
+    for i in (0, 1, n // 2, n - 1):
+        want, err = R.forward(x[i:i + 1].double().cpu().numpy(), gamma.double().cpu().numpy(),
+                              beta.double().cpu().numpy(), 12, EPS, "relu")
+        for name, got, w, e in zip(("y", "mean", "rstd"), (y, mean, rstd), want, err):
+            R.check(f"{name} {i}", got[i:i + 1].double().cpu().numpy(), w, e, "bf16" if name == "y" else "f32")
+
+
 @pytest.mark.parametrize("n,s", [(2, 100), (1, 6000)])
 def test_no_affine(n, s):
     Case(n, s, 64, 8, "f32", "silu", affine=False).check_all()
