@@ -145,7 +145,7 @@ __global__ __launch_bounds__(64 * WR * WC) void k_wgrad(WgradArgs a)
         px += (int64_t)K * a.pitch, lx -= (int64_t)K * a.pitch;
         ps += (int64_t)K * a.nrun, ls -= (int64_t)K * a.nrun;
     };
-    auto stage = [&](char *buf) {
+    auto stage_dy = [&](char *buf) {
 #pragma unroll
         for (int p = 0; p < PA; ++p) {
             const int id = t + p * kThreads;
@@ -166,6 +166,8 @@ __global__ __launch_bounds__(64 * WR * WC) void k_wgrad(WgradArgs a)
                     *(u32x2 *)q = u32x2{w[k][0], w[k][1]};
             }
         }
+    };
+    auto stage_x = [&](char *buf) {
         if (RX <= K || xr < K) {
 #pragma unroll
             for (int p = 0; p < PX; ++p) {
@@ -203,18 +205,29 @@ __global__ __launch_bounds__(64 * WR * WC) void k_wgrad(WgradArgs a)
     };
     int cur = 0;
     load();
-    stage(lds);
+    stage_dy(lds);
+    stage_x(lds);
     load();
     for (int64_t step = lo; step < hi; step += K) {
         __syncthreads();
         const char *buf = lds + cur * BUF;
         cur ^= 1;
+        // The next step's tiles, loaded while the last step ran, are staged between this one's products.
+        // The fences keep the pieces apart: left alone the compiler gathers the LDS reads and the loads
+        // at the end, where the matrix unit waits for them (8192 x 2048 over 16384 rows: 505 us; so 490).
         multiply(buf, 0);
-        stage(lds + cur * BUF);          // loaded while the last step ran
+        stage_dy(lds + cur * BUF);
+        if constexpr (K >= 64) {
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(buf, 16);
+        }
+        stage_x(lds + cur * BUF);
         load();
-        __builtin_amdgcn_sched_barrier(0);   // not later: they have this step's products to arrive in
 #pragma unroll
-        for (int k = 16; k < K; k += 16) multiply(buf, k);
+        for (int k = K >= 64 ? 32 : 16; k < K; k += 16) {
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(buf, k);
+        }
     }
 
     float *out = a.split > 1 ? a.part + (size_t)slice * a.O * a.C : a.dw;

@@ -428,10 +428,13 @@ def _place(first, name: str, stream):
 
 def _on(t, dev: int, name: str):
     """t must be a tensor on device `dev`."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a device tensor")
-    if t.get_device() != dev:
+    try:
+        at = t.get_device()             # -1: host memory
+    except AttributeError:
+        at = -1
+    if at != dev:
+        if at < 0:
+            raise TypeError(f"{name} must be a device tensor")
         raise ValueError(f"{name} is on {t.device}, not on the current device")
 
 
