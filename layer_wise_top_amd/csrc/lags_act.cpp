@@ -63,9 +63,13 @@ GnPlan gn_plan(int dtype, int act, bool backward, bool split, uint64_t N, uint64
             while (p.threads < 256 && (uint64_t)p.threads * 2 < vecs) p.threads *= 2;
             while (p.threads < most && (uint64_t)p.threads * rows < vecs) p.threads *= 2;
             p.rows = (uint32_t)((vecs + p.threads - 1) / p.threads);
-            // backward: several samples a workgroup where there are far more than fill the GPU
+            // backward: several samples a workgroup where there are far more than fill the GPU, or
+            // where their channel sums, eight bytes a channel, would be more than the samples
+            // themselves (8192 x 1 x 2048, one group: their sum takes 26 us for 8192 rows, 8 for 1024)
             uint64_t nper = 1;
-            while (backward && N * p.nslab / nper > 4096 && nper < N) nper *= 2;
+            while (backward && nper < N &&
+                   (N * p.nslab / nper > 4096 || (N * p.nslab / nper > 1024 && S * nper < 32)))
+                nper *= 2;
             p.nper = (uint32_t)nper;
             p.nparts = (uint32_t)((N + nper - 1) / nper);
         }

@@ -103,6 +103,13 @@ struct WgradPlan {
 WgradPlan wgrad_plan(int dtype, int64_t M, int64_t O, int64_t C);
 hipError_t launch_wgrad(const WgradPlan &p, WgradArgs a, int dtype, hipStream_t s);
 
+// Dynamic LDS above 64 KiB has to be asked for.
+inline hipError_t allow_lds(const void *kernel, size_t bytes)
+{
+    if (bytes <= 65536) return hipSuccess;
+    return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 #if defined(__HIPCC__)
 // ---- device side: 16-byte vectors of any element type ----------------------
 // Global vectors are only element-aligned: rows of odd pitch and slices start

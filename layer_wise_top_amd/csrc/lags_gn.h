@@ -140,6 +140,7 @@ __device__ inline void to_groups(const Geo &g, const float *sh, uint32_t cg, flo
         const uint32_t gi = g0 + (threadIdx.x >> lgl);
         float s = 0;
         if (gi < g.ng)
+#pragma unroll 4
             for (uint32_t i = sub; i < items; i += lg) {
                 const uint32_t p = over_cg(i, inv_cg), c = gi * cg + i - p * cg;
                 s += weight ? sh[p * wp + c] * weight[c] : sh[p * wp + c];
@@ -153,6 +154,35 @@ __device__ inline void to_groups(const Geo &g, const float *sh, uint32_t cg, flo
         if (gi < g.ng && sub == 0) done(gi, s);
     }
 }
+
+// Sums of a thread's channels for their groups.  UNI: the thread's vector lies
+// in one group, so its channels are added up first and a lane carries one
+// value; else one a channel.
+template <int V, bool UNI> struct GroupSum {
+    static constexpr int N = UNI ? 1 : V;
+    float v[N];
+    __device__ GroupSum(const float (&s)[V])
+    {
+        if constexpr (UNI) {
+            float t[V];
+            for (int j = 0; j < V; ++j) t[j] = s[j];
+#pragma unroll
+            for (int h = V / 2; h; h >>= 1)
+                for (int j = 0; j < h; ++j) t[j] += t[j + h];
+            v[0] = t[0];
+        } else {
+            for (int j = 0; j < V; ++j) v[j] = s[j];
+        }
+    }
+    __device__ void parts(const Geo &g, float *sh) { to_parts<N>(v, g, sh); }
+    template <typename F> __device__ static void groups(const Geo &g, const float *sh, const GnArgs &a, F done)
+    {
+        if constexpr (UNI)
+            to_groups<1>(g, sh, a.cg / V, a.inv_cg * V, done);
+        else
+            to_groups<V>(g, sh, a.cg, a.inv_cg, done);
+    }
+};
 
 // The sum over a wave, on every lane.
 __device__ inline float wave_sum(float s)
@@ -236,6 +266,12 @@ template <typename F> hipError_t by_rows(uint32_t rows, F f)
 template <int D> bool odd_rows(const void *p, int64_t ld)
 {
     return D != kF32 && p && (((uintptr_t)p | (uint64_t)ld * 2) & 3);
+}
+template <int D, typename F> hipError_t by_odd(bool odd, F f)
+{
+    if constexpr (D != kF32)
+        if (odd) return f(std::true_type());
+    return f(std::false_type());
 }
 // LDS of the sums: `arrays` of per-wave channel sums, and `per_group` floats a group.
 inline size_t lds_bytes(const GnPlan &p, uint32_t V, uint32_t cg, uint32_t arrays, uint32_t per_group,

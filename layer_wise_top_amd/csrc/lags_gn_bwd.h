@@ -151,32 +151,59 @@ __device__ inline float bwd_emit(const Writer<D, ODD> &w, const Stored<D, CK> &x
     return d[0];
 }
 
-// LDS of the joins: two arrays of parts, the group means, gamma, and (resident)
-// the channel sums of the samples so far.
+// LDS of the joins: two arrays of parts of the channel sums and two of the
+// group sums, the group means, and (resident) gamma and the channel sums of
+// the samples so far.
 struct Joins {
-    float *a, *b, *mean, *gamma, *total;
+    float *a, *b, *ga, *gb, *mean, *gamma, *total;
     __device__ Joins(float *sh, const Geo &g, uint32_t V)
     {
-        const uint32_t np = g.parts * (V << g.tcl);
-        a = sh, b = a + np, mean = b + np, gamma = mean + 2 * g.ng, total = gamma + g.wc;
+        const uint32_t nl = g.parts << g.tcl;
+        a = sh, b = a + nl * V, ga = b + nl * V, gb = ga + nl, mean = gb + nl;
+        gamma = mean + 2 * g.ng, total = gamma + g.wc;
     }
 };
 
 // rstd times the means of gamma dz and gamma dz xh over each channel's group,
-// from every thread's per-channel sums, which are used up; `total`: and their
-// sums over the samples, if the slab's threads keep them.
-template <int V, bool UNI>
-__device__ inline void group_means(const GnArgs &a, const Geo &g, const Joins &m, const PerGroup<V, UNI> &rs,
-                                   float (&sa)[V], float (&sb)[V], bool total, PerGroup<V, UNI> &s1,
-                                   PerGroup<V, UNI> &s2)
+// from every thread's per-channel sums, which are used up; TOTAL: and their
+// sums over the samples.  ONE (with UNI): the group sums are made of one value
+// a thread, not of the channels' sums.  That is less to add up where a group is
+// wide (8192 x 1 x 2048, one group: 92 us, else 161), but takes registers that
+// only the shortest samples leave (64 x 784 x 512 in 8 rows: 43 us, else 41).
+template <int V, bool UNI, bool TOTAL, bool ONE>
+__device__ inline void group_means(const GnArgs &a, const Geo &g, const Joins &m, const Chan<V, UNI> &ch,
+                                   float (&sa)[V], float (&sb)[V], PerGroup<V, UNI> &s1, PerGroup<V, UNI> &s2)
 {
-    to_parts<V>(sa, g, m.a);
-    to_parts<V>(sb, g, m.b);
-    __syncthreads();
     const float cnt = (float)((uint64_t)a.S * a.cg);
-    to_groups<V>(g, m.a, a.cg, a.inv_cg, [&](uint32_t i, float s) { m.mean[i] = s / cnt; }, m.gamma);
-    to_groups<V>(g, m.b, a.cg, a.inv_cg, [&](uint32_t i, float s) { m.mean[g.ng + i] = s / cnt; }, m.gamma);
-    if (total)
+    auto mean_a = [&](uint32_t i, float s) { m.mean[i] = s / cnt; };
+    auto mean_b = [&](uint32_t i, float s) { m.mean[g.ng + i] = s / cnt; };
+    if constexpr (TOTAL) {
+        if constexpr (ONE) {
+            float ta[V], tb[V];
+            for (int j = 0; j < V; ++j) ta[j] = sa[j] * ch.ga[j], tb[j] = sb[j] * ch.ga[j];
+            GroupSum<V, true>(ta).parts(g, m.ga);
+            GroupSum<V, true>(tb).parts(g, m.gb);
+        }
+        to_parts<V>(sa, g, m.a);
+        to_parts<V>(sb, g, m.b);
+        __syncthreads();
+        if constexpr (ONE) {
+            GroupSum<V, true>::groups(g, m.ga, a, mean_a);
+            GroupSum<V, true>::groups(g, m.gb, a, mean_b);
+        } else {
+            to_groups<V>(g, m.a, a.cg, a.inv_cg, mean_a, m.gamma);
+            to_groups<V>(g, m.b, a.cg, a.inv_cg, mean_b, m.gamma);
+        }
+    } else {
+        for (int j = 0; j < V; ++j) sa[j] *= ch.ga[j], sb[j] *= ch.ga[j];
+        GroupSum<V, UNI> ua(sa), ub(sb);
+        ua.parts(g, m.a);
+        ub.parts(g, m.b);
+        __syncthreads();
+        ua.groups(g, m.a, a, mean_a);
+        ub.groups(g, m.b, a, mean_b);
+    }
+    if constexpr (TOTAL)
         for (uint32_t i = threadIdx.x; i < g.wc; i += blockDim.x) {
             float u = 0, v = 0;
             for (uint32_t k = 0; k < g.parts; ++k) u += m.a[k * (V << g.tcl) + i], v += m.b[k * (V << g.tcl) + i];
@@ -185,12 +212,7 @@ __device__ inline void group_means(const GnArgs &a, const Geo &g, const Joins &m
     __syncthreads();
     s1.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return m.mean[i]; });
     s2.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return m.mean[g.ng + i]; });
-    for (int j = 0; j < (UNI ? 1 : V); ++j) s1.v[j] *= rs[j], s2.v[j] *= rs[j];
-}
-
-__device__ inline void load_gamma(const GnArgs &a, const Geo &g, const Joins &m)
-{
-    for (uint32_t i = threadIdx.x; i < g.wc; i += blockDim.x) m.gamma[i] = a.gamma ? a.gamma[g.c0 + i] : 1.0f;
+    for (int j = 0; j < (UNI ? 1 : V); ++j) s1.v[j] *= ch.rs[j], s2.v[j] *= ch.rs[j];
 }
 
 // The workgroup's per-channel sums, to p[0..C) (sum dz) and p[C..2C) (sum dz xh).
@@ -223,9 +245,10 @@ __global__ __launch_bounds__(kResidentBwd, bwd_waves(R, UNI)) void k_gn_bwd(GnAr
     load_param<V>(a.gamma, g, 1.0f, ch.ga);
     load_param<V>(a.beta, g, 0.0f, ch.be);
     const Joins joins(sh, g, V);
-    load_gamma(a, g, joins);
-    for (uint32_t i = threadIdx.x; i < 2 * g.wc; i += blockDim.x) joins.total[i] = 0;
-    __syncthreads();                     // the totals' threads are others here
+    for (uint32_t i = threadIdx.x; i < g.wc; i += blockDim.x) {
+        joins.total[i] = joins.total[g.wc + i] = 0;
+        joins.gamma[i] = a.gamma ? a.gamma[g.c0 + i] : 1.0f;    // read after the sums' barrier
+    }
     for (g.n = p * a.nper; g.n < n_hi; ++g.n) {
         const int64_t row0 = (int64_t)g.n * a.S;
         uint32_t first = g.row;          // made anew, or every vector's offsets are kept from sample to sample
@@ -249,7 +272,7 @@ __global__ __launch_bounds__(kResidentBwd, bwd_waves(R, UNI)) void k_gn_bwd(GnAr
             bwd_sums<D, ACT, CK, UNI>(x[k], dy[k], ch, sa, sb);
         }
         PerGroup<V, UNI> s1, s2;
-        group_means<V, UNI>(a, g, joins, ch.rs, sa, sb, true, s1, s2);
+        group_means<V, UNI, true, UNI && R == 2>(a, g, joins, ch, sa, sb, s1, s2);
         const Writer<D, ODD> w(a.dx, row0, a.S, a.lddx, g.c0, g.wc, g.col);
         float last = s1[0];
 #pragma unroll
@@ -313,7 +336,6 @@ __global__ __launch_bounds__(1024) void k_gn_bwd_apply(GnArgs a)
     float sa[V], sb[V];
     for (int j = 0; j < V; ++j) sa[j] = sb[j] = 0;
     const Joins joins(sh, g, V);
-    load_gamma(a, g, joins);             // read after the sums' barrier
     for (uint32_t k = g.row; k < a.nchunk; k += g.tr) {
         const float *p = a.part + ((size_t)g.n * a.nchunk + k) * 2 * a.C;
         float u[V], v[V];
@@ -322,7 +344,7 @@ __global__ __launch_bounds__(1024) void k_gn_bwd_apply(GnArgs a)
         for (int j = 0; j < V; ++j) sa[j] += u[j], sb[j] += v[j];
     }
     PerGroup<V, UNI> s1, s2;
-    group_means<V, UNI>(a, g, joins, ch.rs, sa, sb, false, s1, s2);
+    group_means<V, UNI, false, false>(a, g, joins, ch, sa, sb, s1, s2);
     float last = s1[0];
     const uint32_t lo = g.chunk * a.chunk, rows = min(a.S - lo, a.chunk);
     for (uint32_t s0 = 0; s0 < rows; s0 += U * g.tr) {
@@ -351,14 +373,16 @@ __global__ __launch_bounds__(1024) void k_gn_bwd_apply(GnArgs a)
 template <int D> hipError_t launch_gn_backward(const GnPlan &p, const GnArgs &a, hipStream_t s)
 {
     constexpr uint32_t V = Elem<D>::V;
-    const size_t lds = lds_bytes(p, V, a.cg, 2, 2, 3);
+    const size_t lds = p.resident ? lds_bytes(p, V, a.cg, 3, 2, 3) : lds_bytes(p, V, a.cg, 3, 2);
     const bool odd = odd_rows<D>(a.x, a.ldx) || odd_rows<D>(a.dy, a.lddy) || odd_rows<D>(a.dx, a.lddx);
     return by_act(a.act, [&](auto A) {
         return by_bool(a.rcodes != nullptr, [&](auto K) {
             auto run = [&](auto O, auto U) {
                 if (p.resident)
                     return by_rows(p.rows, [&](auto R) {
-                        k_gn_bwd<D, A(), K(), R(), O(), U()><<<p.nparts * p.nslab, p.threads, lds, s>>>(a);
+                        const auto k = k_gn_bwd<D, A(), K(), R(), O(), U()>;
+                        if (hipError_t e = allow_lds((const void *)k, lds); e != hipSuccess) return e;
+                        k<<<p.nparts * p.nslab, p.threads, lds, s>>>(a);
                         return hipGetLastError();
                     });
                 const uint32_t grid = a.N * p.nchunk * p.nslab;
@@ -367,9 +391,7 @@ template <int D> hipError_t launch_gn_backward(const GnPlan &p, const GnArgs &a,
                 k_gn_bwd_apply<D, A(), K(), O(), U()><<<grid, p.threads, lds, s>>>(a);
                 return hipGetLastError();
             };
-            if constexpr (D != kF32)
-                if (odd) return run(std::true_type(), std::false_type());
-            return by_bool(a.cg % V == 0, [&](auto U) { return run(std::false_type(), U); });
+            return by_odd<D>(odd, [&](auto O) { return by_bool(a.cg % V == 0, [&](auto U) { return run(O, U); }); });
         });
     });
 }

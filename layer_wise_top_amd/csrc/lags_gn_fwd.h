@@ -76,9 +76,10 @@ __global__ __launch_bounds__(kResident) void k_gn_fwd(GnArgs a)
         for (int j = 0; j < V; ++j) acc[j] += f[j];
     }
     const float cnt = (float)((uint64_t)a.S * a.cg);
-    to_parts<V>(acc, g, sh);
+    GroupSum<V, UNI> sum(acc);
+    sum.parts(g, sh);
     __syncthreads();
-    to_groups<V>(g, sh, a.cg, a.inv_cg, [&](uint32_t i, float s) { gs[i] = s / cnt; });
+    sum.groups(g, sh, a, [&](uint32_t i, float s) { gs[i] = s / cnt; });
     __syncthreads();
     nm.mu.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return gs[i]; });
 #pragma unroll
@@ -95,9 +96,10 @@ __global__ __launch_bounds__(kResident) void k_gn_fwd(GnArgs a)
             }
         }
     }
-    to_parts<V>(acc, g, sh);
+    GroupSum<V, UNI> squares(acc);
+    squares.parts(g, sh);
     __syncthreads();
-    to_groups<V>(g, sh, a.cg, a.inv_cg, [&](uint32_t i, float s) {
+    squares.groups(g, sh, a, [&](uint32_t i, float s) {
         const float r = 1.0f / sqrtf(s / cnt + a.eps);
         gs[g.ng + i] = r;
         const int64_t at = (int64_t)g.n * a.G + over_cg(g.c0, a.inv_cg) + i;
@@ -122,7 +124,7 @@ __global__ __launch_bounds__(kResident) void k_gn_fwd(GnArgs a)
 // squares.  That value being one of the data, what its distance from the mean
 // costs in digits is bounded: a relative error of the thread's count of
 // positions times fp32's rounding.
-template <int D, bool ODD> __global__ __launch_bounds__(1024) void k_gn_stats(GnArgs a)
+template <int D, bool ODD, bool UNI> __global__ __launch_bounds__(1024) void k_gn_stats(GnArgs a)
 {
     constexpr int V = Elem<D>::V, U = kSweep;
     extern __shared__ float sh[];
@@ -161,19 +163,21 @@ template <int D, bool ODD> __global__ __launch_bounds__(1024) void k_gn_stats(Gn
         t[j] = cm * mean[j];
     }
     const float cnt = (float)((uint64_t)rows * a.cg);
-    to_parts<V>(t, g, sh);
+    GroupSum<V, UNI> sum(t);
+    sum.parts(g, sh);
     __syncthreads();
-    to_groups<V>(g, sh, a.cg, a.inv_cg, [&](uint32_t i, float s) { gs[i] = s / cnt; });
+    sum.groups(g, sh, a, [&](uint32_t i, float s) { gs[i] = s / cnt; });
     __syncthreads();
-    PerGroup<V, false> mu;
+    PerGroup<V, UNI> mu;
     mu.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return gs[i]; });
     for (int j = 0; j < V; ++j) {
         const float d = mean[j] - mu[j];
         s2[j] = mine ? __builtin_fmaf(cm * d, d, s2[j]) : 0.0f;
     }
-    to_parts<V>(s2, g, sh);
+    GroupSum<V, UNI> squares(s2);
+    squares.parts(g, sh);
     __syncthreads();
-    to_groups<V>(g, sh, a.cg, a.inv_cg, [&](uint32_t i, float s) {
+    squares.groups(g, sh, a, [&](uint32_t i, float s) {
         float *p = a.part + 2 * (((size_t)g.n * a.G + over_cg(g.c0, a.inv_cg) + i) * a.nchunk + g.chunk);
         p[0] = gs[i], p[1] = s;
     });
@@ -239,11 +243,13 @@ template <int D> hipError_t launch_gn_forward(const GnPlan &p, const GnArgs &a, 
     const bool odd = odd_rows<D>(a.x, a.ldx) || odd_rows<D>(a.y, a.ldy);
     const uint32_t grid = a.N * p.nchunk * p.nslab;
     if (!p.resident) {
-        if constexpr (D != kF32) {
-            if (odd) k_gn_stats<D, true><<<grid, p.threads, lds_bytes(p, V, a.cg, 1, 1), s>>>(a);
-        }
-        if (!odd) k_gn_stats<D, false><<<grid, p.threads, lds_bytes(p, V, a.cg, 1, 1), s>>>(a);
-        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        const hipError_t e = by_odd<D>(odd, [&](auto O) {
+            return by_bool(a.cg % V == 0, [&](auto U) {
+                k_gn_stats<D, O(), U()><<<grid, p.threads, lds_bytes(p, V, a.cg, 1, 1), s>>>(a);
+                return hipGetLastError();
+            });
+        });
+        if (e != hipSuccess) return e;
     }
     return by_act(a.act, [&](auto A) {
         return by_bool(a.wcodes != nullptr, [&](auto K) {
@@ -257,9 +263,7 @@ template <int D> hipError_t launch_gn_forward(const GnPlan &p, const GnArgs &a, 
                 k_gn_apply<D, A(), K(), O(), U()><<<grid, p.threads, lds_bytes(p, V, a.cg, 0, 2), s>>>(a);
                 return hipGetLastError();
             };
-            if constexpr (D != kF32)
-                if (odd) return run(std::true_type(), std::false_type());
-            return by_bool(a.cg % V == 0, [&](auto U) { return run(std::false_type(), U); });
+            return by_odd<D>(odd, [&](auto O) { return by_bool(a.cg % V == 0, [&](auto U) { return run(O, U); }); });
         });
     });
 }

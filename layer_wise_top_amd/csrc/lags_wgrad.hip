@@ -287,10 +287,7 @@ template <int D, int BO, int BC, int WR, int WC, int K> hipError_t run(const Wgr
     auto k = k_wgrad<D, BO, BC, WR, WC, K, false>;
     if constexpr (D != kF32)
         if (odd) k = k_wgrad<D, BO, BC, WR, WC, K, true>;
-    if (lds > 65536)
-        if (hipError_t e = hipFuncSetAttribute((const void *)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-            e != hipSuccess)
-            return e;
+    if (hipError_t e = allow_lds((const void *)k, lds); e != hipSuccess) return e;
     k<<<a.to * a.tc * a.split, 64 * WR * WC, lds, s>>>(a);
     return hipGetLastError();
 }

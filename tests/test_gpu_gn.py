@@ -109,6 +109,13 @@ def test_shapes(n, s, c, groups, dtype, act):
     Case(n, s, c, groups, dtype, act, seed=n + s + c).check_all()
 
 
+@pytest.mark.parametrize("dtype,act", [("f32", "silu"), ("bf16", "relu"), ("f16", "none")])
+@pytest.mark.parametrize("n,s,c,groups", [(2050, 1, 512, 1), (1501, 3, 320, 5), (1100, 2, 1000, 4), (2049, 1, 132, 11)])
+def test_many_short_samples(n, s, c, groups, dtype, act):
+    """One to three positions a sample: several samples a workgroup, the last workgroup with fewer."""
+    Case(n, s, c, groups, dtype, act, seed=n + c).check_all()
+
+
 @pytest.mark.parametrize("n,s", [(600, 784), (40, 12544)])
 def test_large_outputs(n, s):
     """Outputs above 64 MB, whose stores pass the caches, resident and split: some samples in full."""
