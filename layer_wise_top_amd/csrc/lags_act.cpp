@@ -12,6 +12,9 @@ static_assert(kF32 == LAGS_F32 && kBF16 == LAGS_BF16 && kF16 == LAGS_F16, "one n
 static_assert(kActNone == LAGS_ACT_NONE && kActRelu == LAGS_ACT_RELU && kActSilu == LAGS_ACT_SILU,
               "one numbering");
 static_assert(kRun == LAGS_CKPT_RUN && kSlabMax == LAGS_SLAB_MAX, "one size");
+// A resident workgroup reaches its rows by 32-bit offsets: its lanes span 32 columns at least (8 lanes
+// of fp32, 4 of 16-bit values), the others take kMostRows rows each, of LAGS_GN_MAX elements at most.
+static_assert((uint64_t)kResident * kMostRows / 2 * LAGS_GN_MAX < 0x7fffffffull, "32-bit offsets");
 
 namespace {
 uint32_t gcd(uint32_t a, uint32_t b) { return b ? gcd(b, a % b) : a; }
@@ -25,7 +28,7 @@ namespace lags {
 // whose own registers 8 rows would spill (51 us; 8: 56 us).
 static uint32_t rows_aimed_at(bool backward, int act) { return backward && act != kActSilu ? 8 : kMostRows; }
 
-GnPlan gn_plan(int dtype, int act, bool backward, bool split, uint64_t N, uint64_t S, uint32_t C, uint32_t G)
+GnPlan gn_plan(int dtype, int act, bool backward, uint64_t N, uint64_t S, uint32_t C, uint32_t G)
 {
     GnPlan p = {};
     const uint32_t E = elem_bytes(dtype), V = 16 / E, cg = C / G;
@@ -45,34 +48,32 @@ GnPlan gn_plan(int dtype, int act, bool backward, bool split, uint64_t N, uint64
     };
     const uint32_t most = backward ? kResidentBwd : kResident;
     const uint64_t room = (uint64_t)most * kMostRows;
-    if (!split) {
-        // the widest slab, up to 256 bytes of a row (forward: 128), that the registers aimed at hold and
-        // that leaves two workgroups a compute unit; else 64 bytes, as long as they fit at all.
-        // 64 x 196 x 1024 backward: 256 bytes 20 us, 64 bytes 23 us.
-        uint64_t vecs = 0;
-        for (uint32_t bytes = backward ? 256 : 128; bytes >= 64; bytes /= 2) {
-            vecs = slab(bytes);
-            if (vecs <= (uint64_t)most * (backward ? 8 : kMostRows) && N * p.nslab >= 512) break;
-        }
-        // too few slabs to fill the GPU: split, unless the work is so small that one launch is what counts
-        p.resident = (1u << p.tcl) <= most && (vecs <= 2048 || (vecs <= room && N * p.nslab >= 128));
-        if (p.resident) {
-            const uint32_t rows = rows_aimed_at(backward, act);
-            p.threads = 1u << p.tcl;
-            if (p.threads < 64) p.threads = 64;
-            while (p.threads < 256 && (uint64_t)p.threads * 2 < vecs) p.threads *= 2;
-            while (p.threads < most && (uint64_t)p.threads * rows < vecs) p.threads *= 2;
-            p.rows = (uint32_t)((vecs + p.threads - 1) / p.threads);
-            // backward: several samples a workgroup where there are far more than fill the GPU, or
-            // where their channel sums, eight bytes a channel, would be more than the samples
-            // themselves (8192 x 1 x 2048, one group: their sum takes 26 us for 8192 rows, 8 for 1024)
-            uint64_t nper = 1;
-            while (backward && nper < N &&
-                   (N * p.nslab / nper > 4096 || (N * p.nslab / nper > 1024 && S * nper < 32)))
-                nper *= 2;
-            p.nper = (uint32_t)nper;
-            p.nparts = (uint32_t)((N + nper - 1) / nper);
-        }
+    // the widest slab, up to 256 bytes of a row (forward: 128), that the registers aimed at hold and
+    // that leaves two workgroups a compute unit; else 64 bytes, as long as they fit at all.
+    // 64 x 196 x 1024 backward: 256 bytes 20 us, 64 bytes 23 us.
+    uint64_t vecs = 0;
+    for (uint32_t bytes = backward ? 256 : 128; bytes >= 64; bytes /= 2) {
+        vecs = slab(bytes);
+        if (vecs <= (uint64_t)most * (backward ? 8 : kMostRows) && N * p.nslab >= 512) break;
+    }
+    // too few slabs to fill the GPU: split, unless the work is so small that one launch is what counts
+    p.resident = (1u << p.tcl) <= most && (vecs <= 2048 || (vecs <= room && N * p.nslab >= 128));
+    if (p.resident) {
+        const uint32_t rows = rows_aimed_at(backward, act);
+        p.threads = 1u << p.tcl;
+        if (p.threads < 64) p.threads = 64;
+        while (p.threads < 256 && (uint64_t)p.threads * 2 < vecs) p.threads *= 2;
+        while (p.threads < most && (uint64_t)p.threads * rows < vecs) p.threads *= 2;
+        p.rows = (uint32_t)((vecs + p.threads - 1) / p.threads);
+        // backward: several samples a workgroup where there are far more than fill the GPU, or
+        // where their channel sums, eight bytes a channel, would be more than the samples
+        // themselves (8192 x 1 x 2048, one group: their sum takes 26 us for 8192 rows, 8 for 1024)
+        uint64_t nper = 1;
+        while (backward && nper < N &&
+               (N * p.nslab / nper > 4096 || (N * p.nslab / nper > 1024 && S * nper < 32)))
+            nper *= 2;
+        p.nper = (uint32_t)nper;
+        p.nparts = (uint32_t)((N + nper - 1) / nper);
     }
     if (!p.resident) {
         // 64 channels: 64 x 3136 x 256 backward 92 us (32: 97, 128: 95, 512: 99)
@@ -174,8 +175,8 @@ int check_pack(int64_t rows, int64_t cols, const void *x, int64_t ldx, int32_t d
 }
 
 struct GnCall {
-    GnPlan fwd[2], bwd[2];           // as the shape asks for, and split
-    size_t need;                     // workspace, of all of them
+    GnPlan fwd, bwd;
+    size_t need;                     // workspace, of both
     int64_t rows;
 };
 
@@ -197,15 +198,11 @@ int plan(const lags_gn *gn, GnCall &c)
     // an empty call is planned as one of one row, whose limits are the same
     const uint64_t N = gn->samples ? gn->samples : 1, S = gn->spatial ? gn->spatial : 1;
     const uint32_t C = (uint32_t)gn->channels, G = (uint32_t)gn->groups;
-    size_t floats = 0;
-    for (int split = 0; split < 2; ++split) {
-        c.fwd[split] = gn_plan(gn->dtype, gn->act, false, split, N, S, C, G);
-        c.bwd[split] = gn_plan(gn->dtype, gn->act, true, split, N, S, C, G);
-        if (!c.fwd[split].threads || !c.bwd[split].threads) return LAGS_ERANGE;
-        const size_t f = gn_part_floats(c.fwd[split], false, N, C, G), b = gn_part_floats(c.bwd[split], true, N, C, G);
-        floats = floats > f ? floats : f;
-        floats = floats > b ? floats : b;
-    }
+    c.fwd = gn_plan(gn->dtype, gn->act, false, N, S, C, G);
+    c.bwd = gn_plan(gn->dtype, gn->act, true, N, S, C, G);
+    if (!c.fwd.threads || !c.bwd.threads) return LAGS_ERANGE;
+    const size_t f = gn_part_floats(c.fwd, false, N, C, G), b = gn_part_floats(c.bwd, true, N, C, G);
+    const size_t floats = f > b ? f : b;
     c.need = c.rows ? (floats * 4 + 15) / 16 * 16 : 0;
     if (c.need < 16) c.need = 16;
     return LAGS_OK;
@@ -221,16 +218,6 @@ void fill(const lags_gn *gn, const GnPlan &p, GnArgs &a)
     a.act = gn->act, a.inv_cg = 1.0f / (float)a.cg;
     a.w = p.w, a.nslab = p.nslab, a.tcl = p.tcl, a.nchunk = p.nchunk, a.chunk = p.chunk;
     a.nper = p.nper, a.nparts = p.nparts;
-}
-
-// A resident workgroup reaches its rows by 32-bit offsets; where a pitch is too
-// large for that the split form runs (its offsets span one sweep of rows).
-bool split_only(const GnPlan &p, int dtype, std::initializer_list<int64_t> lds)
-{
-    for (int64_t ld : lds)
-        if (p.resident && (uint64_t)(p.threads >> p.tcl) * kMostRows * ld * elem_bytes(dtype) >= 0x7fffffffull)
-            return true;
-    return false;
 }
 
 // `out` must not overlap any of the n regions of `all` but itself.
@@ -311,8 +298,7 @@ int lags_gn_forward(const lags_gn *gn, const void *x, int64_t ldx, const float *
     if (overlap(r[1], r[2]) || overlap(r[1], r[3]) || (overlap(r[0], r[1]) && !same(r[0], r[1]))) return LAGS_EINVAL;
     if (!c.rows) return LAGS_OK;
     GnArgs a = {};
-    const GnPlan &p = c.fwd[split_only(c.fwd[0], gn->dtype, {ldx, ldy})];
-    fill(gn, p, a);
+    fill(gn, c.fwd, a);
     a.x = x, a.ldx = ldx, a.y = y, a.ldy = ldy;
     a.gamma = gamma, a.beta = beta, a.mean = mean, a.rstd = rstd;
     if (ckpt) a.wcodes = (uint8_t *)ckpt, a.wscales = (uint8_t *)ckpt + (size_t)c.rows * a.pitch;
@@ -321,7 +307,7 @@ int lags_gn_forward(const lags_gn *gn, const void *x, int64_t ldx, const float *
     // -> 107 us, 206 MB 219 -> 216, 51 MB 56.5 -> 57.7 (and no gain at any size for the backward's dx).
     a.past = (u128)c.rows * gn->channels * elem_bytes(gn->dtype) > ((u128)64 << 20);
     a.part = (float *)ws;
-    return hip(launch_gn_forward(p, a, gn->dtype, (hipStream_t)stream));
+    return hip(launch_gn_forward(c.fwd, a, gn->dtype, (hipStream_t)stream));
 }
 
 int lags_gn_backward(const lags_gn *gn, const void *dy, int64_t lddy, const void *x, int64_t ldx, const void *ckpt,
@@ -360,14 +346,13 @@ int lags_gn_backward(const lags_gn *gn, const void *dy, int64_t lddy, const void
         if (overlap(r[1], r[in])) return LAGS_EINVAL;
     if (overlap(r[0], r[1]) && !same(r[0], r[1])) return LAGS_EINVAL;
     GnArgs a = {};
-    const GnPlan &p = c.bwd[split_only(c.bwd[0], gn->dtype, {lddy, lddx, x ? ldx : 0})];
-    fill(gn, p, a);
+    fill(gn, c.bwd, a);
     a.dy = dy, a.lddy = lddy, a.dx = dx, a.lddx = lddx, a.x = x, a.ldx = ldx;
     if (ckpt) a.rcodes = (const uint8_t *)ckpt, a.rscales = (const uint8_t *)ckpt + (size_t)c.rows * a.pitch;
     a.gamma = gamma, a.beta = beta, a.mean = (float *)mean, a.rstd = (float *)rstd;
     a.dgamma = dgamma, a.dbeta = dbeta, a.add = flags & LAGS_GRAD_ADD;
     a.part = (float *)ws;
-    return hip(launch_gn_backward(p, a, gn->dtype, (hipStream_t)stream));
+    return hip(launch_gn_backward(c.bwd, a, gn->dtype, (hipStream_t)stream));
 }
 
 size_t lags_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols, int32_t dtype)

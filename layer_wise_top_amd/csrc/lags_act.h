@@ -88,7 +88,7 @@ struct GnPlan {
 };
 constexpr uint32_t kSlabMax = 4096;  // channels a workgroup spans, at most
 // .threads == 0: the shape is not supported
-GnPlan gn_plan(int dtype, int act, bool backward, bool split, uint64_t N, uint64_t S, uint32_t C, uint32_t G);
+GnPlan gn_plan(int dtype, int act, bool backward, uint64_t N, uint64_t S, uint32_t C, uint32_t G);
 size_t gn_part_floats(const GnPlan &p, bool backward, uint64_t N, uint32_t C, uint32_t G);
 template <int D> hipError_t launch_gn_forward(const GnPlan &p, const GnArgs &a, hipStream_t s);
 template <int D> hipError_t launch_gn_backward(const GnPlan &p, const GnArgs &a, hipStream_t s);

@@ -1,0 +1,37 @@
+"""What the activation operators plan for a shape, on the host: workspace sizes."""
+import ctypes
+import math
+import random
+
+import pytest
+
+from layer_wise_top_amd import lags
+
+DTYPES = {"f32": (lags.LAGS_F32, 4), "bf16": (lags.LAGS_BF16, 2), "f16": (lags.LAGS_F16, 2)}
+
+
+def gn_bytes(n, s, c, g, dtype, act=2):
+    shape = lags.GnShape(n, s, c, g, DTYPES[dtype][0], act, 1e-5)
+    return int(lags.lib().lags_gn_workspace_bytes(ctypes.byref(shape)))
+
+
+def short_samples(rng, dtype):
+    """Thousands of samples of one to four positions, groups up to the widest."""
+    c = int(math.exp(rng.uniform(math.log(32), math.log(4096 if dtype != "f32" else 2048))))
+    g = rng.choice([k for k in (1, 2, 3, 4, 8, 32) if c % k == 0])
+    return rng.randrange(2000, 100000), rng.randrange(1, 5), c, g
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_group_norm_workspace_of_short_samples(dtype):
+    """A workgroup adds up its samples' channel sums, so what is kept for the last sum is a fraction
+    of the data: 8 bytes a channel of 1024 workgroups at most while a workgroup has under 32 rows (32
+    MiB at the widest slab, 4096 channels), beyond that 8 bytes for every 32 values of a channel."""
+    rng = random.Random(4)
+    shapes = [(16384, 1, 2048, 1), (16384, 2, 2048, 1), (8192, 4, 1024, 32), (100000, 1, 64, 2)]
+    if dtype != "f32":
+        shapes += [(16384, 1, 4096, 1), (16384, 1, 2500, 1)]
+    shapes += [short_samples(rng, dtype) for _ in range(500)]
+    for n, s, c, g in shapes:
+        need, data = gn_bytes(n, s, c, g, dtype), n * s * c * DTYPES[dtype][1]
+        assert 16 <= need <= max(8 * 1024 * 4096, data // 8) + 8 * c + 16, (n, s, c, g)
