@@ -445,7 +445,8 @@ typedef struct lags_gn {
 } lags_gn;
 
 /* Bytes of workspace that lags_gn_forward and lags_gn_backward of this shape
- * need (at least 16); 0 for an invalid shape. */
+ * need (at least 16; at most the bytes of x, or 8 * (2^22 + channels) if that
+ * is more); 0 for an invalid shape. */
 size_t lags_gn_workspace_bytes(const lags_gn *gn);
 
 /*

@@ -47,7 +47,6 @@ GnPlan gn_plan(int dtype, int act, bool backward, uint64_t N, uint64_t S, uint32
         return S << p.tcl;                         // vectors of a slab's lanes
     };
     const uint32_t most = backward ? kResidentBwd : kResident;
-    const uint64_t room = (uint64_t)most * kMostRows;
     // the widest slab, up to 256 bytes of a row (forward: 128), that the registers aimed at hold and
     // that leaves two workgroups a compute unit; else 64 bytes, as long as they fit at all.
     // 64 x 196 x 1024 backward: 256 bytes 20 us, 64 bytes 23 us.
@@ -56,12 +55,17 @@ GnPlan gn_plan(int dtype, int act, bool backward, uint64_t N, uint64_t S, uint32
         vecs = slab(bytes);
         if (vecs <= (uint64_t)most * (backward ? 8 : kMostRows) && N * p.nslab >= 512) break;
     }
+    // A backward slab of 2049 to 4096 fp32 channels has more lanes than other workgroups and takes fewer
+    // rows: in the split form a sample of one position leaves two sums for every value it has (16384 x 1 x
+    // 4096: 537 MB of workspace beside 268 MB of data).
+    const uint32_t lanes = 1u << p.tcl;
+    const bool wide = lanes > most;
     // too few slabs to fill the GPU: split, unless the work is so small that one launch is what counts
-    p.resident = (1u << p.tcl) <= most && (vecs <= 2048 || (vecs <= room && N * p.nslab >= 128));
+    const uint64_t room = wide ? (uint64_t)lanes * kWideRows : (uint64_t)most * kMostRows;
+    p.resident = lanes <= kResident && (vecs <= 2048 || (vecs <= room && N * p.nslab >= 128));
     if (p.resident) {
         const uint32_t rows = rows_aimed_at(backward, act);
-        p.threads = 1u << p.tcl;
-        if (p.threads < 64) p.threads = 64;
+        p.threads = lanes < 64 ? 64 : lanes;
         while (p.threads < 256 && (uint64_t)p.threads * 2 < vecs) p.threads *= 2;
         while (p.threads < most && (uint64_t)p.threads * rows < vecs) p.threads *= 2;
         p.rows = (uint32_t)((vecs + p.threads - 1) / p.threads);

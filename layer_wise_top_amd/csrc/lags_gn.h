@@ -9,7 +9,8 @@
 namespace lags {
 
 constexpr uint32_t kResident = 1024;  // threads of a resident workgroup, at most (forward)
-constexpr uint32_t kResidentBwd = 512;
+constexpr uint32_t kResidentBwd = 512;   // backward; 1024 of up to kWideRows rows where a slab has so many lanes
+constexpr uint32_t kWideRows = 4;
 constexpr uint32_t kMostRows = 13;   // register rows a thread, at most
 
 // A workgroup takes `w` channels (whole groups, whole runs) of one sample:

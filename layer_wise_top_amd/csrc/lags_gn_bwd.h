@@ -239,13 +239,18 @@ __device__ inline void put_channel_sums(const Geo &g, float *sh, uint32_t C, flo
     }
 }
 
+// Threads at most: a slab of 2049 to 4096 fp32 channels has 1024 lanes of columns.
+constexpr int bwd_threads(int dtype, int rows)
+{
+    return dtype == kF32 && rows <= (int)kWideRows ? 1024 : (int)kResidentBwd;
+}
 // Waves a SIMD, at least: two workgroups a compute unit, so that one loads
 // while another sums or stores, where the vectors leave the registers for it.
-constexpr int bwd_waves(int rows, bool uni) { return uni ? rows <= 8 ? 4 : 3 : 2; }
+constexpr int bwd_waves(int threads, int rows, bool uni) { return threads == 1024 || (uni && rows <= 8) ? 4 : uni ? 3 : 2; }
 
 // Resident: R vectors a thread of dy and of the stored input.
 template <int D, int ACT, bool CK, int R, bool ODD, bool UNI>
-__global__ __launch_bounds__(kResidentBwd, bwd_waves(R, UNI)) void k_gn_bwd(GnArgs a)
+__global__ __launch_bounds__(bwd_threads(D, R), bwd_waves(bwd_threads(D, R), R, UNI)) void k_gn_bwd(GnArgs a)
 {
     constexpr int V = Elem<D>::V;
     extern __shared__ float sh[];
