@@ -500,7 +500,8 @@ size_t lags_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols,
  *   flags: 0 or LAGS_GRAD_ADD.
  * rows >= 0 (0: dw becomes 0 unless added to); outs and cols in [1, LAGS_WGRAD_MAX],
  * lddy <= LAGS_WGRAD_MAX.
- * Returns LAGS_OK, LAGS_EINVAL, LAGS_ERANGE, LAGS_EWORKSPACE (ws or ckpt), LAGS_EHIP.
+ * Returns LAGS_OK, LAGS_EINVAL, LAGS_ERANGE (also for a dw of more tiles than one
+ * launch takes, above 130 GB), LAGS_EWORKSPACE (ws or ckpt), LAGS_EHIP.
  */
 int lags_ckpt_wgrad(int64_t rows, int64_t outs, int64_t cols, const void *dy, int64_t lddy,
                     int32_t dtype, const void *ckpt, size_t ckpt_bytes, float *dw, uint32_t flags,

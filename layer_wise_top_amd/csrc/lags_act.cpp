@@ -3,6 +3,7 @@
 #include "lags.h"
 #include "lags_gn.h"
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 
@@ -97,11 +98,12 @@ GnPlan gn_plan(int dtype, int act, bool backward, uint64_t N, uint64_t S, uint32
         if (chunk > S) chunk = S;
         p.chunk = (uint32_t)chunk;
         p.nchunk = (uint32_t)((S + chunk - 1) / chunk);
-        if (N * p.nchunk > 0x7fffffffull) return GnPlan{};
+        if (N * p.nchunk > kMostThreads) return GnPlan{};
         p.nparts = (uint32_t)(N * p.nchunk);
     }
-    const uint64_t grid = (p.resident ? N : N * p.nchunk) * p.nslab;
-    return grid <= 0x7fffffffull ? p : GnPlan{};
+    // a resident forward has as many launches as its samples need
+    const uint64_t grid = (!p.resident ? N * p.nchunk : backward ? p.nparts : 1) * p.nslab;
+    return grid * p.threads <= kMostThreads ? p : GnPlan{};
 }
 
 size_t gn_part_floats(const GnPlan &p, bool backward, uint64_t N, uint32_t C, uint32_t G)
@@ -247,26 +249,32 @@ int lags_ckpt_pack(int64_t rows, int64_t cols, const void *x, int64_t ldx, int32
                    size_t ckpt_bytes, void *stream)
 {
     if (int rc = check_pack(rows, cols, x, ldx, dtype, ckpt, ckpt_bytes); rc != LAGS_OK) return rc;
-    if (!rows) return LAGS_OK;
     PackArgs a = {};
-    a.s = ckpt_shape(rows, cols);
-    a.src = x, a.ld = ldx;
-    a.dst = ckpt;
-    a.wscale = (uint8_t *)ckpt + (size_t)rows * a.s.pitch;
-    return hip(launch_pack(a, dtype, (hipStream_t)stream));
+    a.s = ckpt_shape(rows, cols), a.ld = ldx;
+    uint8_t *codes = (uint8_t *)ckpt, *scales = codes + (size_t)rows * a.s.pitch;
+    for (int64_t r = 0, most = pack_rows(a.s, dtype); r < rows; r += most) {
+        a.s.rows = std::min(most, rows - r);
+        a.src = (const char *)x + r * ldx * elem_bytes(dtype);
+        a.dst = codes + r * a.s.pitch, a.wscale = scales + r * a.s.nrun;
+        if (int rc = hip(launch_pack(a, dtype, (hipStream_t)stream)); rc != LAGS_OK) return rc;
+    }
+    return LAGS_OK;
 }
 
 int lags_ckpt_unpack(int64_t rows, int64_t cols, const void *ckpt, size_t ckpt_bytes, void *x, int64_t ldx,
                      int32_t dtype, void *stream)
 {
     if (int rc = check_pack(rows, cols, x, ldx, dtype, ckpt, ckpt_bytes); rc != LAGS_OK) return rc;
-    if (!rows) return LAGS_OK;
     PackArgs a = {};
-    a.s = ckpt_shape(rows, cols);
-    a.src = ckpt, a.ld = ldx;
-    a.dst = x;
-    a.rscale = (const uint8_t *)ckpt + (size_t)rows * a.s.pitch;
-    return hip(launch_unpack(a, dtype, (hipStream_t)stream));
+    a.s = ckpt_shape(rows, cols), a.ld = ldx;
+    const uint8_t *codes = (const uint8_t *)ckpt, *scales = codes + (size_t)rows * a.s.pitch;
+    for (int64_t r = 0, most = pack_rows(a.s, dtype); r < rows; r += most) {
+        a.s.rows = std::min(most, rows - r);
+        a.src = codes + r * a.s.pitch, a.rscale = scales + r * a.s.nrun;
+        a.dst = (char *)x + r * ldx * elem_bytes(dtype);
+        if (int rc = hip(launch_unpack(a, dtype, (hipStream_t)stream)); rc != LAGS_OK) return rc;
+    }
+    return LAGS_OK;
 }
 
 size_t lags_gn_workspace_bytes(const lags_gn *gn)
@@ -381,7 +389,7 @@ int lags_ckpt_wgrad(int64_t rows, int64_t outs, int64_t cols, const void *dy, in
     if (!ckpt || !aligned(ckpt, 16) || ckpt_bytes < need_ck) return LAGS_EWORKSPACE;
     const size_t need = lags_ckpt_wgrad_workspace_bytes(rows, outs, cols, dtype);
     const WgradPlan p = wgrad_plan(dtype, rows, outs, cols);
-    if (!need || (u128)p.to * p.tc * p.split > kMaxDim) return LAGS_ERANGE;
+    if (!need || (u128)p.to * p.tc * p.split * 512 > kMostThreads) return LAGS_ERANGE;
     if (!ws || !aligned(ws, 16) || ws_bytes < need) return LAGS_EWORKSPACE;
     r[1] = flat(ckpt, need_ck), r[2] = flat(dw, (size_t)outs * cols * 4), r[3] = flat(ws, need);
     if (!clear_of(r, 4, 2) || !clear_of(r, 4, 3)) return LAGS_EINVAL;

@@ -77,6 +77,10 @@ struct WgradArgs {
     uint32_t add;
 };
 
+// Threads of one launch, at most: the runtime takes more and starts that number modulo 2^32.
+constexpr uint64_t kMostThreads = 0xffffffffull;
+
+int64_t pack_rows(const CkptShape &s, int dtype);    // rows of one launch, at most
 hipError_t launch_pack(const PackArgs &a, int dtype, hipStream_t s);
 hipError_t launch_unpack(const PackArgs &a, int dtype, hipStream_t s);
 

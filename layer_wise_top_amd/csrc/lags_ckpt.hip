@@ -99,12 +99,13 @@ template <int D> __global__ __launch_bounds__(kThreads) void k_unpack(PackArgs a
     }
 }
 
+uint32_t vectors_a_row(const CkptShape &s, int dtype) { return s.nrun * (kRun * elem_bytes(dtype) / 16); }
+
 // nvp, and the multiply-shift that divides by it exactly for every value
-// below 2^31 (a workgroup's slots stay below nvp + kThreads * kVecs).
-hipError_t plan(PackArgs &a, int dtype, uint32_t &grid)
+// below 2^31 (a workgroup's slots stay below nvp + kThreads * kVecs).  Returns the workgroups.
+uint32_t plan(PackArgs &a, int dtype)
 {
-    const uint32_t V = 16 / elem_bytes(dtype);
-    a.nvp = a.s.nrun * (kRun / V);
+    a.nvp = vectors_a_row(a.s, dtype);
     uint32_t l = 0;
     while ((uint64_t)1 << l < a.nvp) ++l;
     // ceil(2^(32+l-1) / nvp) for l >= 1 stays below 2^32 and is exact below 2^31
@@ -115,19 +116,21 @@ hipError_t plan(PackArgs &a, int dtype, uint32_t &grid)
         a.shift = l - 1;
     }
     const uint64_t slots = (uint64_t)a.s.rows * a.nvp, per = kThreads * kVecs;
-    const uint64_t g = (slots + per - 1) / per;
-    if (g > 0x7fffffffull) return hipErrorInvalidValue;
-    grid = (uint32_t)g;
-    return hipSuccess;
+    return (uint32_t)((slots + per - 1) / per);
 }
 
 }  // namespace
 
+int64_t pack_rows(const CkptShape &s, int dtype)
+{
+    constexpr uint64_t per = kThreads * kVecs;
+    return (int64_t)(kMostThreads / kThreads * per / vectors_a_row(s, dtype));
+}
+
 hipError_t launch_pack(const PackArgs &a0, int dtype, hipStream_t s)
 {
     PackArgs a = a0;
-    uint32_t g;
-    if (hipError_t e = plan(a, dtype, g); e != hipSuccess) return e;
+    const uint32_t g = plan(a, dtype);
     switch (dtype) {
     case kF32: k_pack<kF32><<<g, kThreads, 0, s>>>(a); break;
     case kBF16: k_pack<kBF16><<<g, kThreads, 0, s>>>(a); break;
@@ -139,8 +142,7 @@ hipError_t launch_pack(const PackArgs &a0, int dtype, hipStream_t s)
 hipError_t launch_unpack(const PackArgs &a0, int dtype, hipStream_t s)
 {
     PackArgs a = a0;
-    uint32_t g;
-    if (hipError_t e = plan(a, dtype, g); e != hipSuccess) return e;
+    const uint32_t g = plan(a, dtype);
     switch (dtype) {
     case kF32: k_unpack<kF32><<<g, kThreads, 0, s>>>(a); break;
     case kBF16: k_unpack<kBF16><<<g, kThreads, 0, s>>>(a); break;

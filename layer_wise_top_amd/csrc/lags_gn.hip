@@ -38,13 +38,26 @@ __global__ __launch_bounds__(kParChan * kParRows) void k_gn_params(GnArgs a, uin
 
 }  // namespace
 
-hipError_t launch_gn_forward(const GnPlan &p, const GnArgs &a, int dtype, hipStream_t s)
+hipError_t launch_gn_forward(const GnPlan &p, const GnArgs &all, int dtype, hipStream_t s)
 {
-    switch (dtype) {
-    case kF32: return launch_gn_forward<kF32>(p, a, s);
-    case kBF16: return launch_gn_forward<kBF16>(p, a, s);
-    default: return launch_gn_forward<kF16>(p, a, s);
+    const uint32_t E = elem_bytes(dtype);
+    // samples of one launch (split: all of them, the plan sees to that)
+    const uint32_t most = p.resident ? (uint32_t)(kMostThreads / p.threads / p.nslab) : all.N;
+    for (uint32_t n = 0; n < all.N;) {
+        GnArgs a = all;
+        a.N = all.N - n < most ? all.N - n : most;
+        const int64_t row = (int64_t)n * a.S, group = (int64_t)n * a.G;
+        a.x = (const char *)a.x + row * a.ldx * E, a.y = (char *)a.y + row * a.ldy * E;
+        if (a.mean) a.mean += group;
+        if (a.rstd) a.rstd += group;
+        if (a.wcodes) a.wcodes += row * a.pitch, a.wscales += row * a.nrun;
+        const hipError_t e = dtype == kF32    ? launch_gn_forward<kF32>(p, a, s)
+                             : dtype == kBF16 ? launch_gn_forward<kBF16>(p, a, s)
+                                              : launch_gn_forward<kF16>(p, a, s);
+        if (e != hipSuccess) return e;
+        n += a.N;
     }
+    return hipSuccess;
 }
 
 hipError_t launch_gn_backward(const GnPlan &p, const GnArgs &a, int dtype, hipStream_t s)

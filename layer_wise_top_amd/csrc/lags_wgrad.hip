@@ -349,7 +349,9 @@ WgradPlan wgrad_plan(int dtype, int64_t M, int64_t O, int64_t C)
         p.to = (uint32_t)((O + kTiles[t].bo - 1) / kTiles[t].bo);
         p.tc = (uint32_t)((C + kTiles[t].bc - 1) / kTiles[t].bc);
         const double tiles = (double)p.to * p.tc;
-        for (int64_t want = 1; want <= 512; want = want < 4 ? want + 1 : want % 3 ? want + want / 2 : want / 3 * 4) {
+        // a dW above 2^32 values is not sliced: its sum would be more threads than a launch has
+        const int64_t slices = O * C > (int64_t)1 << 32 ? 1 : 512;
+        for (int64_t want = 1; want <= slices; want = want < 4 ? want + 1 : want % 3 ? want + want / 2 : want / 3 * 4) {
             int64_t per = ((M + want - 1) / want + 63) / 64 * 64;
             if (per < 64) per = 64;
             p.rows_per = per;

@@ -55,3 +55,12 @@ def test_group_norm_workspace_of_any_shape(dtype):
             continue
         seen += 1
         assert need <= max(8 * 1024 * 4096 + 8 * c, n * s * c * DTYPES[dtype][1]), (n, s, c, g)
+
+
+def test_weight_gradient_that_is_not_sliced():
+    """Slices of a dW above 2^32 values would take twice its bytes and more threads to add up than a
+    launch has; below, a long product has them."""
+    f = lags.lib().lags_ckpt_wgrad_workspace_bytes
+    for rows, outs, cols, dtype in ((386292, 37480, 233212, 0), (1093745, 73993, 116331, 1), (604912, 65741, 132777, 2)):
+        assert f(rows, outs, cols, dtype) == 16
+    assert f(200704, 256, 64, 1) > 16
