@@ -403,7 +403,10 @@ const char *lags_kernel_name(int32_t id);
  * for which every value of the run divided by 2^(s - 127), rounded to the
  * nearest integer with ties to even, is at most 127 in magnitude.  So a value
  * is off by at most half of 2^(s - 127), 1/128 of the run's largest magnitude,
- * and is exact in bf16.  A run that holds an infinity or NaN has s = 255 and
+ * and is exact in bf16 but for one: finite magnitudes from 127.5/128 * 2^128 up
+ * (the largest bf16 value is one) are held as 64 * 2^122 = 2^128, past both
+ * types.  lags_gn_backward takes it as that, lags_ckpt_wgrad as the largest
+ * bf16 value, 255 * 2^120.  A run that holds an infinity or NaN has s = 255 and
  * q = 0 and reads back as NaN throughout.
  * Buffer: codes [rows][pitch], pitch = cols rounded up to 16 (pad codes are
  * 0), then scales [rows][ceil(cols / 32)]; the size is rounded up to 16.
@@ -420,7 +423,9 @@ size_t lags_ckpt_bytes(int64_t rows, int64_t cols);
 int lags_ckpt_pack(int64_t rows, int64_t cols, const void *x, int64_t ldx, int32_t dtype,
                    void *ckpt, size_t ckpt_bytes, void *stream);
 
-/* The values of ckpt, rounded to dtype, into x.  Returns as lags_ckpt_pack. */
+/* The values of ckpt, rounded to dtype, into x: one past the type's range is an
+ * infinity (2^128, and in fp16 65536, which fp16 magnitudes from 65280 up are
+ * held as).  Returns as lags_ckpt_pack. */
 int lags_ckpt_unpack(int64_t rows, int64_t cols, const void *ckpt, size_t ckpt_bytes, void *x,
                      int64_t ldx, int32_t dtype, void *stream);
 

@@ -29,7 +29,9 @@ namespace lags {
 namespace {
 
 // A vector of the stored input: as it was, or 8-bit codes with their scale.
+// `kUnit` is what x and its mean are multiplied by before they are subtracted.
 template <int D, bool CK> struct Stored {
+    static constexpr float kUnit = 1;
     u32x4 v;
     // x - mu, rounded once
     template <bool U> __device__ void centred(const PerGroup<Elem<D>::V, U> &mu, float (&f)[Elem<D>::V]) const
@@ -40,11 +42,13 @@ template <int D, bool CK> struct Stored {
     __device__ void hold(float t) { keep(v, t); }
 };
 template <int D> struct Stored<D, true> {
+    // half: 64 steps of 2^122, which the largest finite values round to, are past fp32
+    static constexpr float kUnit = 0.5f;
     uint32_t q[Elem<D>::V / 4], s;
     // a value is code times step exactly, so this too is rounded once
     template <bool U> __device__ void centred(const PerGroup<Elem<D>::V, U> &mu, float (&f)[Elem<D>::V]) const
     {
-        const float step = run_step(s);
+        const float step = kUnit * run_step(s);
         for (int i = 0; i < Elem<D>::V / 4; ++i) code_values(q[i], f + 4 * i);
         for (int j = 0; j < Elem<D>::V; ++j) f[j] = __builtin_fmaf(f[j], step, -mu[j]);
     }
@@ -111,12 +115,13 @@ template <int ACT, int V> __device__ inline void act_grad(const float (&xh)[V], 
 template <int V, bool UNI> struct Chan {     // a thread's channels
     PerGroup<V, UNI> mu, rs;
     float ga[V], be[V];
-    __device__ void load(const GnArgs &a, const Geo &g)
+    // `unit` times the means, rstd over it
+    __device__ void load(const GnArgs &a, const Geo &g, float unit)
     {
         const float *m = a.mean + (size_t)g.n * a.G + over_cg(g.c0, a.inv_cg);
         const float *r = a.rstd + (size_t)g.n * a.G + over_cg(g.c0, a.inv_cg);
-        mu.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return m[i]; });
-        rs.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return r[i]; });
+        mu.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return unit * m[i]; });
+        rs.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return r[i] / unit; });
     }
 };
 
@@ -155,7 +160,7 @@ __device__ inline float bwd_emit(const Writer<D, ODD> &w, const Stored<D, CK> &x
     act_grad<ACT, V>(xh, ch.ga, ch.be, d);
 #pragma unroll
     for (int j = 0; j < V; ++j)
-        d[j] = __builtin_fmaf(ch.ga[j] * ch.rs[j], d[j], -__builtin_fmaf(xh[j], s2[j], s1[j]));
+        d[j] = __builtin_fmaf(ch.ga[j] * (ch.rs[j] * Stored<D, CK>::kUnit), d[j], -__builtin_fmaf(xh[j], s2[j], s1[j]));
     w.store(row, Elem<D>::pack(d));
     return d[0];
 }
@@ -180,7 +185,7 @@ struct Joins {
 // wide (8192 x 1 x 2048, one group: 92 us, else 161), but takes registers that
 // only the shortest samples leave (64 x 784 x 512 in 8 rows: 43 us, else 41).
 template <int V, bool UNI, bool TOTAL, bool ONE>
-__device__ inline void group_means(const GnArgs &a, const Geo &g, const Joins &m, const Chan<V, UNI> &ch,
+__device__ inline void group_means(const GnArgs &a, const Geo &g, const Joins &m, const Chan<V, UNI> &ch, float unit,
                                    float (&sa)[V], float (&sb)[V], PerGroup<V, UNI> &s1, PerGroup<V, UNI> &s2)
 {
     const float cnt = (float)((uint64_t)a.S * a.cg);
@@ -221,7 +226,7 @@ __device__ inline void group_means(const GnArgs &a, const Geo &g, const Joins &m
     __syncthreads();
     s1.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return m.mean[i]; });
     s2.set(g, a.cg, a.inv_cg, [&](uint32_t i) { return m.mean[g.ng + i]; });
-    for (int j = 0; j < (UNI ? 1 : V); ++j) s1.v[j] *= ch.rs[j], s2.v[j] *= ch.rs[j];
+    for (int j = 0; j < (UNI ? 1 : V); ++j) s1.v[j] *= ch.rs[j] * unit, s2.v[j] *= ch.rs[j] * unit;
 }
 
 // The workgroup's per-channel sums, to p[0..C) (sum dz) and p[C..2C) (sum dz xh).
@@ -277,7 +282,7 @@ __global__ __launch_bounds__(bwd_threads(D, R), bwd_waves(bwd_threads(D, R), R, 
             x[k] = xs.load(first + k * g.tr);
             dy[k] = ds.load(first + k * g.tr);
         }
-        ch.load(a, g);
+        ch.load(a, g, Stored<D, CK>::kUnit);
         float sa[V], sb[V];
         for (int j = 0; j < V; ++j) sa[j] = sb[j] = 0;
 #pragma unroll
@@ -287,7 +292,7 @@ __global__ __launch_bounds__(bwd_threads(D, R), bwd_waves(bwd_threads(D, R), R, 
             bwd_sums<D, ACT, CK, UNI>(x[k], dy[k], ch, sa, sb);
         }
         PerGroup<V, UNI> s1, s2;
-        group_means<V, UNI, true, UNI && R == 2>(a, g, joins, ch, sa, sb, s1, s2);
+        group_means<V, UNI, true, UNI && R == 2>(a, g, joins, ch, Stored<D, CK>::kUnit, sa, sb, s1, s2);
         const Writer<D, ODD> w(a.dx, row0, a.S, a.lddx, g.c0, g.wc, g.col);
         float last = s1[0];
 #pragma unroll
@@ -312,7 +317,7 @@ __global__ __launch_bounds__(1024) void k_gn_bwd_sums(GnArgs a)
     Chan<V, UNI> ch;
     load_param<V>(a.gamma, g, 1.0f, ch.ga);
     load_param<V>(a.beta, g, 0.0f, ch.be);
-    ch.load(a, g);
+    ch.load(a, g, Stored<D, CK>::kUnit);
     float sa[V], sb[V];
     for (int j = 0; j < V; ++j) sa[j] = sb[j] = 0;
     const uint32_t lo = g.chunk * a.chunk, rows = min(a.S - lo, a.chunk);
@@ -347,7 +352,7 @@ __global__ __launch_bounds__(1024) void k_gn_bwd_apply(GnArgs a)
     Chan<V, UNI> ch;
     load_param<V>(a.gamma, g, 1.0f, ch.ga);
     load_param<V>(a.beta, g, 0.0f, ch.be);
-    ch.load(a, g);
+    ch.load(a, g, Stored<D, CK>::kUnit);
     float sa[V], sb[V];
     for (int j = 0; j < V; ++j) sa[j] = sb[j] = 0;
     const Joins joins(sh, g, V);
@@ -359,7 +364,7 @@ __global__ __launch_bounds__(1024) void k_gn_bwd_apply(GnArgs a)
         for (int j = 0; j < V; ++j) sa[j] += u[j], sb[j] += v[j];
     }
     PerGroup<V, UNI> s1, s2;
-    group_means<V, UNI, false, false>(a, g, joins, ch, sa, sb, s1, s2);
+    group_means<V, UNI, false, false>(a, g, joins, ch, Stored<D, CK>::kUnit, sa, sb, s1, s2);
     float last = s1[0];
     const uint32_t lo = g.chunk * a.chunk, rows = min(a.S - lo, a.chunk);
     for (uint32_t s0 = 0; s0 < rows; s0 += U * g.tr) {

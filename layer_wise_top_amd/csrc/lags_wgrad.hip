@@ -73,6 +73,11 @@ template <int D, int T> __device__ inline void terms(u32x4 v, uint32_t (&t)[T][E
     }
 }
 
+// Rounding of fp32 vector operations from here on (the compiler moves nothing
+// across): two bits of the mode register, from bit 0.
+enum : int { kNearest = 0, kTowardZero = 3 };
+template <int MODE> __device__ inline void rounding() { __builtin_amdgcn_s_setreg(1 | (2 - 1) << 11, MODE); }
+
 __device__ inline uint32_t deal(uint32_t b, uint32_t n)
 {
     const uint32_t per = n / 8, main = per * 8;
@@ -214,6 +219,10 @@ __global__ __launch_bounds__(64 * WR * WC) void k_wgrad(WgradArgs a)
             }
     };
     int cur = 0;
+    // What staging computes is exact but for one value, 64 steps of 2^122 (which finite magnitudes from
+    // 127.5/128 2^128 up round to): cut, it is the largest bf16 value; rounded, it would be an infinity,
+    // and NaN where dY is zero.  The matrix instructions have a rounding of their own.
+    rounding<kTowardZero>();
     load();
     stage_dy(lds);
     stage_x(lds);
@@ -240,6 +249,7 @@ __global__ __launch_bounds__(64 * WR * WC) void k_wgrad(WgradArgs a)
         }
     }
 
+    rounding<kNearest>();
     float *out = a.split > 1 ? a.part + (size_t)slice * a.O * a.C : a.dw;
     const bool add = a.split == 1 && a.add;
 #pragma unroll

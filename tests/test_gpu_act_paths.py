@@ -67,3 +67,110 @@ def test_checkpoint_of_more_rows_than_a_launch_has_threads():
     assert torch.equal(x[at].cpu(), want)
     x[at] = 0
     assert not x.any()
+
+
+# ---- magnitudes at the top of the range ------------------------------------
+# From 127.5/128 2^128 up (the largest bf16 value is one of them) a run's largest code is 64 steps of
+# 2^122: a value past fp32.  The gradients stay finite and within the format's bound.
+
+TOPS = {"f32": [3.4028234663852886e38, 127.5 / 128 * 2.0 ** 128], "bf16": [255 * 2.0 ** 120]}
+
+
+def _top_runs(dtype):
+    """Rows of one run each with one or more of the largest magnitudes, and ordinary rows."""
+    import numpy as np
+    import torch
+    rng = np.random.default_rng(11)
+    rows = [rng.standard_normal(32) for _ in range(4)]
+    for t in TOPS[dtype]:
+        for sign in (1.0, -1.0):
+            r = rng.uniform(-1, 1, 32) * t
+            r[3], r[17] = sign * t, 0.0
+            rows.append(r)
+    x = torch.from_numpy(np.array(rows)).to(getattr(torch, "float32" if dtype == "f32" else "bfloat16"))
+    assert torch.isfinite(x).all()
+    return x.cuda()
+
+
+@pytest.mark.parametrize("dtype", list(TOPS))
+@pytest.mark.parametrize("dy_dtype", ["f32", "bf16", "f16"])
+def test_weight_gradient_of_the_largest_values(dtype, dy_dtype):
+    """Finite products, and a zero of dY takes a row out: held values are off by 1/128 of the run's
+    largest magnitude at most, sums by their roundings."""
+    import torch
+    from layer_wise_top_amd import lags
+    x = _top_runs(dtype)
+    m = x.shape[0]
+    ck = lags.checkpoint(m, 32)
+    lags.lags_ckpt_pack(x, ck)
+    dy = torch.zeros(m, 70, device="cuda")
+    dy[torch.arange(m), torch.arange(m)] = 2.0 ** -10        # one row of x each
+    dy[:4, 60] = 1.0                                          # the ordinary rows alone
+    dy = dy.to({"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dy_dtype])
+    dw = torch.full((70, 32), 9.0, device="cuda")
+    lags.lags_ckpt_wgrad(dy, ck, dw, lags.wgrad_workspace(m, 70, 32, dy.dtype))
+    assert torch.isfinite(dw).all()
+    want = dy.double().t() @ x.double()
+    bound = dy.double().abs().t() @ (x.double().abs().amax(dim=1, keepdim=True) / 127.5).expand(m, 32)
+    assert ((dw.double() - want).abs() <= bound * (1 + 1e-6)).all()
+
+
+@pytest.mark.parametrize("s", [1, 9000])
+@pytest.mark.parametrize("dtype", list(TOPS))
+def test_group_norm_backward_of_the_largest_values(dtype, s):
+    """Statistics given: rstd = 2^-127 keeps xh about 1, and the bound is the format's error times rstd
+    through the formula; a group without such values is as it was."""
+    import numpy as np
+    import torch
+    from layer_wise_top_amd import lags
+    rows = _top_runs(dtype)
+    n, c = rows.shape[0], 32
+    x = torch.zeros(n, s, c, dtype=rows.dtype, device="cuda")
+    x[:, 0] = rows
+    rng = np.random.default_rng(12)
+    dy = torch.from_numpy(rng.standard_normal((n, s, c))).to(rows.dtype).cuda()
+    mean = torch.zeros(n, 1, device="cuda")
+    rstd = torch.full((n, 1), 2.0 ** -127, device="cuda")
+    rstd[:4] = 1.0
+    gn = lags.GroupNorm(n, s, c, 1, dtype=rows.dtype, act="none")
+    ck = lags.checkpoint(n * s, c)
+    lags.lags_ckpt_pack(x, ck)
+    dx, dg, db = torch.full_like(x, 9.0), torch.empty(c, device="cuda"), torch.empty(c, device="cuda")
+    lags.lags_gn_backward(gn, dy, None, None, mean, rstd, dx, dg, db, lags.gn_workspace(gn), ckpt=ck)
+    for t in (dx, dg, db):
+        assert torch.isfinite(t).all()
+    xh, e = x.double() * rstd.double()[:, None], (x.double().abs().amax(dim=2, keepdim=True) / 127.5) * rstd.double()[:, None]
+    d = dy.double()
+    # the held xh is off by e, the sums by 2^-16 of their terms at most (chains of up to 100 additions)
+    eg = ((d * e).abs() + 2.0 ** -16 * (d * xh).abs()).sum(dim=(0, 1))
+    assert ((dg.double() - (d * xh).sum(dim=(0, 1))).abs() <= eg).all()
+    s2, es2 = (d * xh).mean(dim=(1, 2), keepdim=True), ((d * e).abs() + 2.0 ** -16 * (d * xh).abs()).mean(dim=(1, 2), keepdim=True)
+    s1, es1 = d.mean(dim=(1, 2), keepdim=True), 2.0 ** -16 * d.abs().mean(dim=(1, 2), keepdim=True)
+    r = rstd.double()[:, None]
+    want = r * (d - s1 - xh * s2)
+    bound = r * (es1 + e * (s2.abs() + es2) + xh.abs() * es2 + 2.0 ** -8 * (d.abs() + s1.abs() + (xh * s2).abs())) + 2.0 ** -133
+    assert ((dx.double() - want).abs() <= bound).all()
+
+
+# ---- small gradients -------------------------------------------------------
+
+def test_weight_gradient_of_small_fp32_values():
+    """The terms of a 32-bit dY end at bf16's smallest value, 2^-133: what is below it is cut.  Down to
+    2^-110 nothing is; sums here have one row, so a product is rounded at most three times."""
+    import numpy as np
+    import torch
+    from layer_wise_top_amd import lags
+    rng = np.random.default_rng(13)
+    e = np.repeat(np.arange(-126, -94), 4)
+    v = (rng.uniform(1, 2, e.size) * 2.0 ** e).astype(np.float32)
+    dy = torch.from_numpy(v[None, :]).cuda()
+    x = torch.full((1, 32), 2.0 ** 60, device="cuda")
+    ck = lags.checkpoint(1, 32)
+    lags.lags_ckpt_pack(x, ck)
+    dw = torch.empty(e.size, 32, device="cuda")
+    lags.lags_ckpt_wgrad(dy, ck, dw, lags.wgrad_workspace(1, e.size, 32, torch.float32))
+    want = v.astype(np.float64) * 2.0 ** 60
+    off = np.abs(dw.double().cpu().numpy() - want[:, None]).max(axis=1)
+    print("relative error by exponent", {int(k): float((off / want)[e == k].max()) for k in np.unique(e)}, flush=True)
+    assert (off[e >= -110] <= 3 * 2.0 ** -24 * want[e >= -110]).all()
+    assert (off <= 3 * 2.0 ** -24 * want + 2.0 ** (-133 + 60)).all()
