@@ -1,4 +1,5 @@
-"""What the activation operators plan for a shape, on the host: workspace sizes."""
+"""What the activation operators plan for a shape, on the host: workspace sizes, and the weight
+gradient's tiles."""
 import ctypes
 import math
 import random
@@ -8,6 +9,34 @@ import pytest
 from layer_wise_top_amd import lags
 
 DTYPES = {"f32": (lags.LAGS_F32, 4), "bf16": (lags.LAGS_BF16, 2), "f16": (lags.LAGS_F16, 2)}
+
+
+# Shapes of every tile of the weight gradient, with rows whole and in slices: ragged in the rows, outs
+# and cols, and more than one tile.
+TILES = ("256x256", "192x256", "128x128", "256x64", "64x256", "64x64")
+WGRAD_SHAPES = {
+    "f32": {"256x256": ((96, 25001, 401), (2093, 2812, 399)), "192x256": ((94, 21762, 257), (1094, 3659, 257)),
+            "128x128": ((76, 25134, 65), (644, 2704, 69)), "64x256": ((78, 67, 16671), (669, 449, 321)),
+            "64x64": ((73, 20, 69), (275, 22, 67))},
+    "bf16": {"256x256": ((78, 26252, 385), (3117, 3004, 645)), "192x256": ((75, 519, 14482), (2517, 643, 1815)),
+             "128x128": ((75, 22025, 131), (16775, 327, 20)), "256x64": ((79, 22341, 266), (14122, 400, 21)),
+             "64x256": ((100, 261, 22198), (4681, 643, 711)), "64x64": ((71, 21, 67), (491, 21, 66))},
+    "f16": {"256x256": ((75, 27121, 263), (2344, 1163, 1031)), "192x256": ((77, 21761, 259), (2049, 867, 887)),
+            "128x128": ((76, 66, 25295), (1070, 1117, 257)), "256x64": ((72, 24821, 259), (1816, 8499, 21)),
+            "64x256": ((84, 135, 16471), (1026, 129, 1968)), "64x64": ((73, 20, 67), (357, 65, 24))},
+}
+
+
+class WgradPlan(ctypes.Structure):
+    _fields_ = [("tile", ctypes.c_uint32), ("to", ctypes.c_uint32), ("tc", ctypes.c_uint32),
+                ("split", ctypes.c_uint32), ("rows_per", ctypes.c_int64)]
+
+
+def wgrad_plan(rows, outs, cols, dtype):
+    """The library's own choice (lags::wgrad_plan, not part of the C ABI)."""
+    f = lags.lib()._ZN4lags10wgrad_planEilll
+    f.restype, f.argtypes = WgradPlan, [ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]
+    return f(DTYPES[dtype][0], rows, outs, cols)
 
 
 def gn_bytes(n, s, c, g, dtype, act=2):
@@ -64,3 +93,17 @@ def test_weight_gradient_that_is_not_sliced():
     for rows, outs, cols, dtype in ((386292, 37480, 233212, 0), (1093745, 73993, 116331, 1), (604912, 65741, 132777, 2)):
         assert f(rows, outs, cols, dtype) == 16
     assert f(200704, 256, 64, 1) > 16
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_weight_gradient_shapes_of_every_tile(dtype):
+    """The shapes that the GPU tests compute with take the tiles they are listed for, and no size takes
+    a tile that is not listed."""
+    for tile, shapes in WGRAD_SHAPES[dtype].items():
+        for shape, sliced in zip(shapes, (False, True)):
+            p = wgrad_plan(*shape, dtype)
+            assert TILES[p.tile] == tile and (p.split > 1) == sliced, (shape, TILES[p.tile], p.split)
+    rng = random.Random(6)
+    seen = {TILES[wgrad_plan(log_int(rng, 1, 1 << 24), log_int(rng, 1, 1 << 22), log_int(rng, 1, 1 << 22), dtype).tile]
+            for _ in range(50000)}
+    assert seen == set(WGRAD_SHAPES[dtype])
