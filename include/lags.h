@@ -402,8 +402,8 @@ const char *lags_kernel_name(int32_t id);
  * stands for q * 2^(s - 127): s - 127 is the smallest exponent, -126 at least,
  * for which every value of the run divided by 2^(s - 127), rounded to the
  * nearest integer with ties to even, is at most 127 in magnitude.  So a value
- * is off by at most half of 2^(s - 127), 1/128 of the run's largest magnitude,
- * and is exact in bf16 but for one: finite magnitudes from 127.5/128 * 2^128 up
+ * is off by at most half of 2^(s - 127), where s > 1 no more than 1/127.5 of the
+ * run's largest magnitude, and is exact in bf16 but for one: finite magnitudes from 127.5/128 * 2^128 up
  * (the largest bf16 value is one) are held as 64 * 2^122 = 2^128, past both
  * types.  lags_gn_backward takes it as that, lags_ckpt_wgrad as the largest
  * bf16 value, 255 * 2^120.  A run that holds an infinity or NaN has s = 255 and
@@ -497,8 +497,9 @@ size_t lags_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols,
 /*
  * Weight gradient of a linear layer (or 1x1 convolution) from its input's
  * checkpoint: dw[o][c] = sum over rows of dy[row][o] * X[row][c], X the values
- * of ckpt ([rows, cols]).  The operands are multiplied exactly and summed in
- * fp32.
+ * of ckpt ([rows, cols]).  The operands are multiplied exactly, but that an
+ * fp32 dy is cut at bf16's smallest value, 2^-133 (from 2^-110 up it is whole),
+ * and summed in fp32.
  *   dy:  device matrix [rows, outs] (lddy);
  *   dw:  device fp32[outs][cols], out, contiguous: the layer's slice of the
  *        flat gradient;

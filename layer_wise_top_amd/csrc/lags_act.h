@@ -299,7 +299,7 @@ template <int V> __device__ inline uint32_t run_top(uint32_t m)
     return m;
 }
 // Scale byte of a run: the step 2^(s - 127) is the power of two that takes
-// the largest magnitude into [64, 127.5), so it rounds to at most 127 (adding
+// the largest magnitude into [63.75, 127.5), so it rounds to at most 127 (adding
 // 2^16 to the bits carries into the exponent exactly from 127.5/64 up); at
 // least 2^-126, so steps are never subnormal.  255 where the run holds an
 // infinity or NaN.

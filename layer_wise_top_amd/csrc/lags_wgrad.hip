@@ -2,11 +2,12 @@
 // as an 8-bit checkpoint: dW[o][c] = sum over rows m of dY[m][o] X[m][c].
 //
 // A value of the checkpoint, q 2^k with |q| <= 127, has seven significant
-// bits and is exact in bf16, so the product runs on the bf16 matrix
-// instructions with fp32 sums and no rounding of X.  dY is cut into bf16 terms
-// that add up to it exactly: one for bf16, two for fp16 (11 bits), three for
-// fp32 (24 bits); every product of two terms is exact in fp32, so what is
-// rounded is the summation alone.
+// bits and is exact in bf16 (2^128 apart, see below), so the product runs on
+// the bf16 matrix instructions with fp32 sums and no rounding of X.  dY is cut
+// into bf16 terms that add up to it: one for bf16, two for fp16 (11 bits), three
+// for fp32 (24 bits, of which bf16 holds those from 2^-133 up: all of them
+// where |dY| >= 2^-110); every product of two terms is exact in fp32, so what
+// is rounded is the summation alone.
 // Both operands lie with the summed index (rows) slow, so a tile is staged in
 // LDS as it comes, X being expanded to bf16 on the way, and is transposed by
 // the LDS transpose reads that feed the matrix instructions.
@@ -47,8 +48,7 @@ template <int B> __device__ inline bf16x8 fragment(const char *tile, int kb, int
 }
 
 // The bf16 terms of a vector of dY, eight (or four) columns, two to a word.
-// The leading term is cut, not rounded, so it cannot overflow; what is left
-// is exact.  An infinity or NaN is its own leading term with nothing left.
+// A term is cut, not rounded, so it cannot overflow; what is left is exact.  An infinity or NaN is its own leading term with nothing left.
 template <int D, int T> __device__ inline void terms(u32x4 v, uint32_t (&t)[T][Elem<D>::V / 2])
 {
     constexpr int V = Elem<D>::V;
