@@ -39,6 +39,31 @@ def wgrad_plan(rows, outs, cols, dtype):
     return f(DTYPES[dtype][0], rows, outs, cols)
 
 
+class GnPlan(ctypes.Structure):
+    _fields_ = [("resident", ctypes.c_bool)] + [(k, ctypes.c_uint32) for k in (
+        "threads", "rows", "w", "nslab", "tcl", "nchunk", "chunk", "nper", "nparts")]
+
+
+def gn_plan(dtype, act, backward, n, s, c, groups):
+    """The library's own choice (lags::gn_plan, not part of the C ABI)."""
+    f = lags.lib()._ZN4lags7gn_planEiibmmjj
+    f.restype = GnPlan
+    f.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_bool, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint32,
+                  ctypes.c_uint32]
+    return f(DTYPES[dtype][0], lags.ACTS[act], backward, n, s, c, groups)
+
+
+# Samples that fill 8 and 13 register rows of a thread in both directions, vectors inside one group and
+# cut by groups of three or five channels: (positions of 16-bit values, of fp32), channels, groups.
+ROWS = {8: (500, 250), 13: (1500, 750)}
+GROUPS = {"inside": (16, 2), "cut": (15, 5)}
+
+
+def rows_case(dtype, rows, groups):
+    c, g = GROUPS[groups]
+    return 130, ROWS[rows][dtype == "f32"], c, g
+
+
 def gn_bytes(n, s, c, g, dtype, act=2):
     shape = lags.GnShape(n, s, c, g, DTYPES[dtype][0], act, 1e-5)
     return int(lags.lib().lags_gn_workspace_bytes(ctypes.byref(shape)))
@@ -107,3 +132,14 @@ def test_weight_gradient_shapes_of_every_tile(dtype):
     seen = {TILES[wgrad_plan(log_int(rng, 1, 1 << 24), log_int(rng, 1, 1 << 22), log_int(rng, 1, 1 << 22), dtype).tile]
             for _ in range(50000)}
     assert seen == set(WGRAD_SHAPES[dtype])
+
+
+@pytest.mark.parametrize("act", list(lags.ACTS))
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_group_norm_shapes_of_every_row_count(dtype, act):
+    """The shapes that the GPU tests compute with run resident, in the kernel of 8 or 13 rows."""
+    for rows, least in ((8, 5), (13, 9)):
+        for groups in GROUPS:
+            for backward in (False, True):
+                p = gn_plan(dtype, act, backward, *rows_case(dtype, rows, groups))
+                assert p.resident and least <= p.rows <= rows, (dtype, act, rows, groups, backward, p.rows)

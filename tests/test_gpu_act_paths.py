@@ -2,6 +2,7 @@
 against float64."""
 import pytest
 
+from test_act_plans import GROUPS, ROWS, rows_case
 from test_gpu_gn import Case
 
 pytestmark = pytest.mark.gpu
@@ -14,6 +15,138 @@ def test_fp32_groups_wider_than_2048_channels(n, s, c, groups, act):
     """A column of lanes of its own for each four channels: short samples whole in 1024 lanes, several
     of them a workgroup; five positions, and all of them where samples are few, in chunks."""
     Case(n, s, c, groups, "f32", act, seed=c + s).check_all()
+
+
+@pytest.mark.parametrize("dtype,act", [("f32", "relu"), ("f32", "silu"), ("bf16", "relu"), ("bf16", "silu"),
+                                       ("bf16", "none"), ("f16", "relu"), ("f16", "silu"), ("f16", "none")])
+@pytest.mark.parametrize("groups", list(GROUPS))
+@pytest.mark.parametrize("rows", list(ROWS))
+def test_many_rows_a_thread(rows, groups, dtype, act):
+    """8 and 13 register rows, with vectors inside one group and cut by groups, both directions, from x
+    and from its checkpoint; then the same through rows of odd pitch at odd offsets (16-bit rows that
+    start inside a word) with NaN around them, bit for bit."""
+    import torch
+    from layer_wise_top_amd import lags
+    k = Case(*rows_case(dtype, rows, groups), dtype, act, seed=rows)
+    k.check_all()
+    n, s, c = k.x.shape
+    ck = lags.checkpoint(n * s, c)
+    fwd = k.forward(ck)
+    bwd = k.backward(fwd[1], fwd[2], x=k.x), k.backward(fwd[1], fwd[2], ckpt=ck)
+
+    def sliced(t, at, width):
+        w = torch.full((n, s, width), float("nan"), dtype=t.dtype, device="cuda")
+        w[..., at:at + c] = t
+        return w[..., at:at + c]
+
+    width = c + 6 + (c + 1) % 2                       # odd
+    k.x, k.dy = sliced(k.x, 1, width), sliced(k.dy, 3, width + 2)
+    y, dx = sliced(torch.zeros_like(fwd[0]), 2, width), sliced(torch.zeros_like(fwd[0]), 5, width)
+    ck2 = lags.checkpoint(n * s, c)
+    for a, b in zip(k.forward(ck2, y=y), fwd):
+        assert torch.equal(a, b)
+    used = lags.lags_ckpt_bytes(n * s, c) // 16 * 16 - 16
+    assert torch.equal(ck[:used], ck2[:used])
+    for src, want in (({"x": k.x}, bwd[0]), ({"ckpt": ck2}, bwd[1])):
+        dx.zero_()
+        for a, b in zip(k.backward(fwd[1], fwd[2], dx=dx, **src), want):
+            assert torch.equal(a, b)
+    for t in (y, dx):
+        whole = torch.as_strided(t, (n, s, width), (s * width, width, 1), 0)
+        assert int(torch.isnan(whole).sum()) == n * s * (width - c)
+
+
+@pytest.mark.parametrize("n,s,c,groups", [(70000, 64, 512, 32), (40, 1 << 20, 64, 8)])
+def test_group_norm_past_32_bits(n, s, c, groups):
+    """More than 2^31 elements, in short samples and in long ones: first and last samples against
+    float64, the parameters' gradients against sums on the device."""
+    import torch
+
+    import act_reference as R
+    from layer_wise_top_amd import lags
+    assert n * s * c > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, dy = torch.empty(n, s, c, dtype=torch.bfloat16, device="cuda"), torch.empty(n, s, c, dtype=torch.bfloat16, device="cuda")
+    for t in (x, dy):
+        t.normal_(generator=g)
+    gamma, beta = torch.randn(c, generator=g, device="cuda"), torch.randn(c, generator=g, device="cuda")
+    gn = lags.GroupNorm(n, s, c, groups, dtype=torch.bfloat16, act="none")
+    ws, ck = lags.gn_workspace(gn), lags.checkpoint(n * s, c)
+    y, mean, rstd = torch.full_like(x, 9.0), torch.empty(n, groups, device="cuda"), torch.empty(n, groups, device="cuda")
+    print("forward", (n, s, c), flush=True)
+    lags.lags_gn_forward(gn, x, gamma, beta, y, mean, rstd, ws, ckpt=ck)
+    rows = min(s, 4096)
+    at = [0, n // 2 + 1, n - 1]
+    want_mean, want_rstd = [], []
+    for i in at:
+        xi = x[i].double().view(s, groups, c // groups)
+        m = xi.mean(dim=(0, 2))
+        r = 1 / torch.sqrt(((xi - m[:, None]) ** 2).mean(dim=(0, 2)) + 1e-5)
+        # sums of s * c / groups terms near 1 in chains of at most 1100 additions
+        assert ((mean[i].double() - m).abs() <= 1100 * R.U).all() and ((rstd[i].double() - r).abs() <= 1100 * R.U).all()
+        z = (x[i, -rows:].double() - m.repeat_interleave(c // groups)) * r.repeat_interleave(c // groups) * gamma + beta
+        assert ((y[i, -rows:].double() - z).abs() <= 2.0 ** -8 * z.abs() + 1e-3).all()
+    dx, dg, db = y.fill_(9.0), torch.empty(c, device="cuda"), torch.empty(c, device="cuda")
+    for src in ({"x": x}, {"ckpt": ck}):
+        dx.fill_(9.0)
+        print("backward", list(src), flush=True)
+        lags.lags_gn_backward(gn, dy, gamma, beta, mean, rstd, dx, dg, db, ws, **src)
+        sb, sg, mb, mg = (torch.zeros(c, dtype=torch.float64, device="cuda") for _ in range(4))
+        step = max(1, (1 << 26) // (s * c))
+        held = torch.empty(min(step, n), s, c, device="cuda") if "ckpt" in src else None
+        for i in range(0, n, step):
+            d = dy[i:i + step].double()
+            if held is None:
+                v = x[i:i + step].double()
+            else:                                       # the same rows packed by themselves
+                part, out = x[i:i + step], held[:min(step, n - i)]
+                pc = lags.checkpoint(part.shape[0] * s, c)
+                lags.lags_ckpt_pack(part, pc)
+                lags.lags_ckpt_unpack(pc, out)
+                v = out.double()
+            cg = c // groups
+            m = mean[i:i + step].double().repeat_interleave(cg, 1)[:, None]
+            r = rstd[i:i + step].double().repeat_interleave(cg, 1)[:, None]
+            xh = (v - m) * r
+            sb, sg, mb, mg = sb + d.sum((0, 1)), sg + (d * xh).sum((0, 1)), mb + d.abs().sum((0, 1)), mg + (d * xh).abs().sum((0, 1))
+            if i == 0 or i + step >= n:                 # the last sample (or the first) in full
+                j = 0 if i == 0 else d.shape[0] - 1
+                dz, h = gamma * d[j], xh[j]
+
+                def mean_g(t):
+                    return t.view(s, groups, cg).mean((0, 2)).repeat_interleave(cg)
+                w = r[j] * (dz - mean_g(dz) - h * mean_g(dz * h))
+                got = dx[i + j].double()
+                assert ((got - w).abs() <= 2.0 ** -8 * w.abs() + 1e-3).all(), (list(src), i + j)
+            del d, v, xh
+        # chains of at most 2100 additions
+        assert ((db.double() - sb).abs() <= 2100 * R.U * mb).all() and ((dg.double() - sg).abs() <= 2100 * R.U * mg).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_weight_gradient_past_32_bits(dtype):
+    """dY of more than 2^31 elements: values in the first and the last rows alone, so that the product is
+    theirs."""
+    import torch
+
+    import act_reference as R
+    from layer_wise_top_amd import lags
+    m, o, c = (1 << 21) + 77, 1030, 64
+    assert m * o > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dy = torch.zeros(m, o, dtype=getattr(torch, "bfloat16" if dtype == "bf16" else "float32"), device="cuda")
+    x = torch.randn(m, c, generator=g, device="cuda")
+    for part in (dy[:200], dy[m // 2:m // 2 + 100], dy[-300:]):
+        part.normal_(generator=g)
+    ck, val = lags.checkpoint(m, c), torch.empty_like(x)
+    lags.lags_ckpt_pack(x, ck)
+    lags.lags_ckpt_unpack(ck, val)
+    dw = torch.full((o, c), 9.0, device="cuda")
+    lags.lags_ckpt_wgrad(dy, ck, dw, lags.wgrad_workspace(m, o, c, dy.dtype))
+    d, v = (torch.cat([t[:200], t[m // 2:m // 2 + 100], t[-300:]]).double() for t in (dy, val))
+    d = d.t().contiguous()
+    want, mag = d @ v, d.abs() @ v.abs()
+    assert ((dw.double() - want).abs() <= (600 / 16 + 64) * R.U * mag).all()
 
 
 def test_group_norm_of_more_samples_than_a_launch_has_threads():
