@@ -24,9 +24,10 @@ uint32_t gcd(uint32_t a, uint32_t b) { return b ? gcd(b, a % b) : a; }
 namespace lags {
 // Register rows a thread of a resident workgroup aims at.  Forward 13: 28 x 28
 // positions by 64 bf16 channels in 512 threads, two workgroups a compute unit
-// (26 us for 64 x 784 x 512; 8 rows in 1024 threads: 28 us).  Backward 8, which
-// leaves the registers for two workgroups (41 us; 13: 46 us), but 13 with silu,
-// whose own registers 8 rows would spill (51 us; 8: 56 us).
+// (26 us for 64 x 784 x 512; 8 rows in 1024 threads: 28 us).  Backward 8, but 13
+// with silu: by time, since both spill a few registers (64 x 784 x 512 bf16, 8
+// and 13 rows: relu from the checkpoint 41.1 and 42.1 us, from x 50.6 and 50.7;
+// silu from the checkpoint 56.7 and 51.0, from x 61.8 and 59.5).
 static uint32_t rows_aimed_at(bool backward, int act) { return backward && act != kActSilu ? 8 : kMostRows; }
 
 GnPlan gn_plan(int dtype, int act, bool backward, uint64_t N, uint64_t S, uint32_t C, uint32_t G)

@@ -254,8 +254,9 @@ template <typename F> hipError_t by_act(int act, F f)
     if (act == kActSilu) return f(std::integral_constant<int, kActSilu>());
     return f(std::integral_constant<int, kActNone>());
 }
-// The kernel for at least `rows` register rows of those for 2, 4, 8 and 13
-// (56 x 56 positions by 256 rows of lanes, 28 x 28 by 64).
+// The kernel for at least `rows` register rows of those for 2, 4, 8 and 13:
+// rows are cheapest where all are used (absent ones read zeros), and 13 rows of
+// two vectors are what a backward thread holds at three waves a SIMD.
 template <typename F> hipError_t by_rows(uint32_t rows, F f)
 {
     if (rows <= 2) return f(std::integral_constant<int, 2>());

@@ -92,12 +92,15 @@ __device__ inline uint32_t deal(uint32_t b, uint32_t n)
 // of LDS between this step's products.  Few rows and outputs are bound by
 // latency, many rows by memory, large products by the LDS reads that feed the
 // matrix instructions and the clock that the card holds under them:
-//   16384 x 8192 x 2048 bf16   480-490 us, 1.13 PFLOP/s (256 x 256, 64 rows
-//                              staged; matrix instructions in 51 % of the cycles)
+//   16384 x 8192 x 2048 bf16   460-490 us, 1.12 to 1.19 PFLOP/s (256 x 256, 64 rows
+//                              staged; matrix instructions in 52 % of the cycles);
+//                              560 us in the first launches after an idle second
+//   8192 x 8192 x 2048 fp16    470-485 us, 1.14 to 1.17 PFLOP/s in two terms (the
+//                              256 x 256 kernel spills 5 registers)
 //   700 x 6000 x 1500 fp32     50 us, 0.75 PFLOP/s in three terms (192 x 256 on
 //                              192 of 256 compute units; 256 x 256 leaves 112 idle)
-//   200704 x 256 x 64 bf16     27 us, 4.6 TB/s (64 x 64, 126 slices)
-//   2048 x 64 x 32 fp32        5.6 us
+//   200704 x 256 x 64 bf16     24-27 us, 4.6 to 5.1 TB/s (64 x 64, 126 slices)
+//   2048 x 64 x 32 fp32        5.5 us
 template <int D, int BO, int BC, int WR, int WC, int K, bool ODD>
 __global__ __launch_bounds__(64 * WR * WC) void k_wgrad(WgradArgs a)
 {
