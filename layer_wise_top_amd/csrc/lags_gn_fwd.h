@@ -132,7 +132,10 @@ __global__ __launch_bounds__(kResident) void k_gn_fwd(GnArgs a)
 // positions, each channel's distances from its first value there and their
 // squares.  That value being one of the data, what its distance from the mean
 // costs in digits is bounded: a relative error of the thread's count of
-// positions times fp32's rounding.
+// positions times fp32's rounding.  Zero stands for a first value of 2^96 or
+// more (a type's lowest value as a mask), distances from which would add up
+// past fp32; squares that do leave a variance of infinity, as in the resident
+// form, not infinity less infinity.
 template <int D, bool ODD, bool UNI> __global__ __launch_bounds__(1024) void k_gn_stats(GnArgs a)
 {
     constexpr int V = Elem<D>::V, U = kSweep;
@@ -147,7 +150,10 @@ template <int D, bool ODD, bool UNI> __global__ __launch_bounds__(1024) void k_g
         u32x4 raw[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) raw[k] = rx.load(g.row + k * g.tr);
-        if (s0 == 0) Elem<D>::unpack(raw[0], first);
+        if (s0 == 0) {
+            Elem<D>::unpack(raw[0], first);
+            for (int j = 0; j < V; ++j) first[j] = __builtin_fabsf(first[j]) < 0x1p96f ? first[j] : 0.0f;
+        }
 #pragma unroll
         for (int k = 0; k < U; ++k)
             if (s0 + g.row + k * g.tr < rows) {
@@ -167,7 +173,8 @@ template <int D, bool ODD, bool UNI> __global__ __launch_bounds__(1024) void k_g
     float mean[V], t[V];
     for (int j = 0; j < V; ++j) {
         const float d = s1[j] * inv;
-        s2[j] = above_zero(s2[j] - s1[j] * d);
+        const float q = s1[j] * d;
+        if (q < __builtin_inff()) s2[j] = above_zero(s2[j] - q);     // else s2 is infinite or NaN
         mean[j] = first[j] + d;
         t[j] = cm * mean[j];
     }

@@ -307,3 +307,36 @@ def test_weight_gradient_of_small_fp32_values():
     print("relative error by exponent", {int(k): float((off / want)[e == k].max()) for k in np.unique(e)}, flush=True)
     assert (off[e >= -110] <= 3 * 2.0 ** -24 * want[e >= -110]).all()
     assert (off <= 3 * 2.0 ** -24 * want + 2.0 ** (-133 + 60)).all()
+
+
+@pytest.mark.parametrize("n,s", [(3, 30), (2, 9000)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("at", [0, 1, 4000])
+def test_group_norm_with_the_lowest_value(dtype, n, s, at):
+    """One value of a group is the type's lowest (a mask), resident and in chunks, at a thread's first
+    position and later: its square is past fp32, so the variance is infinite, rstd 0 and y act(beta);
+    the mean is finite.  So are the gradients; other groups keep their bits."""
+    import numpy as np
+    import torch
+
+    import act_reference as R
+    k = Case(n, s, 64, 8, dtype, "silu", seed=5)
+    clean = k.forward()
+    at %= s
+    lowest = torch.finfo(k.x.dtype).min
+    k.x[0, at, 9] = lowest
+    y, mean, rstd = k.forward()
+    for t in (y, mean, rstd):
+        assert torch.isfinite(t).all()
+    assert rstd[0, 1] == 0
+    want = lowest / (8 * s)                       # the others' part is far below its rounding
+    assert abs(float(mean[0, 1]) - want) <= 1e-5 * abs(want)
+    flat = R.act(k.b64, "silu")[8:16]
+    assert np.abs(y[0, :, 8:16].double().cpu().numpy() - flat).max() <= 2.0 ** -7 * np.abs(flat).max()
+    keep = torch.ones(n, 8, dtype=torch.bool, device="cuda")
+    keep[0, 1] = False
+    assert torch.equal(mean[keep], clean[1][keep]) and torch.equal(rstd[keep], clean[2][keep])
+    wide = keep.repeat_interleave(8, 1)[:, None, :].expand(n, s, 64)
+    assert torch.equal(y[wide], clean[0][wide])
+    for t in k.backward(mean, rstd, x=k.x):
+        assert torch.isfinite(t).all()
