@@ -390,10 +390,12 @@ const char *lags_kernel_name(int32_t id);
 #define LAGS_ACT_NONE 0
 #define LAGS_ACT_RELU 1 /* max(z, 0); gradient 0 at 0 */
 #define LAGS_ACT_SILU 2 /* z / (1 + exp(-z)) */
+#define LAGS_ACT_GELU 3 /* z / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3); linear layers only */
 #define LAGS_GRAD_ADD 1u /* add to the gradient buffer instead of overwriting it */
 #define LAGS_CKPT_RUN 32 /* columns of a row that share a scale */
 #define LAGS_SLAB_MAX 4096 /* see lags_gn */
 #define LAGS_GN_MAX (1 << 18) /* channels and pitches of lags_gn */
+#define LAGS_LN_MAX 16384 /* channels of lags_ln */
 #define LAGS_WGRAD_MAX (1 << 22) /* outs, cols and lddy of lags_ckpt_wgrad */
 
 /*
@@ -512,6 +514,67 @@ size_t lags_ckpt_wgrad_workspace_bytes(int64_t rows, int64_t outs, int64_t cols,
 int lags_ckpt_wgrad(int64_t rows, int64_t outs, int64_t cols, const void *dy, int64_t lddy,
                     int32_t dtype, const void *ckpt, size_t ckpt_bytes, float *dw, uint32_t flags,
                     void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Layer normalisation over the channels of each row, with the residual stream
+ * that a branch is added to in the same pass:
+ *   s = x + res, rounded to dtype (s = x without res);
+ *   mean, rstd: per row; rstd = 1 / sqrt(variance + eps), variance over the count;
+ *   y = (s - mean) * rstd * gamma + beta.
+ * Up to LAGS_LN_MAX channels, every ld <= LAGS_GN_MAX, rows in [0, 2^31), eps >= 0 and
+ * finite.  (lags_gn with spatial = 1 and groups = 1 computes the same without
+ * the stream, with an activation, and not as fast.)
+ */
+typedef struct lags_ln {
+    int64_t rows, channels;
+    int32_t dtype; /* of every matrix */
+    float eps;
+} lags_ln;
+
+/* Bytes of workspace of lags_ln_backward (at least 16; at most 1024 workgroups'
+ * channel sums, eight bytes a channel); 0 for an invalid shape. */
+size_t lags_ln_workspace_bytes(const lags_ln *ln);
+
+/*
+ * y, and what the backward needs.
+ *   x, res:      device matrices (ldx, ldr); res may be null;
+ *   sum:         device matrix out (lds): s; null without res, and may be null with it;
+ *   y:           device matrix out (ldy);  sum and y may each be x or res
+ *                itself (same pointer and ld), but not one another;
+ *   gamma, beta: device fp32[channels]; both null stand for 1 and 0;
+ *   mean, rstd:  device fp32[rows], out; each may be null;
+ *   ckpt, yckpt: null, or checkpoint buffers that receive s, and y (the input
+ *                that lags_ckpt_wgrad of the layer behind this one takes).
+ * With rows 0 nothing is launched.  No workspace.
+ * Returns LAGS_OK, LAGS_EINVAL (null or misaligned pointer, bad shape or ld,
+ * sum without res, one of gamma and beta null, buffers that overlap), LAGS_ERANGE,
+ * LAGS_EWORKSPACE (a checkpoint misaligned or small), LAGS_EHIP.
+ */
+int lags_ln_forward(const lags_ln *ln, const void *x, int64_t ldx, const void *res, int64_t ldr,
+                    const float *gamma, const float *beta, void *sum, int64_t lds, void *y,
+                    int64_t ldy, float *mean, float *rstd, void *ckpt, size_t ckpt_bytes,
+                    void *yckpt, size_t yckpt_bytes, void *stream);
+
+/*
+ * Gradients of the forward call for the gradient dy of y:
+ *   g = gamma * dy;  xh = (s - mean) * rstd;
+ *   dx = rstd * (g - <g> - xh <g xh>) + dsum, < > the mean over the row;
+ *   dgamma = sum dy * xh, dbeta = sum dy, over the rows.
+ *   x or ckpt:     s, or its checkpoint: exactly one is not null;
+ *   gamma:         may be null (1);  mean, rstd: as the forward left them;
+ *   dsum:          null, or the gradient that reaches s from elsewhere (ldds);
+ *   dx:            device matrix out (lddx): the gradient of s, and so of x and
+ *                  of res; may be dy or dsum itself;
+ *   dgamma, dbeta: device fp32[channels], out; each may be null;
+ *   flags:         0 or LAGS_GRAD_ADD (dgamma and dbeta are added to).
+ * With rows 0 dgamma and dbeta become 0 (unless added to).
+ * Returns as lags_ln_forward, and LAGS_EWORKSPACE for ws.
+ */
+int lags_ln_backward(const lags_ln *ln, const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                     const void *ckpt, size_t ckpt_bytes, const float *gamma, const float *mean,
+                     const float *rstd, const void *dsum, int64_t ldds, void *dx, int64_t lddx,
+                     float *dgamma, float *dbeta, uint32_t flags, void *ws, size_t ws_bytes,
+                     void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,6 +1,7 @@
 // Host side of the activation operators: argument validation, workspace sizes
 // and launches.  The entry points are declared in include/lags.h.
 #include "lags.h"
+#include "lags_args.h"
 #include "lags_gn.h"
 
 #include <algorithm>
@@ -117,57 +118,10 @@ size_t gn_part_floats(const GnPlan &p, bool backward, uint64_t N, uint32_t C, ui
 
 namespace {
 
-typedef unsigned __int128 u128;
-constexpr int64_t kMaxDim = 0x7fffffff;
-constexpr u128 kMaxBytes = (u128)1 << 62;
-
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-bool known_dtype(int32_t d) { return d == LAGS_F32 || d == LAGS_BF16 || d == LAGS_F16; }
-
-// A strided region of device memory: `rows` runs of `width` bytes, `pitch` bytes apart.
-struct Region {
-    const void *p;
-    u128 rows, width, pitch;
-    u128 bytes() const { return rows ? (rows - 1) * pitch + width : 0; }
-};
-
-Region flat(const void *p, size_t bytes) { return {p, 1, bytes, bytes}; }
-
-// Columns of one buffer taken at the same pitch do not overlap where their
-// columns do not; regions of unlike pitch count as overlapping where their
-// address ranges meet.
-bool overlap(const Region &a, const Region &b)
-{
-    if (!a.p || !b.p || !a.bytes() || !b.bytes()) return false;
-    const u128 x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    if (x + a.bytes() <= y || y + b.bytes() <= x) return false;
-    if (a.pitch != b.pitch || a.rows < 2 || b.rows < 2) return true;
-    // the later column's distance past the earlier one, within a row
-    const u128 d = x <= y ? (y - x) % a.pitch : (a.pitch - (x - y) % a.pitch) % a.pitch;
-    return d < a.width || d + b.width > a.pitch;
-}
-
-// A [rows, cols] matrix argument: its region, or a status.
-int matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype, Region &r)
-{
-    const uint32_t e = elem_bytes(dtype);
-    if (!p || !aligned(p, e) || ld < cols) return LAGS_EINVAL;
-    if (ld > kMaxDim || (u128)rows * (u128)ld * e > kMaxBytes) return LAGS_ERANGE;
-    r = {p, (u128)rows, (u128)cols * e, (u128)ld * e};
-    return LAGS_OK;
-}
-
-bool ckpt_dims(int64_t rows, int64_t cols)
-{
-    return rows >= 0 && cols >= 1 && cols <= kMaxDim && (u128)rows * (u128)(cols + 64) * 2 <= kMaxBytes;
-}
-
 bool wgrad_dims(int64_t rows, int64_t outs, int64_t cols)
 {
     return ckpt_dims(rows, cols) && cols <= LAGS_WGRAD_MAX && outs >= 1 && outs <= LAGS_WGRAD_MAX;
 }
-
-int hip(hipError_t e) { return e == hipSuccess ? LAGS_OK : LAGS_EHIP; }
 
 int check_pack(int64_t rows, int64_t cols, const void *x, int64_t ldx, int32_t dtype, const void *ckpt,
                size_t ckpt_bytes)
@@ -226,16 +180,6 @@ void fill(const lags_gn *gn, const GnPlan &p, GnArgs &a)
     a.w = p.w, a.nslab = p.nslab, a.tcl = p.tcl, a.nchunk = p.nchunk, a.chunk = p.chunk;
     a.nper = p.nper, a.nparts = p.nparts;
 }
-
-// `out` must not overlap any of the n regions of `all` but itself.
-bool clear_of(const Region *all, int n, int out)
-{
-    for (int i = 0; i < n; ++i)
-        if (i != out && overlap(all[i], all[out])) return false;
-    return true;
-}
-
-bool same(const Region &a, const Region &b) { return a.p == b.p && a.pitch == b.pitch; }
 
 }  // namespace
 

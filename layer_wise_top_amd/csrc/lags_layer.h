@@ -1,0 +1,44 @@
+// Argument blocks and launches of the layer operators (layer normalisation,
+// linear layers, embeddings).  Not part of the public ABI.
+#pragma once
+
+#include "lags_act.h"
+
+namespace lags {
+
+enum : int { kActGelu = 3 };                 // LAGS_ACT_GELU
+
+// ---- layer normalisation ---------------------------------------------------
+struct LnArgs {
+    const void *x, *res, *dy, *dsum;
+    void *sum, *y, *dx;
+    int64_t ldx, ldr, lddy, ldds, lds, ldy, lddx;
+    const uint8_t *rcodes, *rscales;         // checkpoint read (backward)
+    uint8_t *wcodes, *wscales;               // checkpoint of the normalised rows, written (forward)
+    uint8_t *ycodes, *yscales;               // checkpoint of y, written (forward)
+    const float *gamma, *beta;
+    float *mean, *rstd, *dgamma, *dbeta, *part;
+    float eps, inv_c;
+    int64_t rows;
+    uint32_t C, pitch, nrun;
+    uint32_t add;
+    uint32_t tl;                             // 2^tl lanes a row
+};
+struct LnPlan {
+    uint32_t tl, nv;                         // 2^tl lanes a row, vectors a lane
+    uint32_t threads, groups;                // threads a workgroup, workgroups
+};
+constexpr int64_t kLnMax = 16384;            // channels, at most: 1024 threads of 16 values
+// What the edges of rows ask for: nothing (whole vectors from whole words), columns past the last
+// one to be cleared, or also words to be shifted into place (rows of 16-bit values that start inside one).
+enum : int { kWhole = 0, kRagged = 1, kShifted = 2 };
+LnPlan ln_plan(int dtype, bool backward, int edge, int64_t rows, uint32_t C);
+hipError_t launch_ln_forward(const LnPlan &p, LnArgs a, int dtype, int edge, hipStream_t s);
+hipError_t launch_ln_backward(const LnPlan &p, LnArgs a, int dtype, int edge, hipStream_t s);
+
+// dgamma, dbeta: sums over `rows` rows of part [rows][2][C] (dbeta's sums
+// first), in a fixed order; either may be null (lags_gn.hip).
+hipError_t launch_params(const float *part, uint32_t rows, uint32_t C, float *dgamma, float *dbeta, uint32_t add,
+                         hipStream_t s);
+
+}  // namespace lags

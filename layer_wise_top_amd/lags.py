@@ -32,6 +32,7 @@ EXPORTED = (
     "lags_workspace_init", "lags_sparsify_layers_static", "lags_ckpt_bytes", "lags_ckpt_pack",
     "lags_ckpt_unpack", "lags_gn_workspace_bytes", "lags_gn_forward", "lags_gn_backward",
     "lags_ckpt_wgrad_workspace_bytes", "lags_ckpt_wgrad",
+    "lags_ln_workspace_bytes", "lags_ln_forward", "lags_ln_backward",
 )
 
 LAGS_F32, LAGS_BF16, LAGS_F16 = 0, 1, 2
@@ -58,6 +59,12 @@ class GnShape(ctypes.Structure):
     _fields_ = [("samples", ctypes.c_int64), ("spatial", ctypes.c_int64),
                 ("channels", ctypes.c_int64), ("groups", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class LnShape(ctypes.Structure):
+    """lags_ln"""
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -146,6 +153,14 @@ def lib():
     L.lags_ckpt_wgrad_workspace_bytes.argtypes = [i64, i64, i64, i32]
     L.lags_ckpt_wgrad.restype = ctypes.c_int
     L.lags_ckpt_wgrad.argtypes = [i64, i64, i64, vp, i64, i32, vp, sz, vp, u32, vp, sz, vp]
+    ln = ctypes.POINTER(LnShape)
+    L.lags_ln_workspace_bytes.restype = sz
+    L.lags_ln_workspace_bytes.argtypes = [ln]
+    L.lags_ln_forward.restype = ctypes.c_int
+    L.lags_ln_forward.argtypes = [ln, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp, vp, sz, vp, sz, vp]
+    L.lags_ln_backward.restype = ctypes.c_int
+    L.lags_ln_backward.argtypes = [ln, vp, i64, vp, i64, vp, sz, vp, vp, vp, vp, i64, vp, i64, vp, vp, u32, vp, sz,
+                                   vp]
     _lib = L
     return L
 
@@ -614,3 +629,73 @@ def lags_ckpt_wgrad(dy, ckpt, dw, ws, add: bool = False, stream=None):
     rc = lib().lags_ckpt_wgrad(rows, outs, dw.shape[1], pdy, lddy, _dtype_code(dy.dtype), pc, nc,
                                _vector(dw, dev, 0, "dw"), LAGS_GRAD_ADD if add else 0, pw, nw, s)
     _check("lags_ckpt_wgrad", rc)
+
+
+# ---- layer operators ---------------------------------------------------------
+
+def _opt_matrix(t, dev: int, name: str, dtype, rows: int, cols: int):
+    """(pointer, ld) of a matrix argument that may be None."""
+    if t is None:
+        return None, 0
+    p, _, _, ld = _matrix(t, dev, name, dtype, rows, cols)
+    return p, ld
+
+
+class LayerNorm:
+    """A layer normalisation's shape (lags_ln): `rows` rows of `channels`."""
+
+    def __init__(self, rows: int, channels: int, dtype=None, eps: float = 1e-5):
+        import torch
+        self.dtype = dtype if dtype is not None else torch.float32
+        self.shape = LnShape(int(rows), int(channels), _dtype_code(self.dtype), float(eps))
+        self.ref = ctypes.byref(self.shape)
+        self.rows, self.channels = int(rows), int(channels)
+
+    def workspace_bytes(self) -> int:
+        return int(lib().lags_ln_workspace_bytes(self.ref))
+
+
+def ln_workspace(ln: LayerNorm, device=None):
+    """Allocate a workspace for lags_ln_backward of this shape."""
+    import torch
+    nbytes = ln.workspace_bytes()
+    if nbytes == 0:
+        raise ValueError("invalid or unsupported layer normalisation shape")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def lags_ln_forward(ln: LayerNorm, x, gamma, beta, y, mean, rstd, res=None, sum=None, ckpt=None, yckpt=None,
+                    stream=None):
+    """y = layernorm(s), s = x (+ res, rounded and written to sum); mean, rstd [rows] (or None); ckpt, yckpt:
+    checkpoint buffers that receive s and y in the same pass."""
+    dev, s = _place(x, "x", stream)
+    r, c = ln.rows, ln.channels
+    px, _, _, ldx = _matrix(x, dev, "x", ln.dtype, r, c)
+    py, _, _, ldy = _matrix(y, dev, "y", ln.dtype, r, c)
+    pr, ldr = _opt_matrix(res, dev, "res", ln.dtype, r, c)
+    ps, lds = _opt_matrix(sum, dev, "sum", ln.dtype, r, c)
+    pc, nc = _buffer(ckpt, dev, "ckpt")
+    pk, nk = _buffer(yckpt, dev, "yckpt")
+    rc = lib().lags_ln_forward(
+        ln.ref, px, ldx, pr, ldr, _vector(gamma, dev, c, "gamma"), _vector(beta, dev, c, "beta"), ps, lds, py, ldy,
+        _vector(mean, dev, r, "mean"), _vector(rstd, dev, r, "rstd"), pc, nc, pk, nk, s)
+    _check("lags_ln_forward", rc)
+
+
+def lags_ln_backward(ln: LayerNorm, dy, gamma, mean, rstd, dx, dgamma, dbeta, ws, x=None, ckpt=None, dsum=None,
+                     add: bool = False, stream=None):
+    """dx (plus dsum, the gradient that reaches the stream from elsewhere), and dgamma and dbeta (each may be
+    None), from dy and the normalised rows x or their checkpoint."""
+    dev, s = _place(dy, "dy", stream)
+    r, c = ln.rows, ln.channels
+    pdy, _, _, lddy = _matrix(dy, dev, "dy", ln.dtype, r, c)
+    pdx, _, _, lddx = _matrix(dx, dev, "dx", ln.dtype, r, c)
+    px, ldx = _opt_matrix(x, dev, "x", ln.dtype, r, c)
+    pd, ldd = _opt_matrix(dsum, dev, "dsum", ln.dtype, r, c)
+    pw, nw = _buffer(ws, dev, "ws")
+    pc, nc = _buffer(ckpt, dev, "ckpt")
+    rc = lib().lags_ln_backward(
+        ln.ref, pdy, lddy, px, ldx, pc, nc, _vector(gamma, dev, c, "gamma"), _vector(mean, dev, r, "mean"),
+        _vector(rstd, dev, r, "rstd"), pd, ldd, pdx, lddx, _vector(dgamma, dev, c, "dgamma"),
+        _vector(dbeta, dev, c, "dbeta"), LAGS_GRAD_ADD if add else 0, pw, nw, s)
+    _check("lags_ln_backward", rc)

@@ -1,0 +1,105 @@
+"""The layer operators' host side: sizes and refusals, all before any HIP call."""
+import ctypes
+
+import pytest
+
+from layer_wise_top_amd import lags
+
+OK, EINVAL, ERANGE, EWS = 0, -1, -2, -3
+BASE = 1 << 40                                  # never dereferenced
+
+
+def P(i):
+    return BASE + (i << 34)
+
+
+def _ln(m=40, c=64, dtype=1, eps=1e-5):
+    return lags.LnShape(m, c, dtype, eps)
+
+
+BAD_LN = [(dict(dtype=3), EINVAL), (dict(dtype=-1), EINVAL), (dict(eps=-1.0), EINVAL), (dict(eps=float("nan")), EINVAL),
+          (dict(eps=float("inf")), EINVAL), (dict(m=-1), EINVAL), (dict(c=0), EINVAL), (dict(m=1 << 31), ERANGE),
+          (dict(c=16385), ERANGE)]
+
+
+def test_layer_norm_workspace():
+    L = lags.lib()
+    assert L.lags_ln_workspace_bytes(None) == 0
+    for kw, _ in BAD_LN:
+        assert L.lags_ln_workspace_bytes(ctypes.byref(_ln(**kw))) == 0, kw
+    for kw in (dict(), dict(m=0), dict(c=1), dict(m=(1 << 31) - 1, c=16384), dict(dtype=0, c=16384)):
+        need = L.lags_ln_workspace_bytes(ctypes.byref(_ln(**kw)))
+        assert 16 <= need <= 1024 * 8 * kw.get("c", 64), kw
+
+
+def test_layer_norm_forward_refusals():
+    L = lags.lib()
+    ln = _ln()
+    cb = lags.lags_ckpt_bytes(40, 64)
+
+    def call(s=ln, x=P(0), ldx=64, res=P(1), ldr=64, gamma=P(2), beta=P(3), sum=P(4), lds=64, y=P(5), ldy=64,
+             mean=P(6), rstd=P(7), ck=None, ckn=0, yck=None, yckn=0):
+        return L.lags_ln_forward(ctypes.byref(s) if s is not None else None, x, ldx, res, ldr, gamma, beta, sum, lds,
+                                 y, ldy, mean, rstd, ck, ckn, yck, yckn, None)
+    assert call(s=None) == EINVAL
+    for kw, rc in BAD_LN:
+        assert call(s=_ln(**kw), ldx=1 << 18, ldr=1 << 18, lds=1 << 18, ldy=1 << 18) == rc, kw
+    assert call(x=None) == EINVAL and call(y=None) == EINVAL and call(res=None) == EINVAL   # sum without res
+    for k in ("ldx", "ldr", "lds", "ldy"):
+        assert call(**{k: 63}) == EINVAL and call(**{k: (1 << 18) + 1}) == ERANGE, k
+    for k in ("x", "res", "sum", "y"):
+        assert call(**{k: P(9) + 1}) == EINVAL, k
+    assert call(gamma=None) == EINVAL and call(beta=None) == EINVAL
+    assert call(gamma=P(2) + 2) == EINVAL and call(mean=P(6) + 1) == EINVAL and call(rstd=P(7) + 2) == EINVAL
+    for a, n in (("ck", "ckn"), ("yck", "yckn")):
+        assert call(**{a: P(8), n: cb - 1}) == EWS and call(**{a: P(8) + 8, n: cb}) == EWS
+        assert call(**{a: P(0), n: cb}) == EINVAL and call(**{a: P(4), n: cb}) == EINVAL
+    assert call(ck=P(8), ckn=cb, yck=P(8), yckn=cb) == EINVAL
+    # sum and y may be x or res, whole, and not each other
+    assert call(y=P(4)) == EINVAL and call(y=P(0) + 64) == EINVAL and call(sum=P(1), lds=65) == EINVAL
+    assert call(y=P(2)) == EINVAL and call(sum=P(3)) == EINVAL and call(mean=P(7)) == EINVAL and call(rstd=P(5)) == EINVAL
+    assert call(x=P(0), ldx=128, y=P(0) + 126, ldy=128) == EINVAL
+    assert call(s=_ln(m=0)) == OK
+
+
+def test_layer_norm_backward_refusals():
+    L = lags.lib()
+    ln = _ln()
+    need, cb = L.lags_ln_workspace_bytes(ctypes.byref(ln)), lags.lags_ckpt_bytes(40, 64)
+
+    def call(s=ln, dy=P(0), lddy=64, x=P(1), ldx=64, ck=None, ckn=0, gamma=P(2), mean=P(3), rstd=P(4), dsum=P(5),
+             ldds=64, dx=P(6), lddx=64, dg=P(7), db=P(8), flags=0, ws=P(9), wsn=need):
+        return L.lags_ln_backward(ctypes.byref(s) if s is not None else None, dy, lddy, x, ldx, ck, ckn, gamma, mean,
+                                  rstd, dsum, ldds, dx, lddx, dg, db, flags, ws, wsn, None)
+    assert call(s=None) == EINVAL
+    for kw, rc in BAD_LN:
+        assert call(s=_ln(**kw), lddy=1 << 18, ldx=1 << 18, ldds=1 << 18, lddx=1 << 18) == rc, kw
+    assert call(flags=2) == EINVAL
+    assert call(x=None) == EINVAL and call(ck=P(10), ckn=cb) == EINVAL       # one source, not none or two
+    assert call(x=None, ck=P(10), ckn=cb - 1) == EWS and call(x=None, ck=P(10) + 4, ckn=cb) == EWS
+    assert call(dy=None) == EINVAL and call(dx=None) == EINVAL and call(mean=None) == EINVAL and call(rstd=None) == EINVAL
+    for k in ("lddy", "ldx", "ldds", "lddx"):
+        assert call(**{k: 63}) == EINVAL and call(**{k: (1 << 18) + 1}) == ERANGE, k
+    assert call(gamma=P(2) + 1) == EINVAL and call(dg=P(7) + 2) == EINVAL and call(db=P(8) + 1) == EINVAL
+    assert call(ws=None) == EWS and call(ws=P(9) + 8) == EWS and call(wsn=need - 1) == EWS
+    for out in ("dg", "db", "ws"):
+        for at in (0, 1, 2, 3, 4, 5, 6):
+            assert call(**{out: P(at)}) == EINVAL, (out, at)
+    for at in (1, 2, 3, 4, 7, 8, 9):
+        assert call(dx=P(at)) == EINVAL, at
+    assert call(dx=P(0) + 2) == EINVAL and call(dx=P(5), lddx=65) == EINVAL and call(dg=P(8)) == EINVAL
+    assert call(x=None, ck=P(10), ckn=cb, dx=P(10)) == EINVAL
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    x = torch.zeros(4, 8)
+    ln = lags.LayerNorm(4, 8)
+    with pytest.raises(TypeError):
+        lags.lags_ln_forward(ln, x, None, None, x, None, None)
+    with pytest.raises(TypeError):
+        lags.lags_ln_backward(ln, x, None, x, x, x, None, None, None, x=x)
+    with pytest.raises(TypeError):
+        lags.LayerNorm(4, 8, dtype=torch.int8)
+    with pytest.raises(ValueError):
+        lags.ln_workspace(lags.LayerNorm(4, 0))
