@@ -392,11 +392,13 @@ const char *lags_kernel_name(int32_t id);
 #define LAGS_ACT_SILU 2 /* z / (1 + exp(-z)) */
 #define LAGS_ACT_GELU 3 /* z / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3); linear layers only */
 #define LAGS_GRAD_ADD 1u /* add to the gradient buffer instead of overwriting it */
+#define LAGS_IDS64 2u /* ids are int64 (else int32) */
 #define LAGS_CKPT_RUN 32 /* columns of a row that share a scale */
 #define LAGS_SLAB_MAX 4096 /* see lags_gn */
 #define LAGS_GN_MAX (1 << 18) /* channels and pitches of lags_gn */
 #define LAGS_LN_MAX 16384 /* channels of lags_ln */
-#define LAGS_WGRAD_MAX (1 << 22) /* outs, cols and lddy of lags_ckpt_wgrad */
+#define LAGS_VOCAB_MAX (1 << 26) /* rows of an embedding table */
+#define LAGS_WGRAD_MAX (1 << 22) /* outs, cols and lddy of lags_ckpt_wgrad; cols of an embedding */
 
 /*
  * 8-bit checkpoint of a [rows, cols] matrix.  Each run of 32 columns of a row
@@ -575,6 +577,41 @@ int lags_ln_backward(const lags_ln *ln, const void *dy, int64_t lddy, const void
                      const float *rstd, const void *dsum, int64_t ldds, void *dx, int64_t lddx,
                      float *dgamma, float *dbeta, uint32_t flags, void *ws, size_t ws_bytes,
                      void *stream);
+
+/*
+ * Embedding: y[t] = scale * table[ids[t]], the product in fp32, rounded to dtype.  An
+ * id outside [0, vocab) (padding) gives a row of zeros.
+ *   ids:   device int32[tokens], or int64[tokens] with LAGS_IDS64;
+ *   table: device [vocab][cols], contiguous, of table_dtype: LAGS_F32 (the layer's
+ *          slice of the flat weights) or dtype;
+ *   scale: finite;
+ *   y:     device matrix out [tokens, cols] (ldy) of dtype;
+ *   flags: 0 or LAGS_IDS64.
+ * tokens in [0, 2^31) (0: nothing is launched), vocab in [1, LAGS_VOCAB_MAX], cols in
+ * [1, LAGS_WGRAD_MAX].
+ * Returns LAGS_OK, LAGS_EINVAL, LAGS_ERANGE, LAGS_EHIP.
+ */
+int lags_embed_forward(int64_t tokens, int64_t vocab, int64_t cols, const void *ids,
+                       const void *table, int32_t table_dtype, float scale, void *y, int64_t ldy,
+                       int32_t dtype, uint32_t flags, void *stream);
+
+/* Bytes of workspace of lags_embed_grad; 0 for invalid sizes. */
+size_t lags_embed_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols);
+
+/*
+ * Gradient of the table: dtable[v] = scale * sum of dy[t] over the tokens t with
+ * ids[t] = v, zeros where there is none.  Tokens whose id is outside [0, vocab) are
+ * left out, whatever their dy holds.
+ *   dy:     device matrix [tokens, cols] (lddy);
+ *   dtable: device fp32[vocab][cols], out, contiguous: the layer's slice of the
+ *           flat gradient;
+ *   flags:  LAGS_IDS64 and LAGS_GRAD_ADD (dtable is added to, and only the rows of
+ *           ids that occur are touched).
+ * Returns LAGS_OK, LAGS_EINVAL, LAGS_ERANGE, LAGS_EWORKSPACE, LAGS_EHIP.
+ */
+int lags_embed_grad(int64_t tokens, int64_t vocab, int64_t cols, const void *ids, const void *dy,
+                    int64_t lddy, int32_t dtype, float scale, float *dtable, uint32_t flags,
+                    void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

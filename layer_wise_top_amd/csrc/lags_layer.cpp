@@ -60,6 +60,28 @@ int checkpoint(const void *p, size_t bytes, int64_t rows, int64_t cols, Region &
     return LAGS_OK;
 }
 
+bool embed_dims(int64_t tokens, int64_t vocab, int64_t cols)
+{
+    return tokens >= 0 && tokens <= kMaxDim && vocab >= 1 && vocab <= LAGS_VOCAB_MAX && cols >= 1 &&
+           cols <= LAGS_WGRAD_MAX;
+}
+
+// Where a gradient's workspace keeps its parts.
+struct EmbedSpace {
+    size_t order, keys, start, part, bytes;
+};
+EmbedSpace embed_space(int64_t tokens, int64_t vocab, int64_t cols)
+{
+    auto up = [](size_t n) { return (n + 15) / 16 * 16; };
+    EmbedSpace w;
+    w.order = 0;
+    w.keys = up((size_t)tokens * 4);
+    w.start = w.keys + up((size_t)tokens * 4);
+    w.part = w.start + up(((size_t)vocab + 1) * 4);
+    w.bytes = w.part + up((size_t)embed_plan(LAGS_F32, tokens, vocab, cols).nchunk * 2 * cols * 4);
+    return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -151,6 +173,59 @@ int lags_ln_backward(const lags_ln *ln, const void *dy, int64_t lddy, const void
                                edge_of(dsum, ldds, C, ln->dtype)});
     const LnPlan p = ln_plan(ln->dtype, true, edge, R, (uint32_t)C);
     return hip(launch_ln_backward(p, a, ln->dtype, edge, (hipStream_t)stream));
+}
+
+size_t lags_embed_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols)
+{
+    return embed_dims(tokens, vocab, cols) ? embed_space(tokens, vocab, cols).bytes : 0;
+}
+
+int lags_embed_forward(int64_t tokens, int64_t vocab, int64_t cols, const void *ids, const void *table,
+                       int32_t table_dtype, float scale, void *y, int64_t ldy, int32_t dtype, uint32_t flags,
+                       void *stream)
+{
+    if (!known_dtype(dtype) || (table_dtype != LAGS_F32 && table_dtype != dtype)) return LAGS_EINVAL;
+    if ((flags & ~LAGS_IDS64) || !std::isfinite(scale)) return LAGS_EINVAL;
+    if (!embed_dims(tokens, vocab, cols)) return LAGS_ERANGE;
+    const bool wide = flags & LAGS_IDS64;
+    if (!ids || !aligned(ids, wide ? 8 : 4)) return LAGS_EINVAL;
+    Region t, m;
+    if (int rc = matrix(table, vocab, cols, cols, table_dtype, t); rc != LAGS_OK) return rc;
+    if (int rc = matrix(y, tokens, cols, ldy, dtype, m); rc != LAGS_OK) return rc;
+    if (overlap(m, t) || overlap(m, flat(ids, (size_t)tokens * (wide ? 8 : 4)))) return LAGS_EINVAL;
+    if (!tokens) return LAGS_OK;
+    EmbedArgs a = {};
+    a.ids = ids, a.table = table, a.y = y, a.ldy = ldy;
+    a.tokens = tokens, a.vocab = (uint32_t)vocab, a.cols = (uint32_t)cols, a.scale = scale;
+    return hip(launch_embed(a, table_dtype, dtype, wide, (hipStream_t)stream));
+}
+
+int lags_embed_grad(int64_t tokens, int64_t vocab, int64_t cols, const void *ids, const void *dy, int64_t lddy,
+                    int32_t dtype, float scale, float *dtable, uint32_t flags, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!known_dtype(dtype) || (flags & ~(LAGS_IDS64 | LAGS_GRAD_ADD)) || !std::isfinite(scale)) return LAGS_EINVAL;
+    if (!embed_dims(tokens, vocab, cols)) return LAGS_ERANGE;
+    const bool wide = flags & LAGS_IDS64;
+    if (!ids || !aligned(ids, wide ? 8 : 4) || !dtable || !aligned(dtable, 4)) return LAGS_EINVAL;
+    Region r[4];
+    if (int rc = matrix(dy, tokens, cols, lddy, dtype, r[0]); rc != LAGS_OK) return rc;
+    const EmbedPlan p = embed_plan(dtype, tokens, vocab, cols);
+    // threads of one launch
+    if ((u128)(p.sumwgs + vocab / 64 + 1) * 256 > kMostThreads || (u128)p.nchunk * p.njoin * 256 > kMostThreads)
+        return LAGS_ERANGE;
+    const EmbedSpace w = embed_space(tokens, vocab, cols);
+    if (!ws || !aligned(ws, 16) || ws_bytes < w.bytes) return LAGS_EWORKSPACE;
+    r[1] = flat(ids, (size_t)tokens * (wide ? 8 : 4)), r[2] = flat(dtable, (size_t)vocab * cols * 4), r[3] = flat(ws, w.bytes);
+    if (!clear_of(r, 4, 2) || !clear_of(r, 4, 3)) return LAGS_EINVAL;
+    if (!tokens && (flags & LAGS_GRAD_ADD)) return LAGS_OK;
+    EmbedArgs a = {};
+    a.ids = ids, a.dy = dy, a.lddy = lddy, a.dtable = dtable;
+    a.tokens = tokens, a.vocab = (uint32_t)vocab, a.cols = (uint32_t)cols, a.scale = scale;
+    a.add = flags & LAGS_GRAD_ADD;
+    char *b = (char *)ws;
+    a.order = (uint32_t *)(b + w.order), a.keys = (uint32_t *)(b + w.keys), a.start = (uint32_t *)(b + w.start);
+    a.part = (float *)(b + w.part);
+    return hip(launch_embed_grad(p, a, dtype, wide, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -36,6 +36,30 @@ LnPlan ln_plan(int dtype, bool backward, int edge, int64_t rows, uint32_t C);
 hipError_t launch_ln_forward(const LnPlan &p, LnArgs a, int dtype, int edge, hipStream_t s);
 hipError_t launch_ln_backward(const LnPlan &p, LnArgs a, int dtype, int edge, hipStream_t s);
 
+// ---- embeddings ------------------------------------------------------------
+struct EmbedArgs {
+    const void *ids, *table, *dy;
+    void *y;
+    int64_t ldy, lddy, tokens;
+    uint32_t vocab, cols;
+    float scale;
+    uint32_t add;
+    float *dtable;
+    // workspace: tokens by id, their ids, the ids' first places, chunks' sums [nchunk][2][cols]
+    uint32_t *order, *keys, *start;
+    float *part;
+    uint32_t w;                              // ids a workgroup of the sort
+    uint32_t nchunk, tl, nslab;              // chunks, 2^tl lanes a slab, slabs a row
+    uint32_t sumwgs, zl, njoin;              // workgroups of the sums; 2^zl lanes a row of zeros; 256-channel parts
+};
+struct EmbedPlan {
+    uint32_t w, nchunk, tl, nslab, njoin;
+    uint64_t sumwgs;
+};
+EmbedPlan embed_plan(int dtype, int64_t tokens, int64_t vocab, int64_t cols);
+hipError_t launch_embed(EmbedArgs a, int table, int dtype, bool wide, hipStream_t s);
+hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wide, hipStream_t s);
+
 // dgamma, dbeta: sums over `rows` rows of part [rows][2][C] (dbeta's sums
 // first), in a fixed order; either may be null (lags_gn.hip).
 hipError_t launch_params(const float *part, uint32_t rows, uint32_t C, float *dgamma, float *dbeta, uint32_t add,

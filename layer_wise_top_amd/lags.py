@@ -33,10 +33,12 @@ EXPORTED = (
     "lags_ckpt_unpack", "lags_gn_workspace_bytes", "lags_gn_forward", "lags_gn_backward",
     "lags_ckpt_wgrad_workspace_bytes", "lags_ckpt_wgrad",
     "lags_ln_workspace_bytes", "lags_ln_forward", "lags_ln_backward",
+    "lags_embed_forward", "lags_embed_workspace_bytes", "lags_embed_grad",
 )
 
 LAGS_F32, LAGS_BF16, LAGS_F16 = 0, 1, 2
 LAGS_GRAD_ADD = 1
+LAGS_IDS64 = 2
 LAGS_CKPT_RUN = 32
 LAGS_SLAB_MAX = 4096
 ACTS = {"none": 0, "relu": 1, "silu": 2}
@@ -161,6 +163,12 @@ def lib():
     L.lags_ln_backward.restype = ctypes.c_int
     L.lags_ln_backward.argtypes = [ln, vp, i64, vp, i64, vp, sz, vp, vp, vp, vp, i64, vp, i64, vp, vp, u32, vp, sz,
                                    vp]
+    L.lags_embed_forward.restype = ctypes.c_int
+    L.lags_embed_forward.argtypes = [i64, i64, i64, vp, vp, i32, ctypes.c_float, vp, i64, i32, u32, vp]
+    L.lags_embed_workspace_bytes.restype = sz
+    L.lags_embed_workspace_bytes.argtypes = [i64, i64, i64]
+    L.lags_embed_grad.restype = ctypes.c_int
+    L.lags_embed_grad.argtypes = [i64, i64, i64, vp, vp, i64, i32, ctypes.c_float, vp, u32, vp, sz, vp]
     _lib = L
     return L
 
@@ -699,3 +707,54 @@ def lags_ln_backward(ln: LayerNorm, dy, gamma, mean, rstd, dx, dgamma, dbeta, ws
         _vector(rstd, dev, r, "rstd"), pd, ldd, pdx, lddx, _vector(dgamma, dev, c, "dgamma"),
         _vector(dbeta, dev, c, "dbeta"), LAGS_GRAD_ADD if add else 0, pw, nw, s)
     _check("lags_ln_backward", rc)
+
+
+def _ids(t, dev: int):
+    """(pointer, count, flag) of a contiguous int32 or int64 device tensor of any shape."""
+    import torch
+    _on(t, dev, "ids")
+    if t.dtype is not torch.int64 and t.dtype is not torch.int32:
+        raise TypeError(f"ids must be {torch.int64} or {torch.int32}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    return t.data_ptr() or 16, t.numel(), LAGS_IDS64 if t.dtype is torch.int64 else 0
+
+
+def lags_embed_forward(ids, table, y, scale: float = 1.0, stream=None):
+    """y = scale * table[ids], rows of zeros where an id is outside the table.  table: [vocab, cols], fp32
+    or y's dtype, contiguous."""
+    dev, s = _place(y, "y", stream)
+    pi, n, f = _ids(ids, dev)
+    _on(table, dev, "table")
+    if table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous [vocab, cols] tensor")
+    vocab, cols = table.shape
+    py, _, _, ldy = _matrix(y, dev, "y", None, n, cols)
+    rc = lib().lags_embed_forward(n, vocab, cols, pi, table.data_ptr(), _dtype_code(table.dtype), scale, py, ldy,
+                                  _dtype_code(y.dtype), f, s)
+    _check("lags_embed_forward", rc)
+
+
+def embed_workspace(tokens: int, vocab: int, cols: int, device=None):
+    """Allocate a workspace for lags_embed_grad of these sizes."""
+    import torch
+    nbytes = int(lib().lags_embed_workspace_bytes(int(tokens), int(vocab), int(cols)))
+    if nbytes == 0:
+        raise ValueError("invalid embedding sizes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def lags_embed_grad(ids, dy, dtable, ws, scale: float = 1.0, add: bool = False, stream=None):
+    """dtable [vocab, cols] (fp32, contiguous: a layer's slice of the flat gradient): row v is scale times
+    the sum of dy over the tokens whose id is v."""
+    dev, s = _place(dy, "dy", stream)
+    pi, n, f = _ids(ids, dev)
+    _on(dtable, dev, "dtable")
+    if dtable.dim() != 2:
+        raise ValueError("dtable must be a [vocab, cols] tensor")
+    vocab, cols = dtable.shape
+    pdy, _, _, lddy = _matrix(dy, dev, "dy", None, n, cols)
+    pw, nw = _buffer(ws, dev, "ws")
+    rc = lib().lags_embed_grad(n, vocab, cols, pi, pdy, lddy, _dtype_code(dy.dtype), scale,
+                               _vector(dtable, dev, 0, "dtable"), f | (LAGS_GRAD_ADD if add else 0), pw, nw, s)
+    _check("lags_embed_grad", rc)

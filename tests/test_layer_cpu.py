@@ -91,6 +91,50 @@ def test_layer_norm_backward_refusals():
     assert call(x=None, ck=P(10), ckn=cb, dx=P(10)) == EINVAL
 
 
+BAD_EMBED = [(dict(t=-1), ERANGE), (dict(t=1 << 31), ERANGE), (dict(v=0), ERANGE), (dict(v=(1 << 26) + 1), ERANGE),
+             (dict(c=0), ERANGE), (dict(c=(1 << 22) + 1), ERANGE)]
+
+
+def test_embedding_forward_refusals():
+    L = lags.lib()
+
+    def call(t=40, v=100, c=64, ids=P(0), table=P(1), td=0, scale=1.0, y=P(2), ldy=64, dtype=1, flags=2):
+        return L.lags_embed_forward(t, v, c, ids, table, td, scale, y, ldy, dtype, flags, None)
+    for kw, rc in BAD_EMBED:
+        assert call(ldy=1 << 23, **kw) == rc, kw
+    assert call(dtype=3) == EINVAL and call(td=2) == EINVAL and call(td=3) == EINVAL and call(flags=1) == EINVAL
+    assert call(scale=float("nan")) == EINVAL and call(scale=float("inf")) == EINVAL
+    assert call(ids=None) == EINVAL and call(table=None) == EINVAL and call(y=None) == EINVAL
+    assert call(ids=P(0) + 4) == EINVAL and call(ids=P(0) + 2, flags=0) == EINVAL
+    assert call(table=P(1) + 2) == EINVAL and call(y=P(2) + 1) == EINVAL and call(ldy=63) == EINVAL
+    assert call(y=P(0)) == EINVAL and call(y=P(1) + 512) == EINVAL
+    assert call(t=0) == OK
+
+
+def test_embedding_gradient_refusals():
+    L = lags.lib()
+    for kw, _ in BAD_EMBED:
+        assert L.lags_embed_workspace_bytes(kw.get("t", 40), kw.get("v", 100), kw.get("c", 64)) == 0
+    need = L.lags_embed_workspace_bytes(40, 100, 64)
+    # order and ids, first places, two sums for each 32 tokens
+    assert need == 160 + 160 + 416 + 2 * 2 * 64 * 4
+
+    def call(t=40, v=100, c=64, ids=P(0), dy=P(1), lddy=64, dtype=1, scale=1.0, dt=P(2), flags=2, ws=P(3), wsn=need):
+        return L.lags_embed_grad(t, v, c, ids, dy, lddy, dtype, scale, dt, flags, ws, wsn, None)
+    for kw, rc in BAD_EMBED:
+        assert call(lddy=1 << 23, wsn=1 << 60, **kw) == rc, kw
+    assert call(dtype=3) == EINVAL and call(flags=4) == EINVAL and call(scale=float("nan")) == EINVAL
+    assert call(ids=None) == EINVAL and call(dy=None) == EINVAL and call(dt=None) == EINVAL
+    assert call(ids=P(0) + 4) == EINVAL and call(dt=P(2) + 2) == EINVAL and call(dy=P(1) + 1) == EINVAL
+    assert call(lddy=63) == EINVAL
+    assert call(ws=None) == EWS and call(ws=P(3) + 8) == EWS and call(wsn=need - 1) == EWS
+    assert call(dt=P(0)) == EINVAL and call(dt=P(1)) == EINVAL and call(dt=P(3)) == EINVAL
+    assert call(ws=P(0)) == EINVAL and call(ws=P(1)) == EINVAL
+    assert call(t=0, flags=3) == OK
+    # sums of more threads than one launch takes
+    assert call(t=(1 << 31) - 1, v=100, c=1 << 22, lddy=1 << 22, wsn=1 << 62) == ERANGE
+
+
 def test_binding_refuses_host_tensors():
     import torch
     x = torch.zeros(4, 8)
@@ -103,3 +147,9 @@ def test_binding_refuses_host_tensors():
         lags.LayerNorm(4, 8, dtype=torch.int8)
     with pytest.raises(ValueError):
         lags.ln_workspace(lags.LayerNorm(4, 0))
+    with pytest.raises(TypeError):
+        lags.lags_embed_forward(torch.zeros(4, dtype=torch.int64), x, x)
+    with pytest.raises(TypeError):
+        lags.lags_embed_grad(torch.zeros(4, dtype=torch.int64), x, x, None)
+    with pytest.raises(ValueError):
+        lags.embed_workspace(4, 0, 8)
