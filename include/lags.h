@@ -397,6 +397,7 @@ const char *lags_kernel_name(int32_t id);
 #define LAGS_SLAB_MAX 4096 /* see lags_gn */
 #define LAGS_GN_MAX (1 << 18) /* channels and pitches of lags_gn */
 #define LAGS_LN_MAX 16384 /* channels of lags_ln */
+#define LAGS_LINEAR_MAX (1 << 20) /* cols, outs and every ld of lags_linear */
 #define LAGS_VOCAB_MAX (1 << 26) /* rows of an embedding table */
 #define LAGS_WGRAD_MAX (1 << 22) /* outs, cols and lddy of lags_ckpt_wgrad; cols of an embedding */
 
@@ -612,6 +613,63 @@ size_t lags_embed_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols);
 int lags_embed_grad(int64_t tokens, int64_t vocab, int64_t cols, const void *ids, const void *dy,
                     int64_t lddy, int32_t dtype, float scale, float *dtable, uint32_t flags,
                     void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Linear layer (or 1x1 convolution) of a [rows, cols] input and outs outputs, with
+ * what follows it in the same pass:
+ *   z = x W^T + bias;  y = act(z) + res.
+ * Products of 16-bit values are exact in fp32, fp32 values are multiplied in fp32,
+ * and sums are held in fp32; z and y are each rounded to dtype once, from fp32.  The
+ * weight's gradient is lags_ckpt_wgrad's (from dz and x's checkpoint).
+ * rows in [0, 2^31), cols, outs and every ld in [1, LAGS_LINEAR_MAX]; act any
+ * LAGS_ACT_*, LAGS_ACT_GELU among them.
+ */
+typedef struct lags_linear {
+    int64_t rows, cols, outs;
+    int32_t dtype; /* of every matrix, W among them */
+    int32_t act;
+} lags_linear;
+
+/* Bytes of workspace that both directions of this layer need (at least 16); 0 for an
+ * invalid shape. */
+size_t lags_linear_workspace_bytes(const lags_linear *lin);
+
+/*
+ *   x:    device matrix [rows, cols] (ldx);
+ *   w:    device matrix [outs, cols] (ldw);
+ *   bias: device fp32[outs], or null;
+ *   res:  device matrix [rows, outs] (ldr), or null;
+ *   z:    device matrix out [rows, outs] (ldz), or null: what the backward of an
+ *         activation takes;
+ *   y:    device matrix out [rows, outs] (ldy); may be res itself.
+ * With rows 0 nothing is launched.
+ * Returns LAGS_OK, LAGS_EINVAL, LAGS_ERANGE, LAGS_EWORKSPACE, LAGS_EHIP.
+ */
+int lags_linear_forward(const lags_linear *lin, const void *x, int64_t ldx, const void *w,
+                        int64_t ldw, const float *bias, const void *res, int64_t ldr, void *z,
+                        int64_t ldz, void *y, int64_t ldy, void *ws, size_t ws_bytes,
+                        void *stream);
+
+/*
+ * Gradients of the forward call for the gradient dy of y (which is also that of
+ * res):
+ *   dz = dy * act'(z), rounded to dtype;  dbias = its sum over the rows before the
+ *   rounding;  dx = dz W.
+ *   dy:    device matrix [rows, outs] (lddy);
+ *   z:     as the forward left it (ldz); null for LAGS_ACT_NONE;
+ *   w, dx: device matrices (ldw, lddx), or both null (the first layer's input
+ *          needs no gradient);
+ *   dz:    device matrix out [rows, outs] (lddz); may be dy or z itself; null for
+ *          LAGS_ACT_NONE, where dy stands for it;
+ *   dbias: device fp32[outs], out, or null;
+ *   flags: 0 or LAGS_GRAD_ADD (dbias is added to).
+ * With rows 0 dbias becomes 0 (unless added to).
+ * Returns as lags_linear_forward.
+ */
+int lags_linear_backward(const lags_linear *lin, const void *dy, int64_t lddy, const void *z,
+                         int64_t ldz, const void *w, int64_t ldw, void *dz, int64_t lddz,
+                         float *dbias, void *dx, int64_t lddx, uint32_t flags, void *ws,
+                         size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,9 @@ SOURCES = [os.path.join(CSRC, "lags_host.cpp"), os.path.join(CSRC, "lags_schedul
            os.path.join(CSRC, "lags_gn_f32.hip"), os.path.join(CSRC, "lags_gn_bf16.hip"),
            os.path.join(CSRC, "lags_gn_f16.hip"),
            os.path.join(CSRC, "lags_wgrad.hip"), os.path.join(CSRC, "lags_layer.cpp"),
-           os.path.join(CSRC, "lags_ln.hip"), os.path.join(CSRC, "lags_embed.hip")]
+           os.path.join(CSRC, "lags_ln.hip"), os.path.join(CSRC, "lags_embed.hip"),
+           os.path.join(CSRC, "lags_linear.hip"), os.path.join(CSRC, "lags_linear_f32.hip"),
+           os.path.join(CSRC, "lags_linear_bf16.hip"), os.path.join(CSRC, "lags_linear_f16.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -10,7 +10,7 @@
 
 using namespace lags;
 
-static_assert(kActGelu == LAGS_ACT_GELU && kLnMax == LAGS_LN_MAX, "one numbering");
+static_assert(kActGelu == LAGS_ACT_GELU && kLnMax == LAGS_LN_MAX && kLinearMax == LAGS_LINEAR_MAX, "one numbering");
 
 namespace {
 
@@ -80,6 +80,48 @@ EmbedSpace embed_space(int64_t tokens, int64_t vocab, int64_t cols)
     w.part = w.start + up(((size_t)vocab + 1) * 4);
     w.bytes = w.part + up((size_t)embed_plan(LAGS_F32, tokens, vocab, cols).nchunk * 2 * cols * 4);
     return w;
+}
+
+int check_linear(const lags_linear *l)
+{
+    if (!l || !known_dtype(l->dtype) || l->act < LAGS_ACT_NONE || l->act > LAGS_ACT_GELU) return LAGS_EINVAL;
+    if (l->rows < 0 || l->cols < 1 || l->outs < 1) return LAGS_EINVAL;
+    if (l->rows > kMaxDim || l->cols > LAGS_LINEAR_MAX || l->outs > LAGS_LINEAR_MAX) return LAGS_ERANGE;
+    return LAGS_OK;
+}
+
+struct LinearCall {
+    LinPlan fwd, bwd;
+    DzPlan dz;
+    size_t need;                     // workspace, of both directions
+};
+int plan(const lags_linear *l, LinearCall &c)
+{
+    if (int rc = check_linear(l); rc != LAGS_OK) return rc;
+    const int64_t M = std::max<int64_t>(l->rows, 1);
+    c.fwd = linear_plan(l->dtype, M, l->outs, l->cols);
+    c.bwd = linear_plan(l->dtype, M, l->cols, l->outs);
+    c.dz = dz_plan(l->dtype, M, l->outs);
+    // threads of one launch: the product's, and those that join its slices
+    for (const LinPlan *p : {&c.fwd, &c.bwd})
+        if ((u128)p->tm * p->tn * p->split * 512 > kMostThreads) return LAGS_ERANGE;
+    if ((u128)M * std::max(l->outs, l->cols) > kMostThreads && (c.fwd.split > 1 || c.bwd.split > 1)) return LAGS_ERANGE;
+    const u128 f = c.fwd.split > 1 ? (u128)c.fwd.split * M * l->outs * 4 : 0;
+    const u128 b = c.bwd.split > 1 ? (u128)c.bwd.split * M * l->cols * 4 : 0;
+    // dbias is done before the product's sums are written
+    const u128 d = (u128)c.dz.chunks * l->outs * 4;
+    const u128 most = std::max(std::max(f, b), d);
+    c.need = l->rows ? (size_t)((most + 15) / 16 * 16) : 16;
+    return LAGS_OK;
+}
+
+// How a product's operands get into LDS (lags_linear.h).
+int how_of(std::initializer_list<std::pair<const void *, int64_t>> operands, int64_t inner, int32_t dtype)
+{
+    const uint32_t e = elem_bytes(dtype);
+    uintptr_t bits = (uint64_t)inner * e;
+    for (auto &o : operands) bits |= (uintptr_t)o.first | (uint64_t)o.second * e;
+    return bits & 3 ? 2 : bits & 15 ? 1 : 0;
 }
 
 }  // namespace
@@ -226,6 +268,104 @@ int lags_embed_grad(int64_t tokens, int64_t vocab, int64_t cols, const void *ids
     a.order = (uint32_t *)(b + w.order), a.keys = (uint32_t *)(b + w.keys), a.start = (uint32_t *)(b + w.start);
     a.part = (float *)(b + w.part);
     return hip(launch_embed_grad(p, a, dtype, wide, (hipStream_t)stream));
+}
+
+size_t lags_linear_workspace_bytes(const lags_linear *lin)
+{
+    LinearCall c;
+    return plan(lin, c) == LAGS_OK ? c.need : 0;
+}
+
+int lags_linear_forward(const lags_linear *lin, const void *x, int64_t ldx, const void *w, int64_t ldw,
+                        const float *bias, const void *res, int64_t ldr, void *z, int64_t ldz, void *y, int64_t ldy,
+                        void *ws, size_t ws_bytes, void *stream)
+{
+    LinearCall c;
+    if (int rc = plan(lin, c); rc != LAGS_OK) return rc;
+    const int64_t M = lin->rows, K = lin->cols, N = lin->outs;
+    enum { X, W, BIAS, RES, Z, Y, WS, COUNT };
+    Region r[COUNT] = {};
+    if (int rc = matrix(x, M, K, ldx, lin->dtype, r[X]); rc != LAGS_OK) return rc;
+    if (int rc = matrix(w, N, K, ldw, lin->dtype, r[W]); rc != LAGS_OK) return rc;
+    if (res)
+        if (int rc = matrix(res, M, N, ldr, lin->dtype, r[RES]); rc != LAGS_OK) return rc;
+    if (z)
+        if (int rc = matrix(z, M, N, ldz, lin->dtype, r[Z]); rc != LAGS_OK) return rc;
+    if (int rc = matrix(y, M, N, ldy, lin->dtype, r[Y]); rc != LAGS_OK) return rc;
+    if (ldx > LAGS_LINEAR_MAX || ldw > LAGS_LINEAR_MAX || ldy > LAGS_LINEAR_MAX || (res && ldr > LAGS_LINEAR_MAX) ||
+        (z && ldz > LAGS_LINEAR_MAX))
+        return LAGS_ERANGE;
+    if (!aligned(bias, 4)) return LAGS_EINVAL;
+    if (!ws || !aligned(ws, 16) || ws_bytes < c.need) return LAGS_EWORKSPACE;
+    r[BIAS] = flat(bias, N * 4), r[WS] = flat(ws, c.need);
+    for (int out : {Z, WS})
+        if (!clear_of(r, COUNT, out)) return LAGS_EINVAL;
+    // y may be res itself
+    for (int in : {X, W, BIAS})
+        if (overlap(r[Y], r[in])) return LAGS_EINVAL;
+    if (overlap(r[Y], r[RES]) && !same(r[Y], r[RES])) return LAGS_EINVAL;
+    if (!M) return LAGS_OK;
+    LinArgs a = {};
+    a.a = x, a.lda = ldx, a.b = w, a.ldb = ldw, a.M = M, a.N = (uint32_t)N, a.K = (uint32_t)K;
+    a.act = lin->act, a.bias = bias, a.res = res, a.ldr = ldr, a.z = z, a.ldz = ldz, a.y = y, a.ldy = ldy;
+    a.part = (float *)ws;
+    const int how = how_of({{x, ldx}, {w, ldw}}, K, lin->dtype);
+    return hip(launch_linear(c.fwd, a, false, how, lin->dtype, (hipStream_t)stream));
+}
+
+int lags_linear_backward(const lags_linear *lin, const void *dy, int64_t lddy, const void *z, int64_t ldz,
+                         const void *w, int64_t ldw, void *dz, int64_t lddz, float *dbias, void *dx, int64_t lddx,
+                         uint32_t flags, void *ws, size_t ws_bytes, void *stream)
+{
+    LinearCall c;
+    if (int rc = plan(lin, c); rc != LAGS_OK) return rc;
+    const int64_t M = lin->rows, K = lin->cols, N = lin->outs;
+    const bool act = lin->act != LAGS_ACT_NONE;
+    if (flags & ~LAGS_GRAD_ADD) return LAGS_EINVAL;
+    if (!z != !act || !dz != !act || !w != !dx) return LAGS_EINVAL;
+    enum { DY, Z, W, DZ, DBIAS, DX, WS, COUNT };
+    Region r[COUNT] = {};
+    if (int rc = matrix(dy, M, N, lddy, lin->dtype, r[DY]); rc != LAGS_OK) return rc;
+    if (act) {
+        if (int rc = matrix(z, M, N, ldz, lin->dtype, r[Z]); rc != LAGS_OK) return rc;
+        if (int rc = matrix(dz, M, N, lddz, lin->dtype, r[DZ]); rc != LAGS_OK) return rc;
+    }
+    if (dx) {
+        if (int rc = matrix(w, N, K, ldw, lin->dtype, r[W]); rc != LAGS_OK) return rc;
+        if (int rc = matrix(dx, M, K, lddx, lin->dtype, r[DX]); rc != LAGS_OK) return rc;
+    }
+    if (lddy > LAGS_LINEAR_MAX || (act && (ldz > LAGS_LINEAR_MAX || lddz > LAGS_LINEAR_MAX)) ||
+        (dx && (ldw > LAGS_LINEAR_MAX || lddx > LAGS_LINEAR_MAX)))
+        return LAGS_ERANGE;
+    if (!aligned(dbias, 4)) return LAGS_EINVAL;
+    if (!ws || !aligned(ws, 16) || ws_bytes < c.need) return LAGS_EWORKSPACE;
+    r[DBIAS] = flat(dbias, N * 4), r[WS] = flat(ws, c.need);
+    for (int out : {DBIAS, DX, WS})
+        if (!clear_of(r, COUNT, out)) return LAGS_EINVAL;
+    // dz may be dy or z itself
+    if (overlap(r[DZ], r[W])) return LAGS_EINVAL;
+    for (int in : {DY, Z})
+        if (overlap(r[DZ], r[in]) && !same(r[DZ], r[in])) return LAGS_EINVAL;
+    const bool add = flags & LAGS_GRAD_ADD;
+    const hipStream_t s = (hipStream_t)stream;
+    LinArgs a = {};
+    a.M = M, a.act = lin->act;
+    if (M && (act || dbias)) {
+        a.N = (uint32_t)N, a.dy = dy, a.lddy = lddy, a.zin = z, a.ldz = ldz, a.dz = dz, a.lddz = lddz;
+        a.part = dbias ? (float *)ws : nullptr;
+        if (int rc = hip(launch_slopes(c.dz, a, lin->dtype, s)); rc != LAGS_OK) return rc;
+    }
+    if (dbias)
+        if (int rc = hip(launch_dbias((const float *)ws, M ? c.dz.chunks : 0, (uint32_t)N, dbias, add, s)); rc != LAGS_OK)
+            return rc;
+    if (!M || !dx) return LAGS_OK;
+    a = {};
+    a.a = act ? dz : dy, a.lda = act ? lddz : lddy, a.b = w, a.ldb = ldw;
+    a.M = M, a.N = (uint32_t)K, a.K = (uint32_t)N, a.act = LAGS_ACT_NONE, a.y = dx, a.ldy = lddx;
+    a.part = (float *)ws;
+    // along k for dz, along n for W
+    const int how = how_of({{a.a, a.lda}, {w, ldw}}, N | K, lin->dtype);
+    return hip(launch_linear(c.bwd, a, true, how, lin->dtype, s));
 }
 
 }  // extern "C"

@@ -60,6 +60,42 @@ EmbedPlan embed_plan(int dtype, int64_t tokens, int64_t vocab, int64_t cols);
 hipError_t launch_embed(EmbedArgs a, int table, int dtype, bool wide, hipStream_t s);
 hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wide, hipStream_t s);
 
+// ---- linear layers ---------------------------------------------------------
+struct LinArgs {
+    // the product C = A B': a [M][K]; b forward W [N][K], backward W [K][N]
+    const void *a, *b;
+    int64_t lda, ldb, M;
+    uint32_t N, K;
+    int act;
+    const float *bias;
+    const void *res;
+    void *z, *y;                             // C + bias; act of it + res
+    int64_t ldr, ldz, ldy;
+    float *part;                             // slices' sums [split][M][N]; column sums [chunks][N]
+    uint32_t tm, tn, split, steps_per;       // tiles, slices of k, steps of 128 bytes a slice
+    // dz = dy act'(zin) over M x N
+    const void *dy, *zin;
+    void *dz;
+    int64_t lddy, lddz, rows_per;
+    uint32_t tl, nslab;
+};
+struct LinPlan {
+    uint32_t tile, tm, tn, split, steps_per;
+};
+struct DzPlan {
+    uint32_t tl, nslab, chunks;
+    int64_t rows_per;
+};
+constexpr int64_t kLinearMax = 1 << 20;      // cols, outs and every ld: 256 rows stay within 32-bit offsets
+LinPlan linear_plan(int dtype, int64_t M, int64_t N, int64_t K);
+DzPlan dz_plan(int dtype, int64_t M, int64_t N);
+template <int D> hipError_t product(const LinPlan &p, LinArgs a, bool nn, int how, hipStream_t s);
+template <int D> hipError_t slopes(const DzPlan &p, LinArgs a, hipStream_t s);
+// how: 0 operands of whole 16-byte vectors, 1 of rows that start on words, 2 on halves of them
+hipError_t launch_linear(const LinPlan &p, const LinArgs &a, bool nn, int how, int dtype, hipStream_t s);
+hipError_t launch_slopes(const DzPlan &p, const LinArgs &a, int dtype, hipStream_t s);
+hipError_t launch_dbias(const float *part, uint32_t rows, uint32_t N, float *dbias, uint32_t add, hipStream_t s);
+
 // dgamma, dbeta: sums over `rows` rows of part [rows][2][C] (dbeta's sums
 // first), in a fixed order; either may be null (lags_gn.hip).
 hipError_t launch_params(const float *part, uint32_t rows, uint32_t C, float *dgamma, float *dbeta, uint32_t add,

@@ -1,0 +1,490 @@
+// Kernels of a linear layer: z = x W^T + bias, y = act(z) + res, and the product
+// dx = dz W of its backward.
+//
+// Both are C[m][n] = sum over k of A[m][k] B'[k][n]; A's rows (x, dz) run along k.
+// Forward B is W [n][k], whose rows run along k too, so that a matrix
+// instruction's operands are 16 consecutive bytes of LDS each.  Backward B is W
+// [k][n], staged as it comes and transposed by the LDS transpose reads (fp32: by
+// reading a value a lane).  fp32 runs on the fp32 matrix instructions; all sums are
+// held in fp32.
+#pragma once
+
+#include "lags_gn.h"
+#include "lags_layer.h"
+
+namespace lags {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// ---- activations -----------------------------------------------------------
+// s = 1 / (1 + exp(-u)) and 1 - s.  16-bit types: the hardware's exponential and
+// reciprocal, good to a few units of 2^-23.
+template <int D> __device__ inline float sigmoid(float u, float &rest)
+{
+    if constexpr (D == kF32) {
+        const float q = expf(-u), s = 1.0f / (1.0f + q);
+        rest = q * s;
+        return s;
+    }
+    const float q = __expf(-u), s = __builtin_amdgcn_rcpf(1.0f + q);
+    rest = q * s;
+    return s;
+}
+constexpr float kGelu = 1.5957691216057308f;      // 2 sqrt(2 / pi)
+// Past these magnitudes of z, where exp(-u) is about to leave fp32's range and the sigmoid is 0 or 1
+// but for less than 2^-124, z is taken as this (a NaN stays), so that no infinity meets a zero.
+constexpr float kFarSilu = 87, kFarGelu = 10;
+__device__ inline float within(float z, float top) { return z < -top ? -top : z > top ? top : z; }
+
+template <int D> __device__ inline float act_value(float z, int act)
+{
+    float rest;
+    if (act == kActRelu) return above_zero(z);
+    if (act == kActSilu) return (z < -kFarSilu ? -kFarSilu : z) * sigmoid<D>(within(z, kFarSilu), rest);
+    if (act == kActGelu) {
+        const float c = within(z, kFarGelu);
+        return (z < -kFarGelu ? -kFarGelu : z) * sigmoid<D>(kGelu * c * __builtin_fmaf(0.044715f * c, c, 1.0f), rest);
+    }
+    return z;
+}
+template <int D> __device__ inline float act_slope(float z, int act)
+{
+    float rest;
+    if (act == kActRelu) return z > 0 ? 1.0f : z != z ? z : 0.0f;
+    if (act == kActSilu) {
+        const float c = within(z, kFarSilu), s = sigmoid<D>(c, rest);
+        return s * __builtin_fmaf(c, rest, 1.0f);
+    }
+    if (act == kActGelu) {
+        const float c = within(z, kFarGelu), q = c * c;
+        const float s = sigmoid<D>(kGelu * c * __builtin_fmaf(0.044715f, q, 1.0f), rest);
+        return s * __builtin_fmaf(c * rest * kGelu, __builtin_fmaf(0.134145f, q, 1.0f), 1.0f);
+    }
+    return 1.0f;
+}
+
+// ---- what becomes of a sum -------------------------------------------------
+// V consecutive sums of row m from column n on, nv of them within the matrix.
+template <int D> __device__ inline void finish(const LinArgs &a, int64_t m, uint32_t n, int nv, float (&f)[Elem<D>::V])
+{
+    constexpr int V = Elem<D>::V, E = Elem<D>::E;
+    if (a.bias) {
+        for (int i = 0; i < V; i += 4) {
+            if (i + 4 <= nv) {
+                const f32x4_u4 b = *(const f32x4_u4 *)(a.bias + n + i);
+                for (int j = 0; j < 4; ++j) f[i + j] += b[j];
+            } else {
+                for (int j = i; j < i + 4; ++j)
+                    if (j < nv) f[j] += a.bias[n + j];
+            }
+        }
+    }
+    if (a.z) store_vec<D>((char *)a.z + (m * a.ldz + n) * E, Elem<D>::pack(f), nv);
+    if (a.act != kActNone)
+        for (int j = 0; j < V; ++j) f[j] = act_value<D>(f[j], a.act);
+    if (a.res) {
+        float r[V];
+        Elem<D>::unpack(load_vec<D>((const char *)a.res + (m * a.ldr + n) * E, nv), r);
+        for (int j = 0; j < V; ++j) f[j] += r[j];
+    }
+    store_vec<D>((char *)a.y + (m * a.ldy + n) * E, Elem<D>::pack(f), nv);
+}
+
+// ---- the product -----------------------------------------------------------
+constexpr int kStep = 128;                        // bytes of k staged at a time
+enum : int { kDirect = 0, kWords = 1, kHalves = 2 };   // see stage below
+
+// Byte offset of 16-byte vector v of row r in a tile of 128-byte rows: a read of
+// one vector column over 16 rows then takes all banks once.
+__device__ inline int at_rows(int r, int v) { return r * kStep + ((v ^ (r & 7) ^ (r >> 3 & 3)) << 4); }
+// Byte offset of 16-byte vector v of row k in a tile of BN 16-bit columns, for
+// transpose reads: 16 lanes take 32 bytes from each of four consecutive rows.
+template <int BN> __device__ inline int at_columns(int k, int v)
+{
+    const int x = BN % 128 == 0 ? k & 3 : k >> 1 & 1;
+    return k * BN * 2 + ((v >> 2 ^ x) << 6) + ((v & 3) << 4);
+}
+// Eight consecutive rows of one column for each lane: lane l holds column cb +
+// l % 32, rows kb + 8 (l / 32) + 0..7.
+template <int BN> __device__ inline u32x4 transposed(const char *tile, int kb, int cb)
+{
+    const int l = threadIdx.x & 63, i = l & 15;
+    const int k = kb + 8 * (l >> 5) + (i >> 2), c = cb + (l & 16) + (i & 3) * 4;
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(tile + at_columns<BN>(k, c >> 3) + (c & 4) * 2));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(tile + at_columns<BN>(k + 4, c >> 3) + (c & 4) * 2));
+    return __builtin_bit_cast(u32x4, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int D> __device__ inline f32x16 multiply(u32x4 w, u32x4 x, f32x16 acc)
+{
+    if constexpr (D == kBF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+    else if constexpr (D == kF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, x), acc, 0, 0, 0);
+    else {
+        for (int t = 0; t < 4; ++t) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(asf(w[t]), asf(x[t]), acc, 0, 0, 0);
+        return acc;
+    }
+}
+
+// 16 bytes of a buffer into LDS at `to`, which the wave shares, lane after lane.
+__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t r, char *to, uint32_t at)
+{
+#if defined(__HIP_DEVICE_COMPILE__)      // the host pass does not know this size
+    typedef __attribute__((address_space(3))) void lds_void;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)to, 16, at, 0, 0, 0);
+#endif
+}
+// What the lanes of a wave wrote to LDS before is read by any of them after.
+__device__ inline void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ inline uint32_t deal(uint32_t b, uint32_t n)
+{
+    const uint32_t per = n / 8, main = per * 8;
+    return b < main ? (b & 7) * per + (b >> 3) : b;
+}
+
+// A workgroup: a BM x BN tile of the product over one slice of k; WM x WN waves.
+// NN: B is [k][n].  HOW a tile gets into LDS: kDirect, loads that write it themselves
+// (operands of whole, aligned 16-byte vectors); kWords and kHalves, through
+// registers, rows that start on any word, or on any half of one (five words are
+// read for each vector's four and shifted into place).
+template <int D, int BM, int BN, int WM, int WN, bool NN, int HOW>
+__global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
+{
+    constexpr int kThreads = 64 * WM * WN;
+    constexpr int V = Elem<D>::V, E = Elem<D>::E, KS = kStep / E;
+    constexpr int NX = BM / WM / 32, NW = BN / WN / 32;
+    constexpr int PA = BM * 8 / kThreads, PB = BN * 8 / kThreads;     // vectors a thread
+    constexpr int RV = NN ? BN * E / 16 : 8;                          // vectors a row of B's tile
+    constexpr int TA = BM * kStep, BUF = TA + BN * kStep;
+    static_assert(BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0, "whole passes");
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+
+    // tiles in bands of eight rows of them, so that those in flight on an XCD share operands in its L2
+    const uint32_t b = deal(blockIdx.x, gridDim.x), tiles = a.tm * a.tn, slice = b / tiles, tile = b - slice * tiles;
+    const uint32_t band = tile / (8 * a.tn), in = tile - band * 8 * a.tn, high = min(8u, a.tm - band * 8);
+    const int64_t m0 = (int64_t)(band * 8 + in % high) * BM;
+    const uint32_t n0 = in / high * BN;
+    const uint32_t k0 = slice * a.steps_per * KS, k1 = min(a.K, k0 + a.steps_per * KS);
+    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+
+    // windows of the operands from this slice's k on; they end with the last valid value
+    const int64_t rows = min((int64_t)BM, a.M - m0);
+    const char *pa = (const char *)a.a + (m0 * a.lda + k0) * E;
+    int64_t la = ((rows - 1) * a.lda + (a.K - k0)) * E;
+    const char *pb;
+    int64_t lb, step_b;
+    if constexpr (NN) {
+        pb = (const char *)a.b + ((int64_t)k0 * a.ldb + n0) * E;
+        lb = ((int64_t)(a.K - k0 - 1) * a.ldb + (a.N - n0)) * E;
+        step_b = KS * a.ldb * E;
+    } else {
+        pb = (const char *)a.b + ((int64_t)n0 * a.ldb + k0) * E;
+        lb = ((int64_t)(min((uint32_t)BN, a.N - n0) - 1) * a.ldb + (a.K - k0)) * E;
+        step_b = kStep;
+    }
+    const int ia = HOW == kHalves ? (int)((uintptr_t)pa & 3) : 0, ib = HOW == kHalves ? (int)((uintptr_t)pb & 3) : 0;
+    pa -= ia, pb -= ib;
+    if constexpr (HOW == kHalves) la = (la + ia + 3) & ~(int64_t)3, lb = (lb + ib + 3) & ~(int64_t)3;
+
+    // Vector `id` of a tile: the row and vector it holds.  Direct loads write LDS in the order of the
+    // lanes, so there the exchange of vectors is applied to what is loaded.
+    uint32_t oa[PA], ob[PB];
+    auto vec_a = [&](int id) { return HOW == kDirect ? (id & 7) ^ (id >> 3 & 7) ^ (id >> 6 & 3) : id & 7; };
+    auto vec_b = [&](int id) {
+        if constexpr (!NN) return vec_a(id);
+        const int k = id / RV, v = id % RV;
+        if constexpr (HOW != kDirect || E == 4) return v;
+        return ((v >> 2 ^ (BN % 128 == 0 ? k & 3 : k >> 1 & 1)) << 2) | (v & 3);
+    };
+#pragma unroll
+    for (int p = 0; p < PA; ++p) oa[p] = ia + (uint32_t)((t + p * kThreads) / 8 * a.lda * E) + vec_a(t + p * kThreads) * 16;
+#pragma unroll
+    for (int p = 0; p < PB; ++p) ob[p] = ib + (uint32_t)((t + p * kThreads) / RV * a.ldb * E) + vec_b(t + p * kThreads) * 16;
+
+    uint32_t k = k0;                                   // what is loaded next
+    auto move = [&] { k += KS, pa += kStep, la -= kStep, pb += step_b, lb -= step_b; };
+    // loads that write the tiles of the next step to `buf`
+    auto load_direct = [&](char *buf) {
+        const auto ra = window(pa, la), rb = window(pb, lb);
+        char *w = buf + (t & ~63) * 16;
+        const int left = (int)(a.K - k);               // vectors past the last k read as zeros
+#pragma unroll
+        for (int p = 0; p < PA; ++p)
+            load_to_lds(ra, w + p * kThreads * 16,
+                        left >= KS || vec_a(t + p * kThreads) * V < left ? oa[p] : 0x80000000u);
+#pragma unroll
+        for (int p = 0; p < PB; ++p)
+            load_to_lds(rb, w + TA + p * kThreads * 16,
+                        NN || left >= KS || vec_b(t + p * kThreads) * V < left ? ob[p] : 0x80000000u);
+        move();
+    };
+    u32x4 va[HOW == kDirect ? 1 : PA], vb[HOW == kDirect ? 1 : PB];
+    uint32_t xa[HOW == kHalves ? PA : 1], xb[HOW == kHalves ? PB : 1];
+    int held = 0;                                      // how much of k the registers hold
+    auto load = [&] {
+        const auto ra = window(pa, la), rb = window(pb, lb);
+#pragma unroll
+        for (int p = 0; p < PA; ++p) {
+            va[p] = __builtin_amdgcn_raw_buffer_load_b128(ra, oa[p] & ~3u, 0, 0);
+            if constexpr (HOW == kHalves) xa[p] = __builtin_amdgcn_raw_buffer_load_b32(ra, (oa[p] & ~3u) + 16, 0, 0);
+        }
+#pragma unroll
+        for (int p = 0; p < PB; ++p) {
+            vb[p] = __builtin_amdgcn_raw_buffer_load_b128(rb, ob[p] & ~3u, 0, 0);
+            if constexpr (HOW == kHalves) xb[p] = __builtin_amdgcn_raw_buffer_load_b32(rb, (ob[p] & ~3u) + 16, 0, 0);
+        }
+        held = (int)(a.K - k);
+        move();
+    };
+    auto whole = [&](u32x4 &v, uint32_t x, uint32_t o) {
+        const uint32_t sh = (o & 2) * 8;
+        for (int i = 0; i < 3; ++i) v[i] = __builtin_amdgcn_alignbit(v[i + 1], v[i], sh);
+        v[3] = __builtin_amdgcn_alignbit(x, v[3], sh);
+    };
+    auto cut = [&](u32x4 &v, int n) {                  // all but the first n values
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (E == 4)
+                v[i] = i < n ? v[i] : 0;
+            else
+                v[i] = 2 * i + 1 < n ? v[i] : 2 * i < n ? v[i] & 0xffffu : 0;
+        }
+    };
+    auto stage = [&](char *buf) {
+#pragma unroll
+        for (int p = 0; p < PA; ++p) {
+            const int id = t + p * kThreads;
+            if constexpr (HOW == kHalves) whole(va[p], xa[p], oa[p]);
+            if (held < KS) cut(va[p], held - (id & 7) * V);
+            *(u32x4 *)(buf + at_rows(id >> 3, id & 7)) = va[p];
+        }
+#pragma unroll
+        for (int p = 0; p < PB; ++p) {
+            const int id = t + p * kThreads;
+            if constexpr (HOW == kHalves) whole(vb[p], xb[p], ob[p]);
+            if constexpr (NN) {
+                if (id / RV >= held) vb[p] = u32x4{0, 0, 0, 0};
+                *(u32x4 *)(buf + TA + (E == 2 ? at_columns<BN>(id / RV, id % RV) : id * 16)) = vb[p];
+            } else {
+                if (held < KS) cut(vb[p], held - (id & 7) * V);
+                *(u32x4 *)(buf + TA + at_rows(id >> 3, id & 7)) = vb[p];
+            }
+        }
+    };
+
+    const int mw = wave / WN * (BM / WM), nw = wave % WN * (BN / WN);
+    f32x16 acc[NW][NX] = {};
+    auto products = [&](const char *buf, int q) {      // 32 bytes of k
+        u32x4 x[NX], w[NW];
+#pragma unroll
+        for (int j = 0; j < NX; ++j) x[j] = *(const u32x4 *)(buf + at_rows(mw + 32 * j + (lane & 31), 2 * q + (lane >> 5)));
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            const int n = nw + 32 * i;
+            if constexpr (!NN)
+                w[i] = *(const u32x4 *)(buf + TA + at_rows(n + (lane & 31), 2 * q + (lane >> 5)));
+            else if constexpr (E == 2)
+                w[i] = transposed<BN>(buf + TA, 16 * q, n);
+            else
+                for (int e = 0; e < 4; ++e)
+                    w[i][e] = *(const uint32_t *)(buf + TA + ((8 * q + 4 * (lane >> 5) + e) * BN + n + (lane & 31)) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+#pragma unroll
+            for (int j = 0; j < NX; ++j) acc[i][j] = multiply<D>(w[i], x[j], acc[i][j]);
+    };
+    int cur = 0;
+    if constexpr (HOW == kDirect) {
+        load_direct(lds);
+    } else {
+        load();
+        stage(lds);
+        load();
+    }
+    for (uint32_t s = k0; s < k1; s += KS) {
+        __syncthreads();
+        const char *buf = lds + cur * BUF;
+        cur ^= 1;
+        if constexpr (HOW == kDirect) {
+            if (s + KS < k1) load_direct(lds + cur * BUF);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) products(buf, q);
+        } else {
+            products(buf, 0);
+            products(buf, 1);
+            stage(lds + cur * BUF);
+            load();
+            products(buf, 2);
+            products(buf, 3);
+        }
+    }
+
+    // Each wave turns 32 rows of 64 (or 32) sums round in LDS of its own, so that a lane has
+    // consecutive columns of a row.
+    __syncthreads();
+    constexpr int CW = NW >= 2 ? 64 : 32, PITCH = CW + 4, QW = CW / 32;
+    float *own = (float *)lds + wave * 32 * PITCH;
+    constexpr int LR = CW / V, RP = 64 / LR;           // lanes a row, rows at a time
+#pragma unroll
+    for (int j = 0; j < NX; ++j)
+#pragma unroll
+        for (int i0 = 0; i0 < NW; i0 += QW) {
+#pragma unroll
+            for (int i = 0; i < QW; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    *(f32x4 *)(own + (lane & 31) * PITCH + 32 * i + 8 * r + 4 * (lane >> 5)) =
+                        f32x4{acc[i0 + i][j][4 * r], acc[i0 + i][j][4 * r + 1], acc[i0 + i][j][4 * r + 2], acc[i0 + i][j][4 * r + 3]};
+            wave_sync();
+            const uint32_t n = n0 + nw + 32 * i0 + lane % LR * V;
+            const int nv = (int)a.N - (int)n;
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += RP) {
+                const int r = r0 + lane / LR;
+                const int64_t m = m0 + mw + 32 * j + r;
+                float f[V];
+                for (int e = 0; e < V; e += 4) *(f32x4 *)(f + e) = *(const f32x4 *)(own + r * PITCH + lane % LR * V + e);
+                if (m >= a.M || nv <= 0) continue;
+                if (a.split > 1) {
+                    float *out = a.part + ((size_t)slice * a.M + m) * a.N + n;
+                    for (int e = 0; e < V; e += 4) store_vec<kF32>(out + e, u32x4{asu(f[e]), asu(f[e + 1]), asu(f[e + 2]), asu(f[e + 3])}, nv - e);
+                } else {
+                    finish<D>(a, m, n, nv, f);
+                }
+            }
+            wave_sync();
+        }
+}
+
+// The slices' sums, in a fixed order, and what becomes of them.
+template <int D> __global__ __launch_bounds__(256) void k_linear_join(LinArgs a)
+{
+    constexpr int V = Elem<D>::V;
+    const uint32_t nv = (a.N + V - 1) / V;
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = i / nv;
+    const uint32_t n = (uint32_t)(i - (size_t)m * nv) * V;
+    if (m >= a.M) return;
+    const int left = (int)(a.N - n);
+    float f[V] = {};
+#pragma unroll 4
+    for (uint32_t s = 0; s < a.split; ++s) {
+        const float *p = a.part + ((size_t)s * a.M + m) * a.N + n;
+        for (int e = 0; e < V; e += 4) {
+            const u32x4 v = load_vec<kF32>(p + e, left - e);
+            for (int j = 0; j < 4; ++j) f[e + j] += asf(v[j]);
+        }
+    }
+    finish<D>(a, m, n, left, f);
+}
+
+// dz = dy act'(z), and its column sums before rounding: part[workgroup row][N].
+// 2^tl lanes span a slab of a row; the other lanes and the waves take rows.
+template <int D> __global__ __launch_bounds__(256) void k_linear_dz(LinArgs a)
+{
+    constexpr int V = Elem<D>::V, E = Elem<D>::E;
+    __shared__ float sh[4][V][64];
+    const uint32_t T = 1u << a.tl, col = threadIdx.x & (T - 1), R = 256 >> a.tl;
+    const uint32_t slab = blockIdx.x % a.nslab, chunk = blockIdx.x / a.nslab;
+    const uint32_t n = (slab * T + col) * V;
+    const int nv = (int)a.N - (int)n;
+    const int64_t lo = (int64_t)chunk * a.rows_per, hi = min(a.M, lo + a.rows_per);
+    float sum[V] = {};
+    if (nv > 0) {
+        constexpr int U = 4;
+        for (int64_t m = lo + (threadIdx.x >> a.tl); m < hi; m += R * U) {
+            u32x4 d[U], z[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = min(m + u * R, hi - 1);
+                d[u] = load_vec<D>((const char *)a.dy + (r * a.lddy + n) * E, nv);
+                if (a.zin) z[u] = load_vec<D>((const char *)a.zin + (r * a.ldz + n) * E, nv);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (m + u * R >= hi) break;
+                float f[V];
+                Elem<D>::unpack(d[u], f);
+                if (a.zin) {
+                    float g[V];
+                    Elem<D>::unpack(z[u], g);
+                    for (int j = 0; j < V; ++j) f[j] *= act_slope<D>(g[j], a.act);
+                    store_vec<D>((char *)a.dz + ((m + u * R) * a.lddz + n) * E, Elem<D>::pack(f), nv);
+                }
+                for (int j = 0; j < V; ++j) sum[j] += f[j];
+            }
+        }
+    }
+    if (!a.part) return;
+    for (int j = 0; j < V; ++j) {
+        float v = sum[j];
+        if (a.tl < 1) v += lane_xor<1>(v);
+        if (a.tl < 2) v += lane_xor<2>(v);
+        if (a.tl < 3) v += lane_xor<4>(v);
+        if (a.tl < 4) v += lane_xor<8>(v);
+        if (a.tl < 5) v = swap_sum<16>(v, v);
+        if (a.tl < 6) v = swap_sum<32>(v, v);
+        sh[threadIdx.x >> 6][j][threadIdx.x & 63] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x < T && nv > 0)
+        for (int j = 0; j < V; ++j)
+            if (j < nv)
+                a.part[(size_t)chunk * a.N + n + j] =
+                    (sh[0][j][col] + sh[1][j][col]) + (sh[2][j][col] + sh[3][j][col]);
+}
+
+// ---- launches --------------------------------------------------------------
+template <int D, int BM, int BN, int WM, int WN, bool NN> hipError_t run_linear(const LinArgs &a, int how, hipStream_t s)
+{
+    constexpr int turn = WM * WN * 32 * (BN / WN >= 64 ? 68 : 36) * 4, two = 2 * (BM + BN) * kStep;
+    constexpr int lds = two > turn ? two : turn;
+    auto k = k_linear<D, BM, BN, WM, WN, NN, kDirect>;
+    if (how == kWords) k = k_linear<D, BM, BN, WM, WN, NN, kWords>;
+    if constexpr (D != kF32)
+        if (how == kHalves) k = k_linear<D, BM, BN, WM, WN, NN, kHalves>;
+    if (hipError_t e = allow_lds((const void *)k, lds); e != hipSuccess) return e;
+    k<<<a.tm * a.tn * a.split, 64 * WM * WN, lds, s>>>(a);
+    return hipGetLastError();
+}
+template <int D, bool NN> hipError_t run_tile(uint32_t tile, const LinArgs &a, int how, hipStream_t s)
+{
+    switch (tile) {
+    case 0: return run_linear<D, 256, 256, 2, 4, NN>(a, how, s);
+    case 1: return run_linear<D, 128, 128, 2, 2, NN>(a, how, s);
+    case 2: return run_linear<D, 64, 64, 2, 2, NN>(a, how, s);
+    case 3: return run_linear<D, 32, 128, 1, 4, NN>(a, how, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+template <int D> hipError_t product(const LinPlan &p, LinArgs a, bool nn, int how, hipStream_t s)
+{
+    a.tm = p.tm, a.tn = p.tn, a.split = p.split, a.steps_per = p.steps_per;
+    const hipError_t e = nn ? run_tile<D, true>(p.tile, a, how, s) : run_tile<D, false>(p.tile, a, how, s);
+    if (e != hipSuccess || a.split == 1) return e;
+    constexpr uint32_t V = Elem<D>::V;
+    const uint64_t threads = (uint64_t)a.M * ((a.N + V - 1) / V);
+    k_linear_join<D><<<(uint32_t)((threads + 255) / 256), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+template <int D> hipError_t slopes(const DzPlan &p, LinArgs a, hipStream_t s)
+{
+    a.tl = p.tl, a.nslab = p.nslab, a.rows_per = p.rows_per;
+    k_linear_dz<D><<<p.nslab * p.chunks, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace lags

@@ -1,0 +1,7 @@
+// The linear layer's kernels for one element type.
+#include "lags_linear.h"
+
+namespace lags {
+template hipError_t product<kF32>(const LinPlan &, LinArgs, bool, int, hipStream_t);
+template hipError_t slopes<kF32>(const DzPlan &, LinArgs, hipStream_t);
+}  // namespace lags

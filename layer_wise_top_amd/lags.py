@@ -34,6 +34,7 @@ EXPORTED = (
     "lags_ckpt_wgrad_workspace_bytes", "lags_ckpt_wgrad",
     "lags_ln_workspace_bytes", "lags_ln_forward", "lags_ln_backward",
     "lags_embed_forward", "lags_embed_workspace_bytes", "lags_embed_grad",
+    "lags_linear_workspace_bytes", "lags_linear_forward", "lags_linear_backward",
 )
 
 LAGS_F32, LAGS_BF16, LAGS_F16 = 0, 1, 2
@@ -42,6 +43,7 @@ LAGS_IDS64 = 2
 LAGS_CKPT_RUN = 32
 LAGS_SLAB_MAX = 4096
 ACTS = {"none": 0, "relu": 1, "silu": 2}
+LINEAR_ACTS = {**ACTS, "gelu": 3}
 
 
 class LagsError(RuntimeError):
@@ -67,6 +69,12 @@ class LnShape(ctypes.Structure):
     """lags_ln"""
     _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("eps", ctypes.c_float)]
+
+
+class LinearShape(ctypes.Structure):
+    """lags_linear"""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("outs", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
 _lib = None
@@ -169,6 +177,13 @@ def lib():
     L.lags_embed_workspace_bytes.argtypes = [i64, i64, i64]
     L.lags_embed_grad.restype = ctypes.c_int
     L.lags_embed_grad.argtypes = [i64, i64, i64, vp, vp, i64, i32, ctypes.c_float, vp, u32, vp, sz, vp]
+    lin = ctypes.POINTER(LinearShape)
+    L.lags_linear_workspace_bytes.restype = sz
+    L.lags_linear_workspace_bytes.argtypes = [lin]
+    L.lags_linear_forward.restype = ctypes.c_int
+    L.lags_linear_forward.argtypes = [lin, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp, sz, vp]
+    L.lags_linear_backward.restype = ctypes.c_int
+    L.lags_linear_backward.argtypes = [lin, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, u32, vp, sz, vp]
     _lib = L
     return L
 
@@ -758,3 +773,59 @@ def lags_embed_grad(ids, dy, dtable, ws, scale: float = 1.0, add: bool = False, 
     rc = lib().lags_embed_grad(n, vocab, cols, pi, pdy, lddy, _dtype_code(dy.dtype), scale,
                                _vector(dtable, dev, 0, "dtable"), f | (LAGS_GRAD_ADD if add else 0), pw, nw, s)
     _check("lags_embed_grad", rc)
+
+
+class Linear:
+    """A linear layer's shape (lags_linear): [rows, cols] inputs, `outs` outputs."""
+
+    def __init__(self, rows: int, cols: int, outs: int, dtype=None, act: str = "none"):
+        import torch
+        if act not in LINEAR_ACTS:
+            raise ValueError(f"act must be one of {sorted(LINEAR_ACTS)}, got {act!r}")
+        self.dtype = dtype if dtype is not None else torch.float32
+        self.shape = LinearShape(int(rows), int(cols), int(outs), _dtype_code(self.dtype), LINEAR_ACTS[act])
+        self.ref = ctypes.byref(self.shape)
+        self.rows, self.cols, self.outs = int(rows), int(cols), int(outs)
+
+    def workspace_bytes(self) -> int:
+        return int(lib().lags_linear_workspace_bytes(self.ref))
+
+
+def linear_workspace(lin: Linear, device=None):
+    """Allocate a workspace for lags_linear_forward and lags_linear_backward of this shape."""
+    import torch
+    nbytes = lin.workspace_bytes()
+    if nbytes == 0:
+        raise ValueError("invalid or unsupported linear layer shape")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def lags_linear_forward(lin: Linear, x, w, y, ws, bias=None, res=None, z=None, stream=None):
+    """y = act(x w^T + bias) + res; w [outs, cols]; z (or None) receives what the activation takes."""
+    dev, s = _place(x, "x", stream)
+    m, n = lin.rows, lin.outs
+    px, _, _, ldx = _matrix(x, dev, "x", lin.dtype, m, lin.cols)
+    pwt, _, _, ldw = _matrix(w, dev, "w", lin.dtype, n, lin.cols)
+    py, _, _, ldy = _matrix(y, dev, "y", lin.dtype, m, n)
+    pr, ldr = _opt_matrix(res, dev, "res", lin.dtype, m, n)
+    pz, ldz = _opt_matrix(z, dev, "z", lin.dtype, m, n)
+    pw, nw = _buffer(ws, dev, "ws")
+    rc = lib().lags_linear_forward(lin.ref, px, ldx, pwt, ldw, _vector(bias, dev, n, "bias"), pr, ldr, pz, ldz, py,
+                                   ldy, pw, nw, s)
+    _check("lags_linear_forward", rc)
+
+
+def lags_linear_backward(lin: Linear, dy, w, dx, ws, z=None, dz=None, dbias=None, add: bool = False, stream=None):
+    """dz = dy act'(z) (z and dz None without an activation), dbias (or None) and dx = dz w (w and dx may
+    both be None)."""
+    dev, s = _place(dy, "dy", stream)
+    m, n = lin.rows, lin.outs
+    pdy, _, _, lddy = _matrix(dy, dev, "dy", lin.dtype, m, n)
+    pwt, ldw = _opt_matrix(w, dev, "w", lin.dtype, n, lin.cols)
+    pdx, lddx = _opt_matrix(dx, dev, "dx", lin.dtype, m, lin.cols)
+    pz, ldz = _opt_matrix(z, dev, "z", lin.dtype, m, n)
+    pdz, lddz = _opt_matrix(dz, dev, "dz", lin.dtype, m, n)
+    pw, nw = _buffer(ws, dev, "ws")
+    rc = lib().lags_linear_backward(lin.ref, pdy, lddy, pz, ldz, pwt, ldw, pdz, lddz, _vector(dbias, dev, n, "dbias"),
+                                    pdx, lddx, LAGS_GRAD_ADD if add else 0, pw, nw, s)
+    _check("lags_linear_backward", rc)

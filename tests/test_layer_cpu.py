@@ -135,6 +135,84 @@ def test_embedding_gradient_refusals():
     assert call(t=(1 << 31) - 1, v=100, c=1 << 22, lddy=1 << 22, wsn=1 << 62) == ERANGE
 
 
+def _lin(m=40, k=64, n=48, dtype=1, act=0):
+    return lags.LinearShape(m, k, n, dtype, act)
+
+
+BAD_LINEAR = [(dict(dtype=3), EINVAL), (dict(act=4), EINVAL), (dict(act=-1), EINVAL), (dict(m=-1), EINVAL),
+              (dict(k=0), EINVAL), (dict(n=0), EINVAL), (dict(m=1 << 31), ERANGE), (dict(k=(1 << 20) + 1), ERANGE),
+              (dict(n=(1 << 20) + 1), ERANGE), (dict(m=(1 << 31) - 1, n=1 << 20), ERANGE)]
+
+
+def test_linear_workspace():
+    L = lags.lib()
+    assert L.lags_linear_workspace_bytes(None) == 0
+    for kw, _ in BAD_LINEAR:
+        assert L.lags_linear_workspace_bytes(ctypes.byref(_lin(**kw))) == 0, kw
+    for kw in (dict(), dict(m=0), dict(m=1, k=1, n=1), dict(k=1 << 20, n=1 << 20), dict(m=1 << 24)):
+        assert L.lags_linear_workspace_bytes(ctypes.byref(_lin(**kw))) >= 16, kw
+
+
+def test_linear_forward_refusals():
+    L = lags.lib()
+    lin = _lin()
+    need = L.lags_linear_workspace_bytes(ctypes.byref(lin))
+
+    def call(s=lin, x=P(0), ldx=64, w=P(1), ldw=64, bias=P(2), res=P(3), ldr=48, z=P(4), ldz=48, y=P(5), ldy=48,
+             ws=P(6), wsn=need):
+        return L.lags_linear_forward(ctypes.byref(s) if s is not None else None, x, ldx, w, ldw, bias, res, ldr, z, ldz,
+                                     y, ldy, ws, wsn, None)
+    assert call(s=None) == EINVAL
+    for kw, rc in BAD_LINEAR:
+        assert call(s=_lin(**kw), ldx=1 << 20, ldw=1 << 20, ldr=1 << 20, ldz=1 << 20, ldy=1 << 20, wsn=1 << 62) == rc, kw
+    assert call(x=None) == EINVAL and call(w=None) == EINVAL and call(y=None) == EINVAL
+    for k, least in (("ldx", 64), ("ldw", 64), ("ldr", 48), ("ldz", 48), ("ldy", 48)):
+        assert call(**{k: least - 1}) == EINVAL and call(**{k: (1 << 20) + 1}) == ERANGE, k
+    for k in ("x", "w", "res", "z", "y"):
+        assert call(**{k: P(9) + 1}) == EINVAL, k
+    assert call(bias=P(2) + 2) == EINVAL
+    assert call(ws=None) == EWS and call(ws=P(6) + 4) == EWS and call(wsn=need - 1) == EWS
+    # y may be res itself, and nothing else
+    for at in (0, 1, 2, 4, 6):
+        assert call(y=P(at)) == EINVAL, at
+    assert call(y=P(3) + 32) == EINVAL and call(y=P(3), ldy=50) == EINVAL
+    for at in (0, 1, 2, 3, 5, 6):
+        assert call(z=P(at)) == EINVAL, at
+    for at in (0, 1, 2, 3):
+        assert call(ws=P(at)) == EINVAL, at
+    assert call(s=_lin(m=0)) == OK
+
+
+def test_linear_backward_refusals():
+    L = lags.lib()
+    lin, none = _lin(act=3), _lin()
+    need = L.lags_linear_workspace_bytes(ctypes.byref(lin))
+
+    def call(s=lin, dy=P(0), lddy=48, z=P(1), ldz=48, w=P(2), ldw=64, dz=P(3), lddz=48, db=P(4), dx=P(5), lddx=64,
+             flags=0, ws=P(6), wsn=need):
+        return L.lags_linear_backward(ctypes.byref(s) if s is not None else None, dy, lddy, z, ldz, w, ldw, dz, lddz, db,
+                                      dx, lddx, flags, ws, wsn, None)
+    assert call(s=None) == EINVAL
+    for kw, rc in BAD_LINEAR:
+        assert call(s=_lin(**{"act": 3, **kw}), lddy=1 << 20, ldz=1 << 20, ldw=1 << 20, lddz=1 << 20, lddx=1 << 20,
+                    wsn=1 << 62) == rc, kw
+    assert call(flags=2) == EINVAL
+    assert call(dy=None) == EINVAL and call(z=None) == EINVAL and call(dz=None) == EINVAL
+    assert call(w=None) == EINVAL and call(dx=None) == EINVAL              # both or neither
+    assert call(s=none) == EINVAL and call(s=none, z=None) == EINVAL and call(s=none, dz=None) == EINVAL
+    for k, least in (("lddy", 48), ("ldz", 48), ("ldw", 64), ("lddz", 48), ("lddx", 64)):
+        assert call(**{k: least - 1}) == EINVAL and call(**{k: (1 << 20) + 1}) == ERANGE, k
+    assert call(db=P(4) + 2) == EINVAL
+    assert call(ws=None) == EWS and call(ws=P(6) + 4) == EWS and call(wsn=need - 1) == EWS
+    for out in ("db", "dx", "ws"):
+        for at in (0, 1, 2, 3):
+            assert call(**{out: P(at)}) == EINVAL, (out, at)
+    assert call(dx=P(4)) == EINVAL and call(ws=P(5)) == EINVAL and call(ws=P(4)) == EINVAL
+    # dz may be dy or z itself
+    assert call(dz=P(2)) == EINVAL and call(dz=P(0) + 32) == EINVAL and call(dz=P(1), lddz=50) == EINVAL
+    assert call(s=_lin(m=0, act=3), db=None) == OK
+
+
 def test_binding_refuses_host_tensors():
     import torch
     x = torch.zeros(4, 8)
@@ -153,3 +231,12 @@ def test_binding_refuses_host_tensors():
         lags.lags_embed_grad(torch.zeros(4, dtype=torch.int64), x, x, None)
     with pytest.raises(ValueError):
         lags.embed_workspace(4, 0, 8)
+    lin = lags.Linear(4, 8, 8)
+    with pytest.raises(TypeError):
+        lags.lags_linear_forward(lin, x, x, x, None)
+    with pytest.raises(TypeError):
+        lags.lags_linear_backward(lin, x, None, None, None)
+    with pytest.raises(ValueError):
+        lags.Linear(4, 8, 8, act="tanh")
+    with pytest.raises(ValueError):
+        lags.linear_workspace(lags.Linear(4, 0, 8))
