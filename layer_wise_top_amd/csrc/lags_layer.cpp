@@ -95,12 +95,11 @@ struct LinearCall {
     DzPlan dz;
     size_t need;                     // workspace, of both directions
 };
-int plan(const lags_linear *l, LinearCall &c)
+int plan_anew(const lags_linear *l, LinearCall &c)
 {
-    if (int rc = check_linear(l); rc != LAGS_OK) return rc;
     const int64_t M = std::max<int64_t>(l->rows, 1);
-    c.fwd = linear_plan(l->dtype, M, l->outs, l->cols);
-    c.bwd = linear_plan(l->dtype, M, l->cols, l->outs);
+    c.fwd = linear_plan(l->dtype, false, M, l->outs, l->cols);
+    c.bwd = linear_plan(l->dtype, true, M, l->cols, l->outs);
     c.dz = dz_plan(l->dtype, M, l->outs);
     // threads of one launch: the product's, and those that join its slices
     for (const LinPlan *p : {&c.fwd, &c.bwd})
@@ -113,6 +112,27 @@ int plan(const lags_linear *l, LinearCall &c)
     const u128 most = std::max(std::max(f, b), d);
     c.need = l->rows ? (size_t)((most + 15) / 16 * 16) : 16;
     return LAGS_OK;
+}
+
+// The plan is a function of the shape alone; what it weighs takes the host a microsecond, as much as a
+// fifth of a small call, so each thread keeps the last shapes'.
+int plan(const lags_linear *l, LinearCall &c)
+{
+    if (int rc = check_linear(l); rc != LAGS_OK) return rc;
+    struct Kept {
+        lags_linear of;
+        LinearCall call;
+        int rc;
+    };
+    thread_local Kept kept[32];      // rows 0, cols 0 at first: no shape that is looked for
+    const uint64_t h = ((uint64_t)l->rows * 31 + l->cols) * 31 + l->outs * 7 + l->dtype;
+    Kept &k = kept[(h ^ h >> 17) % 32];
+    if (k.of.rows != l->rows || k.of.cols != l->cols || k.of.outs != l->outs || k.of.dtype != l->dtype) {
+        k.rc = plan_anew(l, k.call);
+        k.of = *l;
+    }
+    c = k.call;
+    return k.rc;
 }
 
 // How a product's operands get into LDS (lags_linear.h).

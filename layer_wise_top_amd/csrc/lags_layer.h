@@ -72,22 +72,27 @@ struct LinArgs {
     void *z, *y;                             // C + bias; act of it + res
     int64_t ldr, ldz, ldy;
     float *part;                             // slices' sums [split][M][N]; column sums [chunks][N]
-    uint32_t tm, tn, split, steps_per;       // tiles, slices of k, steps of 128 bytes a slice
+    uint32_t tm, tn, split, k_per;           // tiles, slices of k, what a slice has of it (whole steps)
     // dz = dy act'(zin) over M x N
     const void *dy, *zin;
     void *dz;
     int64_t lddy, lddz, rows_per;
     uint32_t tl, nslab;
 };
+// Tiles of the product (rows, columns) and their waves.
+struct LinTile {
+    int bm, bn, wm, wn;
+};
+constexpr LinTile kLinTiles[] = {{256, 256, 2, 4}, {128, 128, 2, 2}, {64, 64, 2, 2}, {32, 128, 1, 4}};
 struct LinPlan {
-    uint32_t tile, tm, tn, split, steps_per;
+    uint32_t tile, tm, tn, split, k_per;
 };
 struct DzPlan {
     uint32_t tl, nslab, chunks;
     int64_t rows_per;
 };
 constexpr int64_t kLinearMax = 1 << 20;      // cols, outs and every ld: 256 rows stay within 32-bit offsets
-LinPlan linear_plan(int dtype, int64_t M, int64_t N, int64_t K);
+LinPlan linear_plan(int dtype, bool backward, int64_t M, int64_t N, int64_t K);
 DzPlan dz_plan(int dtype, int64_t M, int64_t N);
 template <int D> hipError_t product(const LinPlan &p, LinArgs a, bool nn, int how, hipStream_t s);
 template <int D> hipError_t slopes(const DzPlan &p, LinArgs a, hipStream_t s);

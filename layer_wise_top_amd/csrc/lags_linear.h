@@ -176,7 +176,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
     const uint32_t band = tile / (8 * a.tn), in = tile - band * 8 * a.tn, high = min(8u, a.tm - band * 8);
     const int64_t m0 = (int64_t)(band * 8 + in % high) * BM;
     const uint32_t n0 = in / high * BN;
-    const uint32_t k0 = slice * a.steps_per * KS, k1 = min(a.K, k0 + a.steps_per * KS);
+    const uint32_t k0 = slice * a.k_per, k1 = min(a.K, k0 + a.k_per);
     const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
 
     // windows of the operands from this slice's k on; they end with the last valid value
@@ -285,10 +285,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
 
     const int mw = wave / WN * (BM / WM), nw = wave % WN * (BN / WN);
     f32x16 acc[NW][NX] = {};
-    auto products = [&](const char *buf, int q) {      // 32 bytes of k
-        u32x4 x[NX], w[NW];
-#pragma unroll
-        for (int j = 0; j < NX; ++j) x[j] = *(const u32x4 *)(buf + at_rows(mw + 32 * j + (lane & 31), 2 * q + (lane >> 5)));
+    // 32 bytes of k: the operands of the products, and these
+    auto fetch = [&](const char *buf, int q, u32x4 (&x)[NX], u32x4 (&w)[NW]) {
 #pragma unroll
         for (int i = 0; i < NW; ++i) {
             const int n = nw + 32 * i;
@@ -300,6 +298,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
                 for (int e = 0; e < 4; ++e)
                     w[i][e] = *(const uint32_t *)(buf + TA + ((8 * q + 4 * (lane >> 5) + e) * BN + n + (lane & 31)) * 4);
         }
+#pragma unroll
+        for (int j = 0; j < NX; ++j) x[j] = *(const u32x4 *)(buf + at_rows(mw + 32 * j + (lane & 31), 2 * q + (lane >> 5)));
+    };
+    auto products = [&](u32x4 (&x)[NX], u32x4 (&w)[NW]) {
 #pragma unroll
         for (int i = 0; i < NW; ++i)
 #pragma unroll
@@ -318,16 +320,37 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
         const char *buf = lds + cur * BUF;
         cur ^= 1;
         if constexpr (HOW == kDirect) {
+            // A quarter's operands are read between the products of the quarter before.  (16384 x 2048 ->
+            // 8192 bf16: 526 us left to the compiler, 507 so.  Not kept: a barrier only before the last quarter's
+            // products, with the next step's first operands read past it, and wave priorities: the same; loads
+            // spread over the quarters: slower, the last come late; steps of 64 bytes in a ring of three to
+            // five: the same, loads of 64-byte rows run at half the rate; four waves of 128 x 128: 611.)
+            u32x4 x[2][NX], w[2][NW];
+            fetch(buf, 0, x[0], w[0]);
             if (s + KS < k1) load_direct(lds + cur * BUF);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) products(buf, q);
+            for (int q = 0; q < 4; ++q) {
+                if (q < 3) fetch(buf, q + 1, x[(q + 1) & 1], w[(q + 1) & 1]);
+                products(x[q & 1], w[q & 1]);
+                if (q < 3)
+                    for (int r = 0; r < NX + NW * (!NN ? 1 : E == 2 ? 2 : 4); ++r) {
+                        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);       // a product
+                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // a read of LDS
+                    }
+                __builtin_amdgcn_sched_group_barrier(0x8, NX * NW * (E == 2 ? 1 : 4), 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         } else {
-            products(buf, 0);
-            products(buf, 1);
-            stage(lds + cur * BUF);
-            load();
-            products(buf, 2);
-            products(buf, 3);
+            u32x4 x[NX], w[NW];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (q == 2) {
+                    stage(lds + cur * BUF);
+                    load();
+                }
+                fetch(buf, q, x, w);
+                products(x, w);
+            }
         }
     }
 
@@ -379,7 +402,7 @@ template <int D> __global__ __launch_bounds__(256) void k_linear_join(LinArgs a)
     if (m >= a.M) return;
     const int left = (int)(a.N - n);
     float f[V] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (uint32_t s = 0; s < a.split; ++s) {
         const float *p = a.part + ((size_t)s * a.M + m) * a.N + n;
         for (int e = 0; e < V; e += 4) {
@@ -461,18 +484,19 @@ template <int D, int BM, int BN, int WM, int WN, bool NN> hipError_t run_linear(
 }
 template <int D, bool NN> hipError_t run_tile(uint32_t tile, const LinArgs &a, int how, hipStream_t s)
 {
+    constexpr LinTile t0 = kLinTiles[0], t1 = kLinTiles[1], t2 = kLinTiles[2], t3 = kLinTiles[3];
     switch (tile) {
-    case 0: return run_linear<D, 256, 256, 2, 4, NN>(a, how, s);
-    case 1: return run_linear<D, 128, 128, 2, 2, NN>(a, how, s);
-    case 2: return run_linear<D, 64, 64, 2, 2, NN>(a, how, s);
-    case 3: return run_linear<D, 32, 128, 1, 4, NN>(a, how, s);
+    case 0: return run_linear<D, t0.bm, t0.bn, t0.wm, t0.wn, NN>(a, how, s);
+    case 1: return run_linear<D, t1.bm, t1.bn, t1.wm, t1.wn, NN>(a, how, s);
+    case 2: return run_linear<D, t2.bm, t2.bn, t2.wm, t2.wn, NN>(a, how, s);
+    case 3: return run_linear<D, t3.bm, t3.bn, t3.wm, t3.wn, NN>(a, how, s);
     }
     return hipErrorInvalidValue;
 }
 
 template <int D> hipError_t product(const LinPlan &p, LinArgs a, bool nn, int how, hipStream_t s)
 {
-    a.tm = p.tm, a.tn = p.tn, a.split = p.split, a.steps_per = p.steps_per;
+    a.tm = p.tm, a.tn = p.tn, a.split = p.split, a.k_per = p.k_per;
     const hipError_t e = nn ? run_tile<D, true>(p.tile, a, how, s) : run_tile<D, false>(p.tile, a, how, s);
     if (e != hipSuccess || a.split == 1) return e;
     constexpr uint32_t V = Elem<D>::V;

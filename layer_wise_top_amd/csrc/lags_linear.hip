@@ -28,27 +28,57 @@ __global__ __launch_bounds__(64 * kBiasWaves) void k_linear_dbias(const float *p
     dbias[n] = add ? dbias[n] + s : s;
 }
 
-struct Tile {
-    int bm, bn;
-};
-constexpr Tile kTiles[] = {{256, 256}, {128, 128}, {64, 64}, {32, 128}};
-
 }  // namespace
 
-LinPlan linear_plan(int dtype, int64_t M, int64_t N, int64_t K)
+namespace {
+// Microseconds that a tile takes a step of 128 bytes of k on a compute unit that is full of them
+// (`alone`: when it is the only one on an idle card), and for its results, and how many a compute unit
+// holds; 16-bit values and fp32, whose steps are half as long.  Measured with 512 x 512 to 8192 x 4096 outputs over 2048 to 8192 of k; the backward product
+// takes 1.17 times as long, but as long with 32 x 128.
+struct Cost {
+    float full, alone, out;
+    int held;
+};
+constexpr Cost kCost[2][4] = {
+    {{1.75f, 1.25f, 4.0f, 1}, {0.52f, 0.60f, 1.0f, 2}, {0.198f, 0.47f, 0.3f, 5}, {0.23f, 0.47f, 0.3f, 4}},
+    {{7.7f, 7.5f, 4.0f, 1}, {2.0f, 2.05f, 1.0f, 2}, {0.53f, 0.68f, 0.3f, 5}, {0.54f, 0.70f, 0.3f, 4}}};
+}  // namespace
+
+// The tile and the slices of k with the least time by a model of it: the rounds of workgroups on 256
+// compute units, or the bytes of the operands; then the slices' sums, written and read again.
+//   700 x 6000 x 1500 fp32   127 us (64 x 64, 8 slices; 128 x 128 in 6: 138), the library's product 132
+//   1 x 2048 x 8192 bf16     9.9 us (64 x 64, 4 slices; whole 12)
+LinPlan linear_plan(int dtype, bool backward, int64_t M, int64_t N, int64_t K)
 {
-    LinPlan p = {};
-    const int64_t ks = 128 / elem_bytes(dtype), steps = (K + ks - 1) / ks;
-    // large tiles where there are enough of them; slices of k where there are few
-    p.tile = M <= 32 ? 3 : 2;
-    if (M * N >= (int64_t)128 * 128 * 200) p.tile = 1;
-    if (M * N >= (int64_t)256 * 256 * 200) p.tile = 0;
-    p.tm = (uint32_t)((M + kTiles[p.tile].bm - 1) / kTiles[p.tile].bm);
-    p.tn = (uint32_t)((N + kTiles[p.tile].bn - 1) / kTiles[p.tile].bn);
-    int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / ((int64_t)p.tm * p.tn), steps / 4));
-    p.steps_per = (uint32_t)((steps + want - 1) / want);
-    p.split = (uint32_t)((steps + p.steps_per - 1) / p.steps_per);
-    return p;
+    const int64_t e = elem_bytes(dtype), ks = 128 / e, steps = (K + ks - 1) / ks;
+    const double in = (double)(M * K + N * K) * e / 4.5e6, sums = (double)M * N * 4 / 4.5e6;
+    LinPlan best = {};
+    double least = 0;
+    for (uint32_t t = 0; t < 4; ++t) {
+        const Cost &c = kCost[dtype == kF32][t];
+        LinPlan p = {};
+        p.tile = t;
+        p.tm = (uint32_t)((M + kLinTiles[t].bm - 1) / kLinTiles[t].bm);
+        p.tn = (uint32_t)((N + kLinTiles[t].bn - 1) / kLinTiles[t].bn);
+        const double tiles = (double)p.tm * p.tn, slow = backward && dtype != kF32 && t != 3 ? 1.17 : 1;
+        int64_t last = 0;
+        for (int64_t want = 1; want <= 32 && want <= steps; want += want < 4 ? 1 : want / 4) {
+            const int64_t per = (steps + want - 1) / want;
+            if (per == last) continue;
+            last = per;
+            p.k_per = (uint32_t)std::min(per * ks, K);
+            p.split = (uint32_t)((steps + per - 1) / per);
+            // whole rounds of all the card holds, and the rest; a card that is part idle runs faster
+            const double units = tiles * p.split / 256, whole = std::floor(units / c.held) * c.held;
+            const double rest = units - whole, some = rest > 1 ? 1 : rest * rest;
+            const double step = whole * c.full + (rest ? std::fmax(std::ceil(rest) * c.full, c.alone) * some +
+                                                             c.alone * (1 - some) : 0);
+            double us = std::fmax(per * slow * step, in) + std::ceil(units) * c.out;
+            if (p.split > 1) us += 4.5 + 0.2 * p.split + sums * (p.split + 1);     // another launch, loads in turn
+            if (!least || us < least) least = us, best = p;
+        }
+    }
+    return best;
 }
 
 // 2^tl lanes of 16-byte vectors a slab, rows in chunks of about 2048 workgroups.
