@@ -4,11 +4,17 @@
 //
 // Forward: a gather bound by memory; a thread has four tokens' vectors in flight.
 // Gradient: the tokens are sorted by id (their order within an id kept), and
-// the sorted list is cut into chunks of kChunk tokens, so that a frequent id is
+// the sorted list is cut into chunks of 8 or 16 tokens, so that a frequent id is
 // the work of many workgroups.  A chunk adds up each id's rows in registers; an
 // id that lies within one chunk is written to the table's gradient, the others
 // leave a sum for each chunk, which are then added up in the order of the chunks.
 // No atomics on floats: results repeat bit for bit.
+//   lookup, 16384 tokens of 50304 x 2048, fp32 to bf16   26 us (3.4 TB/s with each row read once)
+//   gradient of the same                                 118 us (4.0 TB/s): 72 sorting beside 350 MB of
+//                                                        zeros, 40 the sums, 6 joining them
+//   gradient, 700 tokens of 10000 x 1500 fp32            22 us: 15, 4, 4
+// Many more tokens are bound by the sort of the most frequent ids in one workgroup: 200000 tokens of 50304 x
+// 512 take 333 us.
 #include "lags_gn.h"
 #include "lags_layer.h"
 
@@ -67,16 +73,20 @@ template <int TD, int D, bool WIDE, int U> __global__ __launch_bounds__(256) voi
 }
 
 // Tokens sorted by id: order[], their ids keys[], and start[v], the first place
-// of id v (start[vocab]: how many tokens have an id).  A workgroup owns a.w ids;
-// its 16 waves each read a section of all tokens, count the ids of its range,
-// and then place them: where an id's tokens of a section go follows from the
-// counts, the place within 64 tokens from comparing ids across the wave.
-//   16384 tokens of 50304 ids: see k_embed_sum
+// of id v (start[vocab]: how many tokens have an id); and (not adding) zeros in the
+// rows of ids without tokens.  A workgroup owns a.w ids.  Its 16 waves each read a
+// section of all tokens; within 64 of them a token's place among those of its id
+// comes from comparing ids across the wave, and the section's count so far from
+// LDS.  What ids and sections before it hold is added last.  The zeros, most of
+// the memory that a gradient writes, are written while workgroups with frequent
+// ids still sort (16384 tokens whose frequencies fall as 1 / rank: half of them in the first
+// of 256 workgroups).
 constexpr int kSortWaves = 16, kHeld = 16;
 template <bool WIDE> __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(EmbedArgs a)
 {
-    extern __shared__ uint32_t cnt[];               // [wave][a.w]
+    extern __shared__ uint32_t cnt[];               // [wave][a.w], then each id's count
     __shared__ uint32_t sum[kSortWaves], low[kSortWaves];
+    uint32_t *count = cnt + kSortWaves * a.w;
     const uint32_t lo = blockIdx.x * a.w, w = min(a.w, a.vocab - lo);
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     for (uint32_t i = threadIdx.x; i < kSortWaves * a.w; i += 64 * kSortWaves) cnt[i] = 0;
@@ -84,7 +94,7 @@ template <bool WIDE> __global__ __launch_bounds__(64 * kSortWaves) void k_embed_
     const int64_t per = (a.tokens + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64;
     const int64_t s0 = min(a.tokens, per * wave), s1 = min(a.tokens, s0 + per);
     uint32_t *mine = cnt + wave * a.w;
-    uint32_t id[kHeld], below = 0;
+    uint32_t id[kHeld], place[kHeld];
     auto load = [&](int64_t s) {
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
@@ -92,18 +102,45 @@ template <bool WIDE> __global__ __launch_bounds__(64 * kSortWaves) void k_embed_
             id[k] = t < s1 ? id_of<WIDE>(a, t) : kNone;
         }
     };
+    const int bits = 32 - __builtin_clz(a.w);
+    // A token's place among its id's, counted on from what `mine` holds.
+    auto rank = [&](uint32_t key, bool in) -> uint32_t {
+        const uint64_t all = __ballot(in);
+        uint32_t same0 = (uint32_t)all, same1 = (uint32_t)(all >> 32);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t m = __ballot(key >> b & 1);
+            const uint32_t mine1 = (uint32_t)((int)(key << (31 - b)) >> 31);          // all ones where the bit is set
+            same0 &= ~((uint32_t)m ^ mine1), same1 &= ~((uint32_t)(m >> 32) ^ mine1);
+        }
+        uint32_t at = 0;
+        if (in) {
+            const int first = same0 ? __builtin_ctz(same0) : 32 + __builtin_ctz(same1);
+            const uint32_t before = __builtin_amdgcn_mbcnt_hi(same1, __builtin_amdgcn_mbcnt_lo(same0, 0));
+            if ((int)lane == first) at = atomicAdd(mine + key, (uint32_t)(__builtin_popcount(same0) + __builtin_popcount(same1)));
+            at = __shfl(at, first) + before;
+        }
+        return at;
+    };
+    const bool held = per <= 64 * kHeld;             // a section stays in registers
+    uint32_t below = 0;
     for (int64_t s = s0; s < s1; s += 64 * kHeld) {
         load(s);
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
+            const uint32_t key = id[k] - lo;
+            const bool in = key < w;
             below += id[k] < lo;
-            if (id[k] - lo < w) atomicAdd(mine + (id[k] - lo), 1u);
+            if (!__ballot(in)) continue;
+            if (held)
+                place[k] = rank(key, in);
+            else if (in)
+                atomicAdd(mine + key, 1u);
         }
     }
     for (int o = 32; o; o >>= 1) below += __shfl_xor(below, o);
     if (lane == 0) low[wave] = below;
     __syncthreads();
-    // ids' totals, their exclusive sum over the range, and each wave's first place
+    // ids' counts, their exclusive sum over the range, and each wave's first place
     const uint32_t i = threadIdx.x;
     uint32_t total = 0;
     if (i < w)
@@ -119,6 +156,7 @@ template <bool WIDE> __global__ __launch_bounds__(64 * kSortWaves) void k_embed_
     for (uint32_t k = 0; k < kSortWaves; ++k) at += low[k] + (k < wave ? sum[k] : 0);
     if (i < w) {
         a.start[lo + i] = at;
+        count[i] = total;
         if (lo + i + 1 == a.vocab) a.start[a.vocab] = at + total;
         for (int k = 0; k < kSortWaves; ++k) {
             const uint32_t c = cnt[k * a.w + i];
@@ -127,62 +165,50 @@ template <bool WIDE> __global__ __launch_bounds__(64 * kSortWaves) void k_embed_
         }
     }
     __syncthreads();
-    const int bits = 32 - __builtin_clz(a.w);
     for (int64_t s = s0; s < s1; s += 64 * kHeld) {
-        if (s1 - s0 > 64 * kHeld) load(s);           // else they are still held
+        if (!held) load(s);
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
             const uint32_t key = id[k] - lo;
             const bool in = key < w;
-            uint64_t same = __ballot(in);
-            if (!same) continue;
-            for (int b = 0; b < bits; ++b) {
-                const uint64_t m = __ballot(key >> b & 1);
-                same &= key >> b & 1 ? m : ~m;
-            }
+            if (!__ballot(in)) continue;
+            uint32_t p = held ? place[k] : rank(key, in);
             if (in) {
-                const int first = __builtin_ctzll(same);
-                const uint32_t rank = __builtin_popcountll(same & ((1ull << lane) - 1));
-                uint32_t place = 0;
-                if ((int)lane == first) place = atomicAdd(mine + key, (uint32_t)__builtin_popcountll(same));
-                place = __shfl(place, first) + rank;
-                a.order[place] = (uint32_t)(s + k * 64 + lane);
-                a.keys[place] = id[k];
+                if (held) p += mine[key];
+                a.order[p] = (uint32_t)(s + k * 64 + lane);
+                a.keys[p] = id[k];
             }
+        }
+    }
+    if (a.add) return;
+    const uint32_t T = 1u << a.zl;                   // lanes a row of zeros
+    const f32x4_u4 zero = {0, 0, 0, 0};
+    for (uint32_t v = threadIdx.x >> a.zl; v < w; v += 64 * kSortWaves >> a.zl) {
+        if (count[v]) continue;
+        float *p = a.dtable + (size_t)(lo + v) * a.cols;
+        for (uint32_t c = (threadIdx.x & (T - 1)) * 4; c < a.cols; c += T * 4) {
+            if (c + 4 <= a.cols)
+                *(f32x4_u4 *)(p + c) = zero;
+            else
+                for (uint32_t j = c; j < a.cols; ++j) p[j] = 0;
         }
     }
 }
 
-// Sums of one chunk's tokens for each id in it, and (not adding) zeros for ids
-// without tokens.  2^tl lanes span a slab of a row's vectors, 64 of them at most; the
-// workgroups after the chunks' take rows of the table.
-constexpr uint32_t kChunk = 32, kAhead = 8, kZeroRows = 64;
+// Sums of one chunk's tokens for each id in it.  2^tl lanes span a slab of a row's
+// vectors, 64 of them at most.
+constexpr uint32_t kAhead = 8;
 template <int D> __global__ __launch_bounds__(256) void k_embed_sum(EmbedArgs a)
 {
     constexpr int V = Elem<D>::V, E = Elem<D>::E;
-    if (blockIdx.x >= a.sumwgs) {
-        const uint32_t T = 1u << a.zl, v0 = (blockIdx.x - a.sumwgs) * kZeroRows;
-        const f32x4_u4 zero = {0, 0, 0, 0};
-        for (uint32_t v = v0 + (threadIdx.x >> a.zl); v < min(a.vocab, v0 + kZeroRows); v += 256 >> a.zl) {
-            if (a.start[v] != a.start[v + 1]) continue;
-            float *p = a.dtable + (size_t)v * a.cols;
-            for (uint32_t c = (threadIdx.x & (T - 1)) * 4; c < a.cols; c += T * 4) {
-                if (c + 4 <= a.cols)
-                    *(f32x4_u4 *)(p + c) = zero;
-                else
-                    for (uint32_t j = c; j < a.cols; ++j) p[j] = 0;
-            }
-        }
-        return;
-    }
     const uint32_t T = 1u << a.tl;
     const uint64_t unit = (uint64_t)blockIdx.x * (256 >> a.tl) + (threadIdx.x >> a.tl);
     const uint32_t chunk = (uint32_t)(unit / a.nslab), slab = (uint32_t)(unit % a.nslab);
     const uint32_t c = (slab * T + (threadIdx.x & (T - 1))) * V;
     const int n = (int)a.cols - (int)c;
-    const uint32_t total = a.start[a.vocab], p0 = chunk * kChunk;
+    const uint32_t total = a.start[a.vocab], p0 = chunk * a.chunk;
     if (chunk >= a.nchunk || p0 >= total || n <= 0) return;
-    const uint32_t p1 = min(p0 + kChunk, total);
+    const uint32_t p1 = min(p0 + a.chunk, total);
     const uint32_t before = p0 ? a.keys[p0 - 1] : kNone, after = p1 < total ? a.keys[p1] : kNone;
     float acc[V] = {};
     uint32_t cur = a.keys[p0];
@@ -208,20 +234,20 @@ template <int D> __global__ __launch_bounds__(256) void k_embed_sum(EmbedArgs a)
         }
     };
     for (uint32_t p = p0; p < p1; p += kAhead) {
-        u32x4 v[kAhead];
-        uint32_t key[kAhead];
+        // eight places at a time; those past the last token's are not looked at
+        u32x4 v[kAhead], t[2], key[2];
+        for (int h = 0; h < 2; ++h) t[h] = *(const u32x4 *)(a.order + p + 4 * h), key[h] = *(const u32x4 *)(a.keys + p + 4 * h);
 #pragma unroll
         for (uint32_t k = 0; k < kAhead; ++k) {
-            const uint32_t q = min(p + k, p1 - 1);
-            key[k] = a.keys[q];
-            v[k] = load_vec<D>((const char *)a.dy + ((size_t)a.order[q] * a.lddy + c) * E, n);
+            const uint32_t token = p + k < p1 ? t[k / 4][k % 4] : t[0][0];
+            v[k] = load_vec<D>((const char *)a.dy + ((size_t)token * a.lddy + c) * E, n);
         }
 #pragma unroll
         for (uint32_t k = 0; k < kAhead; ++k) {
             if (p + k >= p1) break;
-            if (key[k] != cur) {
+            if (key[k / 4][k % 4] != cur) {
                 leave(false);
-                cur = key[k], first = false;
+                cur = key[k / 4][k % 4], first = false;
                 for (int j = 0; j < V; ++j) acc[j] = 0;
             }
             float f[V];
@@ -238,11 +264,11 @@ __global__ __launch_bounds__(256) void k_embed_join(EmbedArgs a)
 {
     __shared__ float4 sh[4][64];
     const uint32_t chunk = blockIdx.x / a.njoin, c = (blockIdx.x % a.njoin * 64 + (threadIdx.x & 63)) * 4;
-    const uint32_t total = a.start[a.vocab], p0 = chunk * kChunk, p1 = p0 + kChunk;
+    const uint32_t total = a.start[a.vocab], p0 = chunk * a.chunk, p1 = p0 + a.chunk;
     if (p1 >= total) return;
     const uint32_t v = a.keys[p1 - 1];
     if (a.keys[p1] != v || a.start[v] < p0) return;
-    const uint32_t n = (a.start[v + 1] - 1) / kChunk - chunk + 1;       // chunks with this id: this one's second sum, the others' first
+    const uint32_t n = (a.start[v + 1] - 1) / a.chunk - chunk + 1;       // chunks with this id: this one's second sum, the others' first
     const uint32_t wave = threadIdx.x >> 6, k0 = (uint32_t)((uint64_t)n * wave / 4), k1 = (uint32_t)((uint64_t)n * (wave + 1) / 4);
     const int left = (int)a.cols - (int)c;
     float4 s = {0, 0, 0, 0};
@@ -288,7 +314,10 @@ EmbedPlan embed_plan(int dtype, int64_t tokens, int64_t vocab, int64_t cols)
     EmbedPlan p = {};
     // ids a workgroup of the sort: 256 workgroups if the counts of 16 waves then stay within 32 KiB
     p.w = (uint32_t)std::min<int64_t>(512, (vocab + 255) / 256);
-    p.nchunk = (uint32_t)((tokens + kChunk - 1) / kChunk);
+    // Tokens a chunk: short ones fill the card where there are few.  us for 8, 16 and 32: 700 tokens of 1500
+    // fp32 22, 24, 28; 16384 of 2048 bf16 124, 118, 118 (1000 ids: 44, 40, 39).
+    p.chunk = tokens < 8192 ? 8 : 16;
+    p.nchunk = (uint32_t)((tokens + p.chunk - 1) / p.chunk);
     const uint32_t V = 16 / elem_bytes(dtype);
     const uint64_t vecs = (cols + V - 1) / V;
     p.tl = log2_up(vecs, 2, 6);
@@ -335,24 +364,22 @@ hipError_t launch_embed(EmbedArgs a, int table, int dtype, bool wide, hipStream_
 
 hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wide, hipStream_t s)
 {
-    a.w = p.w, a.nchunk = p.nchunk, a.tl = p.tl, a.nslab = p.nslab, a.njoin = p.njoin;
-    a.sumwgs = (uint32_t)p.sumwgs;
-    a.zl = log2_up(((uint64_t)a.cols + 3) / 4, 2, 8);
-    const uint32_t groups = (a.vocab + a.w - 1) / a.w, lds = kSortWaves * a.w * 4;
+    a.w = p.w, a.chunk = p.chunk, a.nchunk = p.nchunk, a.tl = p.tl, a.nslab = p.nslab, a.njoin = p.njoin;
+    a.zl = log2_up(((uint64_t)a.cols + 3) / 4, 2, 10);
+    const uint32_t groups = (a.vocab + a.w - 1) / a.w, lds = (kSortWaves + 1) * a.w * 4;
     if (wide)
         k_embed_sort<true><<<groups, 64 * kSortWaves, lds, s>>>(a);
     else
         k_embed_sort<false><<<groups, 64 * kSortWaves, lds, s>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    const uint32_t zero = a.add ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
-    if (a.sumwgs + zero) {
-        switch (dtype) {
-        case kF32: k_embed_sum<kF32><<<a.sumwgs + zero, 256, 0, s>>>(a); break;
-        case kBF16: k_embed_sum<kBF16><<<a.sumwgs + zero, 256, 0, s>>>(a); break;
-        default: k_embed_sum<kF16><<<a.sumwgs + zero, 256, 0, s>>>(a); break;
-        }
-        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (!a.nchunk) return hipSuccess;
+    const uint32_t sums = (uint32_t)p.sumwgs;
+    switch (dtype) {
+    case kF32: k_embed_sum<kF32><<<sums, 256, 0, s>>>(a); break;
+    case kBF16: k_embed_sum<kBF16><<<sums, 256, 0, s>>>(a); break;
+    default: k_embed_sum<kF16><<<sums, 256, 0, s>>>(a); break;
     }
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (a.nchunk < 2) return hipSuccess;
     k_embed_join<<<(uint32_t)((uint64_t)a.nchunk * a.njoin), 256, 0, s>>>(a);
     return hipGetLastError();

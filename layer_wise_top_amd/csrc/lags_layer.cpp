@@ -74,7 +74,7 @@ EmbedSpace embed_space(int64_t tokens, int64_t vocab, int64_t cols)
 {
     auto up = [](size_t n) { return (n + 15) / 16 * 16; };
     EmbedSpace w;
-    w.order = 0;
+    w.order = 0;                     // read eight at a time: what follows is the workspace's too
     w.keys = up((size_t)tokens * 4);
     w.start = w.keys + up((size_t)tokens * 4);
     w.part = w.start + up(((size_t)vocab + 1) * 4);
@@ -273,7 +273,7 @@ int lags_embed_grad(int64_t tokens, int64_t vocab, int64_t cols, const void *ids
     if (int rc = matrix(dy, tokens, cols, lddy, dtype, r[0]); rc != LAGS_OK) return rc;
     const EmbedPlan p = embed_plan(dtype, tokens, vocab, cols);
     // threads of one launch
-    if ((u128)(p.sumwgs + vocab / 64 + 1) * 256 > kMostThreads || (u128)p.nchunk * p.njoin * 256 > kMostThreads)
+    if ((u128)p.sumwgs * 256 > kMostThreads || (u128)p.nchunk * p.njoin * 256 > kMostThreads)
         return LAGS_ERANGE;
     const EmbedSpace w = embed_space(tokens, vocab, cols);
     if (!ws || !aligned(ws, 16) || ws_bytes < w.bytes) return LAGS_EWORKSPACE;

@@ -49,11 +49,11 @@ struct EmbedArgs {
     uint32_t *order, *keys, *start;
     float *part;
     uint32_t w;                              // ids a workgroup of the sort
-    uint32_t nchunk, tl, nslab;              // chunks, 2^tl lanes a slab, slabs a row
-    uint32_t sumwgs, zl, njoin;              // workgroups of the sums; 2^zl lanes a row of zeros; 256-channel parts
+    uint32_t chunk, nchunk, tl, nslab;       // tokens a chunk, chunks, 2^tl lanes a slab, slabs a row
+    uint32_t zl, njoin;                      // 2^zl lanes a row of zeros; 256-channel parts
 };
 struct EmbedPlan {
-    uint32_t w, nchunk, tl, nslab, njoin;
+    uint32_t w, chunk, nchunk, tl, nslab, njoin;
     uint64_t sumwgs;
 };
 EmbedPlan embed_plan(int dtype, int64_t tokens, int64_t vocab, int64_t cols);

@@ -116,8 +116,8 @@ def test_embedding_gradient_refusals():
     for kw, _ in BAD_EMBED:
         assert L.lags_embed_workspace_bytes(kw.get("t", 40), kw.get("v", 100), kw.get("c", 64)) == 0
     need = L.lags_embed_workspace_bytes(40, 100, 64)
-    # order and ids, first places, two sums for each 32 tokens
-    assert need == 160 + 160 + 416 + 2 * 2 * 64 * 4
+    # order and ids, first places, two sums for each 8 or 16 tokens
+    assert 160 + 160 + 416 + 3 * 2 * 64 * 4 <= need <= 160 + 160 + 416 + 5 * 2 * 64 * 4
 
     def call(t=40, v=100, c=64, ids=P(0), dy=P(1), lddy=64, dtype=1, scale=1.0, dt=P(2), flags=2, ws=P(3), wsn=need):
         return L.lags_embed_grad(t, v, c, ids, dy, lddy, dtype, scale, dt, flags, ws, wsn, None)
