@@ -93,7 +93,7 @@ int check_linear(const lags_linear *l)
 struct LinearCall {
     LinPlan fwd, bwd;
     DzPlan dz;
-    size_t need;                     // workspace, of both directions
+    size_t need, turned;             // workspace, of both directions; where W turned round is in it
 };
 int plan_anew(const lags_linear *l, LinearCall &c)
 {
@@ -110,7 +110,8 @@ int plan_anew(const lags_linear *l, LinearCall &c)
     // dbias is done before the product's sums are written
     const u128 d = (u128)c.dz.chunks * l->outs * 4;
     const u128 most = std::max(std::max(f, b), d);
-    c.need = l->rows ? (size_t)((most + 15) / 16 * 16) : 16;
+    c.turned = (size_t)((most + 15) / 16 * 16);
+    c.need = l->rows ? std::max<size_t>(c.turned + (c.bwd.turn ? (size_t)l->outs * l->cols * 2 : 0), 16) : 16;
     return LAGS_OK;
 }
 
@@ -382,9 +383,9 @@ int lags_linear_backward(const lags_linear *lin, const void *dy, int64_t lddy, c
     a = {};
     a.a = act ? dz : dy, a.lda = act ? lddz : lddy, a.b = w, a.ldb = ldw;
     a.M = M, a.N = (uint32_t)K, a.K = (uint32_t)N, a.act = LAGS_ACT_NONE, a.y = dx, a.ldy = lddx;
-    a.part = (float *)ws;
-    // along k for dz, along n for W
-    const int how = how_of({{a.a, a.lda}, {w, ldw}}, N | K, lin->dtype);
+    a.part = (float *)ws, a.turned = (char *)ws + c.turned;
+    // W's rows run along the product's columns; turned round, along the outs
+    const int how = c.bwd.turn && !how_of({{a.a, a.lda}}, N, lin->dtype) ? 0 : how_of({{a.a, a.lda}, {w, ldw}}, N | K, lin->dtype);
     return hip(launch_linear(c.bwd, a, true, how, lin->dtype, s));
 }
 

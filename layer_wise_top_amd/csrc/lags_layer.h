@@ -72,6 +72,7 @@ struct LinArgs {
     void *z, *y;                             // C + bias; act of it + res
     int64_t ldr, ldz, ldy;
     float *part;                             // slices' sums [split][M][N]; column sums [chunks][N]
+    void *turned;                            // W turned round
     uint32_t tm, tn, split, k_per;           // tiles, slices of k, what a slice has of it (whole steps)
     // dz = dy act'(zin) over M x N
     const void *dy, *zin;
@@ -86,6 +87,7 @@ struct LinTile {
 constexpr LinTile kLinTiles[] = {{256, 256, 2, 4}, {128, 128, 2, 2}, {64, 64, 2, 2}, {32, 128, 1, 4}};
 struct LinPlan {
     uint32_t tile, tm, tn, split, k_per;
+    bool turn;                               // backward: W is turned round first, where that can be used
 };
 struct DzPlan {
     uint32_t tl, nslab, chunks;

@@ -12,6 +12,8 @@
 #include "lags_gn.h"
 #include "lags_layer.h"
 
+#include <type_traits>
+
 namespace lags {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -425,31 +427,47 @@ template <int D> __global__ __launch_bounds__(256) void k_linear_dz(LinArgs a)
     const int nv = (int)a.N - (int)n;
     const int64_t lo = (int64_t)chunk * a.rows_per, hi = min(a.M, lo + a.rows_per);
     float sum[V] = {};
-    if (nv > 0) {
+    // whole: every lane of the wave has a whole vector, so that no load stands behind a branch
+    auto pass = [&](auto whole, auto act) {
         constexpr int U = 4;
+        const int n_of = whole ? V : nv;
         for (int64_t m = lo + (threadIdx.x >> a.tl); m < hi; m += R * U) {
             u32x4 d[U], z[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t r = min(m + u * R, hi - 1);
-                d[u] = load_vec<D>((const char *)a.dy + (r * a.lddy + n) * E, nv);
-                if (a.zin) z[u] = load_vec<D>((const char *)a.zin + (r * a.ldz + n) * E, nv);
+                d[u] = load_vec<D>((const char *)a.dy + (r * a.lddy + n) * E, n_of);
+                if (act) z[u] = load_vec<D>((const char *)a.zin + (r * a.ldz + n) * E, n_of);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (m + u * R >= hi) break;
                 float f[V];
                 Elem<D>::unpack(d[u], f);
-                if (a.zin) {
+                if (act) {
                     float g[V];
                     Elem<D>::unpack(z[u], g);
-                    for (int j = 0; j < V; ++j) f[j] *= act_slope<D>(g[j], a.act);
-                    store_vec<D>((char *)a.dz + ((m + u * R) * a.lddz + n) * E, Elem<D>::pack(f), nv);
+                    for (int j = 0; j < V; ++j) f[j] *= act_slope<D>(g[j], act);
+                    store_vec<D>((char *)a.dz + ((m + u * R) * a.lddz + n) * E, Elem<D>::pack(f), n_of);
                 }
                 for (int j = 0; j < V; ++j) sum[j] += f[j];
             }
         }
-    }
+    };
+    auto with = [&](auto act) {
+        if (__all(nv >= V))
+            pass(std::true_type(), act);
+        else if (nv > 0)
+            pass(std::false_type(), act);
+    };
+    if (a.act == kActRelu)
+        with(std::integral_constant<int, kActRelu>());
+    else if (a.act == kActSilu)
+        with(std::integral_constant<int, kActSilu>());
+    else if (a.act == kActGelu)
+        with(std::integral_constant<int, kActGelu>());
+    else
+        with(std::integral_constant<int, kActNone>());
     if (!a.part) return;
     for (int j = 0; j < V; ++j) {
         float v = sum[j];
@@ -467,6 +485,34 @@ template <int D> __global__ __launch_bounds__(256) void k_linear_dz(LinArgs a)
             if (j < nv)
                 a.part[(size_t)chunk * a.N + n + j] =
                     (sh[0][j][col] + sh[1][j][col]) + (sh[2][j][col] + sh[3][j][col]);
+}
+
+// W [N][K] (a.b, a.ldb) turned round: out [K][N].  A workgroup turns 64 x 64
+// values in LDS.  8192 x 2048 bf16: see linear_plan.
+template <int D> __global__ __launch_bounds__(256) void k_linear_turn(LinArgs a, void *out)
+{
+    static_assert(Elem<D>::E == 2, "");
+    __shared__ uint16_t sh[64][66];
+    const uint32_t tk = (a.N + 63) / 64, n0 = blockIdx.x / tk * 64, k0 = blockIdx.x % tk * 64;   // a.N: W's columns
+    const uint32_t r = threadIdx.x >> 3, v = (threadIdx.x & 7) * 8;
+    u32x4 x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t n = n0 + r + 32 * i;
+        x[i] = n < a.K ? load_vec<D>((const uint16_t *)a.b + (int64_t)n * a.ldb + k0 + v, (int)a.N - (int)(k0 + v)) : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 4; ++j) *(uint32_t *)&sh[r + 32 * i][v + 2 * j] = x[i][j];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t k = k0 + r + 32 * i;
+        u32x4 y;
+        for (int j = 0; j < 4; ++j)
+            y[j] = (uint32_t)sh[v + 2 * j][r + 32 * i] | (uint32_t)sh[v + 2 * j + 1][r + 32 * i] << 16;
+        if (k < a.N) store_vec<D>((uint16_t *)out + (size_t)k * a.K + n0 + v, y, (int)a.K - (int)(n0 + v));
+    }
 }
 
 // ---- launches --------------------------------------------------------------
@@ -496,6 +542,13 @@ template <int D, bool NN> hipError_t run_tile(uint32_t tile, const LinArgs &a, i
 
 template <int D> hipError_t product(const LinPlan &p, LinArgs a, bool nn, int how, hipStream_t s)
 {
+    if constexpr (D != kF32)
+        if (nn && p.turn && how == kDirect) {
+            // a.N columns of W, a.K rows
+            k_linear_turn<D><<<((a.K + 63) / 64) * ((a.N + 63) / 64), 256, 0, s>>>(a, a.turned);
+            if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+            a.b = a.turned, a.ldb = a.K, nn = false;
+        }
     a.tm = p.tm, a.tn = p.tn, a.split = p.split, a.k_per = p.k_per;
     const hipError_t e = nn ? run_tile<D, true>(p.tile, a, how, s) : run_tile<D, false>(p.tile, a, how, s);
     if (e != hipSuccess || a.split == 1) return e;

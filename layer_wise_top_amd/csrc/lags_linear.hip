@@ -44,16 +44,16 @@ constexpr Cost kCost[2][4] = {
     {{7.7f, 7.5f, 4.0f, 1}, {2.0f, 2.05f, 1.0f, 2}, {0.53f, 0.68f, 0.3f, 5}, {0.54f, 0.70f, 0.3f, 4}}};
 }  // namespace
 
-// The tile and the slices of k with the least time by a model of it: the rounds of workgroups on 256
+// The tile and the slices of k with the least time by a model of it (`least`): the rounds of workgroups on 256
 // compute units, or the bytes of the operands; then the slices' sums, written and read again.
 //   700 x 6000 x 1500 fp32   127 us (64 x 64, 8 slices; 128 x 128 in 6: 138), the library's product 132
 //   1 x 2048 x 8192 bf16     9.9 us (64 x 64, 4 slices; whole 12)
-LinPlan linear_plan(int dtype, bool backward, int64_t M, int64_t N, int64_t K)
+static LinPlan plan_of(int dtype, bool backward, int64_t M, int64_t N, int64_t K, double &least)
 {
     const int64_t e = elem_bytes(dtype), ks = 128 / e, steps = (K + ks - 1) / ks;
     const double in = (double)(M * K + N * K) * e / 4.5e6, sums = (double)M * N * 4 / 4.5e6;
     LinPlan best = {};
-    double least = 0;
+    least = 0;
     for (uint32_t t = 0; t < 4; ++t) {
         const Cost &c = kCost[dtype == kF32][t];
         LinPlan p = {};
@@ -79,6 +79,20 @@ LinPlan linear_plan(int dtype, bool backward, int64_t M, int64_t N, int64_t K)
         }
     }
     return best;
+}
+
+LinPlan linear_plan(int dtype, bool backward, int64_t M, int64_t N, int64_t K)
+{
+    double as_is, turned;
+    LinPlan p = plan_of(dtype, backward, M, N, K, as_is);
+    // A large backward product of 16-bit values takes W turned round, in the workspace, rather than
+    // staged as it comes and transposed on the way to the registers; the plan is then the same for
+    // operands that cannot use it, whose sums have the same order.
+    if (!backward || dtype == kF32 || K % 8 || N * K > (int64_t)1 << 35) return p;      // more would be more threads than a launch has
+    LinPlan q = plan_of(dtype, false, M, N, K, turned);
+    if (turned + 4.5 + (double)N * K * 4 / 3.5e6 >= as_is) return p;
+    q.turn = true;
+    return q;
 }
 
 // 2^tl lanes of 16-byte vectors a slab, rows in chunks of about 2048 workgroups.

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 import act_reference as R
+from test_linear_plans import CASES
 
 pytestmark = pytest.mark.gpu
 DT = {"f32": "float32", "bf16": "bfloat16", "f16": "float16"}
@@ -149,6 +150,34 @@ def test_shapes(m, k, n, dtype):
         _check_backward(tag, dy, w, act, z, dz, db, dx, dtype)
     dz, db, dx = _backward(dy, w, "none")
     _check_backward(tag + " none", dy, w, "none", None, dz, db, dx, dtype)
+
+
+@pytest.mark.parametrize("dtype,key,shape", CASES)
+def test_every_tile(dtype, key, shape):
+    """Ragged tiles of every kind, whole and in slices, W as it is and turned round; compared on the GPU in
+    float64.  A slice at an odd offset gives the same bits."""
+    import torch
+    (m, k, n), back = shape, key[0]
+    g = torch.Generator(device="cuda").manual_seed(m + k + n)
+    inner, outer = (n, k) if back else (k, n)
+    a = torch.randn(m, inner, generator=g, device="cuda").to(_dt(dtype))
+    w = (torch.randn(n, k, generator=g, device="cuda") / inner ** 0.5).to(_dt(dtype))
+
+    def run(a, w):
+        return _backward(a, w, bias=False)[2] if back else _forward(a, w)[0]
+
+    got = run(a, w)
+    b = w.double() if back else w.double().t().contiguous()
+    want, mag = a.double() @ b, a.double().abs() @ b.abs()
+    lim = _sum_bound(inner, dtype) * mag * (1 + R.ROUND[dtype]) + R.ROUND[dtype] * want.abs() + R.TINY[dtype]
+    assert ((got.double() - want).abs() <= lim).all()
+    assert torch.equal(run(a, w), got)
+    for off in (1, 2):
+        wide = torch.full((m, inner + 5), float("nan"), dtype=a.dtype, device="cuda")
+        wide[:, off:off + inner] = a
+        wv = torch.full((n, k + 5), float("nan"), dtype=a.dtype, device="cuda")
+        wv[:, off:off + k] = w
+        assert torch.equal(run(wide[:, off:off + inner], w), got) and torch.equal(run(a, wv[:, off:off + k]), got)
 
 
 @pytest.mark.parametrize("dtype", list(DT))

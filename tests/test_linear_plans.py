@@ -1,0 +1,69 @@
+"""What a linear layer plans for a shape, on the host: tiles, slices of the summed index, and whether the
+backward turns W round."""
+import ctypes
+import random
+
+import pytest
+
+from layer_wise_top_amd import lags
+
+TILES = ((256, 256), (128, 128), (64, 64), (32, 128))
+# (rows, cols, outs) whose product, forward or backward, is made of ragged tiles of each kind, whole and in
+# slices; of 16-bit values and of fp32.  Keys: backward, tile, sliced, W turned round.
+SHAPES = {
+    "f32": {(0, 0, 0, 0): (3022, 19, 4742), (0, 0, 1, 0): (1681, 2239, 1164), (0, 1, 0, 0): (6353, 16, 454),
+            (0, 1, 1, 0): (1160, 837, 865), (0, 2, 0, 0): (1, 16, 66), (0, 2, 1, 0): (2, 322, 66),
+            (0, 3, 0, 0): (67, 17, 8685), (0, 3, 1, 0): (201, 394, 605), (1, 0, 0, 0): (1688, 8479, 8),
+            (1, 0, 1, 0): (2858, 731, 2240), (1, 1, 0, 0): (7059, 386, 11), (1, 1, 1, 0): (4366, 72, 877),
+            (1, 2, 0, 0): (1, 65, 8), (1, 2, 1, 0): (1, 65, 328), (1, 3, 0, 0): (66, 8393, 11),
+            (1, 3, 1, 0): (643, 207, 355)},
+    "bf16": {(0, 0, 0, 0): (8311, 19, 1410), (0, 0, 1, 0): (1538, 6546, 1219), (0, 1, 0, 0): (6353, 16, 456),
+             (0, 1, 1, 0): (1194, 1800, 530), (0, 2, 0, 0): (1, 16, 66), (0, 2, 1, 0): (2, 907, 67),
+             (0, 3, 0, 0): (67, 17, 8685), (0, 3, 1, 0): (195, 1035, 688), (1, 0, 0, 0): (5439, 2177, 8),
+             (1, 0, 0, 1): (8390, 910, 1976), (1, 0, 1, 0): (1701, 1158, 5326), (1, 0, 1, 1): (8365, 387, 5496),
+             (1, 1, 0, 0): (7059, 386, 11), (1, 1, 0, 1): (8351, 602, 2128), (1, 1, 1, 0): (1474, 461, 1896),
+             (1, 1, 1, 1): (6197, 273, 7536), (1, 2, 0, 0): (8202, 17, 8), (1, 2, 0, 1): (6630, 583, 2600),
+             (1, 2, 1, 0): (679, 129, 1288), (1, 3, 0, 0): (33, 16, 8), (1, 3, 1, 0): (34, 17, 927)},
+}
+SHAPES["f16"] = SHAPES["bf16"]
+CASES = [(dtype, key, shape) for dtype, t in SHAPES.items() for key, shape in t.items()]
+
+
+class LinPlan(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_uint32) for k in ("tile", "tm", "tn", "split", "k_per")] + [("turn", ctypes.c_bool)]
+
+
+def linear_plan(dtype, backward, rows, cols, outs):
+    """The library's own choice (lags::linear_plan, not part of the C ABI)."""
+    f = lags.lib()._ZN4lags11linear_planEiblll
+    f.restype, f.argtypes = LinPlan, [ctypes.c_int, ctypes.c_bool, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]
+    code = {"f32": lags.LAGS_F32, "bf16": lags.LAGS_BF16, "f16": lags.LAGS_F16}[dtype]
+    return f(code, bool(backward), rows, cols if backward else outs, outs if backward else cols)
+
+
+@pytest.mark.parametrize("dtype,key,shape", CASES)
+def test_shapes_take_every_path(dtype, key, shape):
+    backward, tile, sliced, turn = key
+    p = linear_plan(dtype, backward, *shape)
+    assert (p.tile, p.split > 1, p.turn) == (tile, bool(sliced), bool(turn))
+
+
+def test_tiles_and_slices_cover_the_product():
+    """Any shape: tiles cover the outputs, slices are whole steps of 128 bytes that cover the sum, none
+    empty, and the workspace holds what the plans write."""
+    rng = random.Random(1)
+    for _ in range(3000):
+        dtype = rng.choice(["f32", "bf16", "f16"])
+        rows, cols, outs = (int(2 ** rng.uniform(0, e)) for e in (15, 13, 13))
+        step = 32 if dtype == "f32" else 64
+        shape = lags.LinearShape(rows, cols, outs, {"f32": 0, "bf16": 1, "f16": 2}[dtype], 0)
+        need = int(lags.lib().lags_linear_workspace_bytes(ctypes.byref(shape)))
+        for back in (0, 1):
+            p = linear_plan(dtype, back, rows, cols, outs)
+            n, k = (cols, outs) if back else (outs, cols)
+            bm, bn = TILES[p.tile]
+            assert (p.tm - 1) * bm < rows <= p.tm * bm and (p.tn - 1) * bn < n <= p.tn * bn
+            assert (p.split - 1) * p.k_per < k <= p.split * p.k_per and (p.split == 1 or p.k_per % step == 0)
+            sums = 4 * p.split * rows * n if p.split > 1 else 0
+            assert need >= sums + (2 * cols * outs if p.turn else 0)
+            assert not p.turn or (back and dtype != "f32" and outs % 8 == 0)
