@@ -98,6 +98,7 @@ template <int D> __device__ inline void finish(const LinArgs &a, int64_t m, uint
 
 // ---- the product -----------------------------------------------------------
 constexpr int kStep = 128;                        // bytes of k staged at a time
+#define LAGS_INLINE __attribute__((always_inline))    // lambdas that take arrays of registers
 enum : int { kDirect = 0, kWords = 1, kHalves = 2 };   // see stage below
 
 // Byte offset of 16-byte vector v of row r in a tile of 128-byte rows: a read of
@@ -157,6 +158,12 @@ __device__ inline uint32_t deal(uint32_t b, uint32_t n)
 }
 
 // A workgroup: a BM x BN tile of the product over one slice of k; WM x WN waves.
+// The loop (direct loads): a step is 128 bytes of k, in quarters; a quarter's operands are read
+// from LDS between the products of the quarter before, and the loads of steps to come are issued
+// between products too, a few at a time, since a burst of them keeps the waves from issuing anything
+// else for half a step.  Loads need most of a step to arrive: A has three places in LDS and B two (160 KB
+// with 256 x 256), so that B's for the next step but one follow the barrier that frees their place, and A's
+// come after them, a step ahead of need.  One barrier a step, before its last quarter.
 // NN: B is [k][n].  HOW a tile gets into LDS: kDirect, loads that write it themselves
 // (operands of whole, aligned 16-byte vectors); kWords and kHalves, through
 // registers, rows that start on any word, or on any half of one (five words are
@@ -179,7 +186,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
     const int64_t m0 = (int64_t)(band * 8 + in % high) * BM;
     const uint32_t n0 = in / high * BN;
     const uint32_t k0 = slice * a.k_per, k1 = min(a.K, k0 + a.k_per);
-    const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+    const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t >> 6), lane = t & 63;
 
     // windows of the operands from this slice's k on; they end with the last valid value
     const int64_t rows = min((int64_t)BM, a.M - m0);
@@ -189,7 +196,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
     int64_t lb, step_b;
     if constexpr (NN) {
         pb = (const char *)a.b + ((int64_t)k0 * a.ldb + n0) * E;
-        lb = ((int64_t)(a.K - k0 - 1) * a.ldb + (a.N - n0)) * E;
+        lb = ((int64_t)(k1 - k0 - 1) * a.ldb + (a.N - n0)) * E;
         step_b = KS * a.ldb * E;
     } else {
         pb = (const char *)a.b + ((int64_t)n0 * a.ldb + k0) * E;
@@ -217,21 +224,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
 
     uint32_t k = k0;                                   // what is loaded next
     auto move = [&] { k += KS, pa += kStep, la -= kStep, pb += step_b, lb -= step_b; };
-    // loads that write the tiles of the next step to `buf`
-    auto load_direct = [&](char *buf) {
-        const auto ra = window(pa, la), rb = window(pb, lb);
-        char *w = buf + (t & ~63) * 16;
-        const int left = (int)(a.K - k);               // vectors past the last k read as zeros
-#pragma unroll
-        for (int p = 0; p < PA; ++p)
-            load_to_lds(ra, w + p * kThreads * 16,
-                        left >= KS || vec_a(t + p * kThreads) * V < left ? oa[p] : 0x80000000u);
-#pragma unroll
-        for (int p = 0; p < PB; ++p)
-            load_to_lds(rb, w + TA + p * kThreads * 16,
-                        NN || left >= KS || vec_b(t + p * kThreads) * V < left ? ob[p] : 0x80000000u);
-        move();
-    };
     u32x4 va[HOW == kDirect ? 1 : PA], vb[HOW == kDirect ? 1 : PB];
     uint32_t xa[HOW == kHalves ? PA : 1], xb[HOW == kHalves ? PB : 1];
     int held = 0;                                      // how much of k the registers hold
@@ -287,62 +279,105 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
 
     const int mw = wave / WN * (BM / WM), nw = wave % WN * (BN / WN);
     f32x16 acc[NW][NX] = {};
-    // 32 bytes of k: the operands of the products, and these
-    auto fetch = [&](const char *buf, int q, u32x4 (&x)[NX], u32x4 (&w)[NW]) {
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            const int n = nw + 32 * i;
-            if constexpr (!NN)
-                w[i] = *(const u32x4 *)(buf + TA + at_rows(n + (lane & 31), 2 * q + (lane >> 5)));
-            else if constexpr (E == 2)
-                w[i] = transposed<BN>(buf + TA, 16 * q, n);
-            else
-                for (int e = 0; e < 4; ++e)
-                    w[i][e] = *(const uint32_t *)(buf + TA + ((8 * q + 4 * (lane >> 5) + e) * BN + n + (lane & 31)) * 4);
+    // Operand f of a quarter's products (32 bytes of k; W's first, x's, W's others), and product p.
+    auto fetch = [&](const char *ta, const char *tb, int q, int f, u32x4 (&x)[NX], u32x4 (&w)[NW]) LAGS_INLINE {
+        const int j = f - 1, i = f == 0 ? 0 : f - NX;
+        if (j >= 0 && j < NX) {
+            x[j] = *(const u32x4 *)(ta + at_rows(mw + 32 * j + (lane & 31), 2 * q + (lane >> 5)));
+            return;
         }
-#pragma unroll
-        for (int j = 0; j < NX; ++j) x[j] = *(const u32x4 *)(buf + at_rows(mw + 32 * j + (lane & 31), 2 * q + (lane >> 5)));
+        const int n = nw + 32 * i;
+        if constexpr (!NN)
+            w[i] = *(const u32x4 *)(tb + at_rows(n + (lane & 31), 2 * q + (lane >> 5)));
+        else if constexpr (E == 2)
+            w[i] = transposed<BN>(tb, 16 * q, n);
+        else
+            for (int e = 0; e < 4; ++e)
+                w[i][e] = *(const uint32_t *)(tb + ((8 * q + 4 * (lane >> 5) + e) * BN + n + (lane & 31)) * 4);
     };
-    auto products = [&](u32x4 (&x)[NX], u32x4 (&w)[NW]) {
-#pragma unroll
-        for (int i = 0; i < NW; ++i)
-#pragma unroll
-            for (int j = 0; j < NX; ++j) acc[i][j] = multiply<D>(w[i], x[j], acc[i][j]);
+    constexpr int P = NX * NW, F = NX + NW;
+    auto product = [&](int p, u32x4 (&x)[NX], u32x4 (&w)[NW]) LAGS_INLINE {
+        acc[p / NX][p % NX] = multiply<D>(w[p / NX], x[p % NX], acc[p / NX][p % NX]);
     };
-    int cur = 0;
     if constexpr (HOW == kDirect) {
-        load_direct(lds);
+        const int steps = (int)((k1 - k0 + KS - 1) / KS);
+        const auto ra = window(pa, la), rb0 = window(pb, lb);
+        const int vec = vec_a(t) * V;
+        char *const wa = lds + wave * 1024, *const wb = wa + 3 * TA;
+        // loads l0 .. l1 - 1 of step i's rows of A to `to`, or of B
+        auto load_a = [&](char *to, int i, int l0, int l1) LAGS_INLINE {
+            const uint32_t kv = vec < (int)(k1 - k0) - i * KS ? i * kStep : 0x80000000u;
+#pragma unroll
+            for (int p = 0; p < PA; ++p)
+                if (p >= l0 && p < l1) load_to_lds(ra, to + p * kThreads * 16, oa[p] + kv);
+        };
+        auto load_b = [&](char *to, int i, int l0, int l1) LAGS_INLINE {
+            if constexpr (NN) {
+                const auto rb = window(pb + i * step_b, lb - i * step_b);
+#pragma unroll
+                for (int p = 0; p < PB; ++p)
+                    if (p >= l0 && p < l1) load_to_lds(rb, to + p * kThreads * 16, ob[p]);
+            } else {
+                const uint32_t kv = vec < (int)(k1 - k0) - i * KS ? i * kStep : 0x80000000u;
+#pragma unroll
+                for (int p = 0; p < PB; ++p)
+                    if (p >= l0 && p < l1) load_to_lds(rb0, to + p * kThreads * 16, ob[p] + kv);
+            }
+        };
+        // this wave's loads but the last `left`, its reads of LDS, and everybody else's
+        auto arrived = [&](auto left) LAGS_INLINE {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0x0070 | (left & 15) | (left >> 4) << 14);
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+        };
+        u32x4 x0[NX], w0[NW], x1[NX], w1[NW];
+        // a quarter's products, between them the reads of the next quarter's operands and n loads
+        auto quarter = [&](u32x4 (&x)[NX], u32x4 (&w)[NW], const char *ta, const char *tb, int q, u32x4 (&xn)[NX], u32x4 (&wn)[NW],
+                           int n, auto ld) LAGS_INLINE {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                product(p, x, w);
+#pragma unroll
+                for (int f = (p * F + P - 1) / P; f < ((p + 1) * F + P - 1) / P; ++f) fetch(ta, tb, q, f, xn, wn);
+                const int l0 = (p * n + P - 1) / P, l1 = ((p + 1) * n + P - 1) / P;
+                if (l1 > l0) ld(l0, l1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // steps past the last read as zeros: nobody looks at them
+        load_a(wa, 0, 0, PA);
+        load_b(wb, 0, 0, PB);
+        load_a(wa + TA, 1, 0, PA);
+        load_b(wb + BN * kStep, 1, 0, PB);
+        arrived(std::integral_constant<int, PA + PB>());
+#pragma unroll
+        for (int f = 0; f < F; ++f) fetch(lds, lds + 3 * TA, 0, f, x0, w0);
+        int ca = 0;                                    // A's place in its ring
+        constexpr int H = (PA + 1) / 2;
+        for (int s = 0; s < steps; ++s) {
+            const int cb = s & 1, na = ca == 2 ? 0 : ca + 1, fa = na == 2 ? 0 : na + 1;
+            const char *ta = lds + ca * TA, *tb = lds + 3 * TA + cb * (BN * kStep);
+            const char *ta1 = lds + na * TA, *tb1 = lds + 3 * TA + (cb ^ 1) * (BN * kStep);
+            char *la2 = wa + fa * TA, *lb2 = wb + cb * (BN * kStep);
+            quarter(x0, w0, ta, tb, 1, x1, w1, H, [&](int l0, int l1) LAGS_INLINE { load_a(la2, s + 2, l0, l1); });
+            quarter(x1, w1, ta, tb, 2, x0, w0, PA - H, [&](int l0, int l1) LAGS_INLINE { load_a(la2, s + 2, H + l0, H + l1); });
+            quarter(x0, w0, ta, tb, 3, x1, w1, 0, [&](int, int) {});
+            // all but the loads of A just issued have arrived, everybody has read this step's last operands
+            arrived(std::integral_constant<int, PA>());
+            quarter(x1, w1, ta1, tb1, 0, x0, w0, PB, [&](int l0, int l1) LAGS_INLINE { load_b(lb2, s + 2, l0, l1); });
+            ca = na;
+        }
+        arrived(std::integral_constant<int, 0>());     // the loads past the last step, before LDS is used again
     } else {
         load();
         stage(lds);
         load();
-    }
-    for (uint32_t s = k0; s < k1; s += KS) {
-        __syncthreads();
-        const char *buf = lds + cur * BUF;
-        cur ^= 1;
-        if constexpr (HOW == kDirect) {
-            // A quarter's operands are read between the products of the quarter before.  (16384 x 2048 ->
-            // 8192 bf16: 526 us left to the compiler, 507 so.  Not kept: a barrier only before the last quarter's
-            // products, with the next step's first operands read past it, and wave priorities: the same; loads
-            // spread over the quarters: slower, the last come late; steps of 64 bytes in a ring of three to
-            // five: the same, loads of 64-byte rows run at half the rate; four waves of 128 x 128: 611.)
-            u32x4 x[2][NX], w[2][NW];
-            fetch(buf, 0, x[0], w[0]);
-            if (s + KS < k1) load_direct(lds + cur * BUF);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (q < 3) fetch(buf, q + 1, x[(q + 1) & 1], w[(q + 1) & 1]);
-                products(x[q & 1], w[q & 1]);
-                if (q < 3)
-                    for (int r = 0; r < NX + NW * (!NN ? 1 : E == 2 ? 2 : 4); ++r) {
-                        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);       // a product
-                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // a read of LDS
-                    }
-                __builtin_amdgcn_sched_group_barrier(0x8, NX * NW * (E == 2 ? 1 : 4), 0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        } else {
+        int cur = 0;
+        for (uint32_t s = k0; s < k1; s += KS) {
+            __syncthreads();
+            const char *buf = lds + cur * BUF;
+            cur ^= 1;
             u32x4 x[NX], w[NW];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -350,15 +385,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
                     stage(lds + cur * BUF);
                     load();
                 }
-                fetch(buf, q, x, w);
-                products(x, w);
+#pragma unroll
+                for (int f = 0; f < F; ++f) fetch(buf, buf + TA, q, f, x, w);
+#pragma unroll
+                for (int p = 0; p < P; ++p) product(p, x, w);
             }
         }
+        __syncthreads();
     }
 
     // Each wave turns 32 rows of 64 (or 32) sums round in LDS of its own, so that a lane has
     // consecutive columns of a row.
-    __syncthreads();
     constexpr int CW = NW >= 2 ? 64 : 32, PITCH = CW + 4, QW = CW / 32;
     float *own = (float *)lds + wave * 32 * PITCH;
     constexpr int LR = CW / V, RP = 64 / LR;           // lanes a row, rows at a time
@@ -518,8 +555,10 @@ template <int D> __global__ __launch_bounds__(256) void k_linear_turn(LinArgs a,
 // ---- launches --------------------------------------------------------------
 template <int D, int BM, int BN, int WM, int WN, bool NN> hipError_t run_linear(const LinArgs &a, int how, hipStream_t s)
 {
-    constexpr int turn = WM * WN * 32 * (BN / WN >= 64 ? 68 : 36) * 4, two = 2 * (BM + BN) * kStep;
-    constexpr int lds = two > turn ? two : turn;
+    constexpr int turn = WM * WN * 32 * (BN / WN >= 64 ? 68 : 36) * 4, ring = (3 * BM + 2 * BN) * kStep;
+    constexpr int two = 2 * (BM + BN) * kStep;
+    static_assert(two >= turn, "the results' turn fits");
+    const int lds = how == kDirect ? ring : two;
     auto k = k_linear<D, BM, BN, WM, WN, NN, kDirect>;
     if (how == kWords) k = k_linear<D, BM, BN, WM, WN, NN, kWords>;
     if constexpr (D != kF32)
