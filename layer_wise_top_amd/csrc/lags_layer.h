@@ -73,6 +73,8 @@ struct LinArgs {
     int64_t ldr, ldz, ldy;
     float *part;                             // slices' sums [split][M][N]; column sums [chunks][N]
     void *turned;                            // W turned round
+    uint32_t whole, past;                    // y, z and res have rows of whole vectors from whole words; they are
+                                             // stored past the caches
     uint32_t tm, tn, split, k_per;           // tiles, slices of k, what a slice has of it (whole steps)
     // dz = dy act'(zin) over M x N
     const void *dy, *zin;

@@ -96,6 +96,15 @@ template <int D> __device__ inline void finish(const LinArgs &a, int64_t m, uint
     store_vec<D>((char *)a.y + (m * a.ldy + n) * E, Elem<D>::pack(f), nv);
 }
 
+// 16 bytes to a row; `past`: past the caches.
+__device__ inline void put_row(u32x4 v, __amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t past)
+{
+    if (past)
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 2);
+    else
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
+}
+
 // ---- the product -----------------------------------------------------------
 constexpr int kStep = 128;                        // bytes of k staged at a time
 #define LAGS_INLINE __attribute__((always_inline))    // lambdas that take arrays of registers
@@ -399,25 +408,83 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
     constexpr int CW = NW >= 2 ? 64 : 32, PITCH = CW + 4, QW = CW / 32;
     float *own = (float *)lds + wave * 32 * PITCH;
     constexpr int LR = CW / V, RP = 64 / LR;           // lanes a row, rows at a time
+    auto turn = [&](int i0, int j) LAGS_INLINE {
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < QW; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *(f32x4 *)(own + (lane & 31) * PITCH + 32 * i + 8 * r + 4 * (lane >> 5)) =
+                    f32x4{acc[i0 + i][j][4 * r], acc[i0 + i][j][4 * r + 1], acc[i0 + i][j][4 * r + 2], acc[i0 + i][j][4 * r + 3]};
+        wave_sync();
+    };
+    auto row = [&](int r, float (&f)[V]) LAGS_INLINE {
+        for (int e = 0; e < V; e += 4) *(f32x4 *)(f + e) = *(const f32x4 *)(own + r * PITCH + lane % LR * V + e);
+    };
+    // Rows of whole vectors from whole words go through windows that end with the last row, so that no
+    // store stands behind a branch.
+    auto rows_at = [&](const void *p, int64_t ld, int e) LAGS_INLINE {
+        return window((const char *)p + (m0 * ld + n0) * e, p ? ((rows - 1) * ld + (a.N - n0)) * e : 0);
+    };
+    auto whole_rows = [&](auto act) LAGS_INLINE {
+        const auto ry = rows_at(a.y, a.ldy, E), rz = rows_at(a.z, a.ldz, E), rr = rows_at(a.res, a.ldr, E);
+        const auto rb = window(a.bias + n0, a.bias ? (int64_t)(a.N - n0) * 4 : 0);
+#pragma unroll
+        for (int i0 = 0; i0 < NW; i0 += QW) {
+            const uint32_t c = nw + 32 * i0 + lane % LR * V;
+            const bool on = n0 + c < a.N;
+            float b[V];
+            for (int e = 0; e < V; e += 4)
+                *(u32x4 *)(b + e) = __builtin_amdgcn_raw_buffer_load_b128(rb, on ? (c + e) * 4 : 0x80000000u, 0, 0);
+#pragma unroll
+            for (int j = 0; j < NX; ++j) {
+                turn(i0, j);
+                const uint32_t r1 = mw + 32 * j + lane / LR;
+                uint32_t oy = on ? (r1 * (uint32_t)a.ldy + c) * E : 0x80000000u, oz = on ? (r1 * (uint32_t)a.ldz + c) * E : 0x80000000u;
+                uint32_t orr = on ? (r1 * (uint32_t)a.ldr + c) * E : 0x80000000u;
+#pragma unroll
+                for (int r0 = 0; r0 < 32; r0 += RP) {
+                    float f[V];
+                    row(r0 + lane / LR, f);
+                    if (a.bias)
+                        for (int e = 0; e < V; ++e) f[e] += b[e];
+                    if (a.z) put_row(Elem<D>::pack(f), rz, oz, a.past);
+                    if constexpr (act != kActNone)
+                        for (int e = 0; e < V; ++e) f[e] = act_value<D>(f[e], act);
+                    if (a.res) {
+                        float g[V];
+                        Elem<D>::unpack(__builtin_amdgcn_raw_buffer_load_b128(rr, orr, 0, 0), g);
+                        for (int e = 0; e < V; ++e) f[e] += g[e];
+                    }
+                    put_row(Elem<D>::pack(f), ry, oy, a.past);
+                    oy += RP * (uint32_t)a.ldy * E, oz += RP * (uint32_t)a.ldz * E, orr += RP * (uint32_t)a.ldr * E;
+                }
+            }
+        }
+    };
+    if (a.whole && a.split == 1) {
+        if (a.act == kActRelu)
+            whole_rows(std::integral_constant<int, kActRelu>());
+        else if (a.act == kActSilu)
+            whole_rows(std::integral_constant<int, kActSilu>());
+        else if (a.act == kActGelu)
+            whole_rows(std::integral_constant<int, kActGelu>());
+        else
+            whole_rows(std::integral_constant<int, kActNone>());
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < NX; ++j)
 #pragma unroll
         for (int i0 = 0; i0 < NW; i0 += QW) {
-#pragma unroll
-            for (int i = 0; i < QW; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    *(f32x4 *)(own + (lane & 31) * PITCH + 32 * i + 8 * r + 4 * (lane >> 5)) =
-                        f32x4{acc[i0 + i][j][4 * r], acc[i0 + i][j][4 * r + 1], acc[i0 + i][j][4 * r + 2], acc[i0 + i][j][4 * r + 3]};
-            wave_sync();
+            turn(i0, j);
             const uint32_t n = n0 + nw + 32 * i0 + lane % LR * V;
             const int nv = (int)a.N - (int)n;
-#pragma unroll
-            for (int r0 = 0; r0 < 32; r0 += RP) {
-                const int r = r0 + lane / LR;
+#pragma unroll 1
+            for (int r = lane / LR; r < 32; r += RP) {
                 const int64_t m = m0 + mw + 32 * j + r;
                 float f[V];
-                for (int e = 0; e < V; e += 4) *(f32x4 *)(f + e) = *(const f32x4 *)(own + r * PITCH + lane % LR * V + e);
+                row(r, f);
                 if (m >= a.M || nv <= 0) continue;
                 if (a.split > 1) {
                     float *out = a.part + ((size_t)slice * a.M + m) * a.N + n;
@@ -426,7 +493,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_linear(LinArgs a)
                     finish<D>(a, m, n, nv, f);
                 }
             }
-            wave_sync();
         }
 }
 
