@@ -11,6 +11,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblags.so")
@@ -83,7 +84,7 @@ _lib = None
 def lib():
     """Load liblags.so (raises if it has not been built).
 
-    torch is imported first: its HIP runtime (torch/lib/libamdhip64.so, soname
+    torch is imported first (above): its HIP runtime (torch/lib/libamdhip64.so, soname
     libamdhip64.so.7) must be the one the library binds to, since the device
     pointers and streams passed in come from torch.  Loaded the other way
     round, the library would pull the system runtime under its soname and
@@ -94,7 +95,6 @@ def lib():
         return _lib
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built; run `python -m layer_wise_top_amd.build`")
-    import torch  # noqa: F401  (binds the library to torch's HIP runtime)
     L = ctypes.CDLL(LIB_PATH)
     i32, i64, u32, vp, sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
                              ctypes.c_void_p, ctypes.c_size_t)
@@ -255,14 +255,12 @@ class Layout:
 
 
 def _stream_handle(stream):
-    import torch
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(int(stream.cuda_stream))
 
 
 def _dev_tensor(t, dtype, numel: int, name: str):
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
     if t.dtype != dtype:
@@ -277,7 +275,6 @@ def workspace(layout: Layout, P: int = 1, device=None, stream=None):
     workers and initialise it (lags_workspace_init on `stream`, then that
     stream is synchronised, so the workspace is ready for calls on any
     stream)."""
-    import torch
     nbytes = layout.workspace_bytes(P)
     if nbytes == 0:
         raise ValueError("invalid P")
@@ -289,7 +286,6 @@ def workspace(layout: Layout, P: int = 1, device=None, stream=None):
 
 def lags_workspace_init(layout: Layout, ws, P: int = 1, stream=None):
     """Copy the layout's tables (and the chunk tables for P workers) into ws."""
-    import torch
     w = _dev_tensor(ws, torch.uint8, 1, "ws")
     rc = lib().lags_workspace_init(layout.handle, w, ws.numel(), int(P), _stream_handle(stream))
     _check("lags_workspace_init", rc)
@@ -297,7 +293,6 @@ def lags_workspace_init(layout: Layout, ws, P: int = 1, stream=None):
 
 def lags_sparsify_layers(layout: Layout, grad, residual, msg_idx, msg_val, ws,
                          flags: int = 0, stream=None):
-    import torch
     g = _dev_tensor(grad, torch.float32, layout.n, "grad")
     r = _dev_tensor(residual, torch.float32, layout.n, "residual")
     mi = _dev_tensor(msg_idx, torch.int32, layout.K, "msg_idx")  # uint32 bits
@@ -311,7 +306,6 @@ def lags_sparsify_layers(layout: Layout, grad, residual, msg_idx, msg_val, ws,
 def lags_sparsify_layers_static(layout: Layout, grad, residual, msg_idx, msg_val, flags: int = 0,
                                 stream=None):
     """lags_sparsify_layers on the library's static scratch (no workspace)."""
-    import torch
     g = _dev_tensor(grad, torch.float32, layout.n, "grad")
     r = _dev_tensor(residual, torch.float32, layout.n, "residual")
     mi = _dev_tensor(msg_idx, torch.int32, layout.K, "msg_idx")
@@ -323,7 +317,6 @@ def lags_sparsify_layers_static(layout: Layout, grad, residual, msg_idx, msg_val
 
 def lags_aggregate_apply(layout: Layout, weights, msg_idx, msg_val, P: int, lr: float, ws,
                          stream=None):
-    import torch
     wt = _dev_tensor(weights, torch.float32, layout.n, "weights")
     mi = _dev_tensor(msg_idx, torch.int32, int(P) * layout.K, "msg_idx")
     mv = _dev_tensor(msg_val, torch.float32, int(P) * layout.K, "msg_val")
@@ -336,7 +329,6 @@ def lags_aggregate_apply(layout: Layout, weights, msg_idx, msg_val, P: int, lr: 
 def lags_sparsify_range(layout: Layout, l0: int, l1: int, grad, residual, msg_idx, msg_val, ws,
                         flags: int = 0, stream=None):
     """Layers [l0, l1) only; the buffers are the full-model ones."""
-    import torch
     g = _dev_tensor(grad, torch.float32, layout.n, "grad")
     r = _dev_tensor(residual, torch.float32, layout.n, "residual")
     mi = _dev_tensor(msg_idx, torch.int32, layout.K, "msg_idx")
@@ -350,7 +342,6 @@ def lags_sparsify_range(layout: Layout, l0: int, l1: int, grad, residual, msg_id
 def lags_aggregate_range(layout: Layout, l0: int, l1: int, weights, msg_idx, msg_val, P: int,
                          lr: float, ws, stream=None):
     """Layers [l0, l1) only; the buffers are the full-model ones."""
-    import torch
     wt = _dev_tensor(weights, torch.float32, layout.n, "weights")
     mi = _dev_tensor(msg_idx, torch.int32, int(P) * layout.K, "msg_idx")
     mv = _dev_tensor(msg_val, torch.float32, int(P) * layout.K, "msg_val")
@@ -409,7 +400,6 @@ def lags_adaptive_k(off, backward_time, P: int, alpha: float, beta: float,
 
 
 def lags_workspace_report(layout: Layout, ws, stream=None) -> dict:
-    import torch
     w = _dev_tensor(ws, torch.uint8, 1, "ws")
     rep = Report()
     rc = lib().lags_workspace_report(layout.handle, w, ws.numel(), _stream_handle(stream),
@@ -440,28 +430,27 @@ def kernel_names():
 # arguments costs more than the kernels.  Each check asks torch once, and
 # pointers go to ctypes as plain integers.
 
-_DTYPES = {}
+_C, _F32, _U8 = torch._C, torch.float32, torch.uint8
+_DTYPES = {torch.float32: LAGS_F32, torch.bfloat16: LAGS_BF16, torch.float16: LAGS_F16}
 
 
 def _dtype_code(dtype) -> int:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: LAGS_F32, torch.bfloat16: LAGS_BF16, torch.float16: LAGS_F16})
-    if dtype not in _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    return _DTYPES[dtype]
+    return code
 
 
 def _place(first, name: str, stream):
     """(current device, raw stream): `stream`, or the current one.  `first`: a tensor of the call,
     checked before the device is asked for, so that this raises the same without one."""
-    import torch
-    if not isinstance(first, torch.Tensor) or not first.is_cuda:
-        raise TypeError(f"{name} must be a device tensor")
-    dev = torch.cuda.current_device()
-    if stream is not None:
-        return dev, stream.cuda_stream
-    return dev, torch._C._cuda_getCurrentRawStream(dev)
+    try:
+        if first.get_device() < 0:
+            raise TypeError(f"{name} must be a device tensor")
+    except AttributeError:
+        raise TypeError(f"{name} must be a device tensor") from None
+    dev = _C._cuda_getDevice()
+    return dev, _C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _on(t, dev: int, name: str):
@@ -480,6 +469,15 @@ def _matrix(t, dev: int, name: str, dtype=None, rows=None, cols=None):
     """A device tensor as a matrix: the last dimension is the columns, the others are rows that
     one pitch separates (a contiguous tensor, or a slice of its last dimension).  Returns
     (pointer, rows, cols, ld)."""
+    # what most calls bring: a contiguous matrix as it should be
+    try:
+        r, c = t.shape
+        if (c == cols or cols is None) and (r == rows or rows is None) and t.get_device() == dev and (
+                t.dtype is dtype or dtype is None) and t.is_contiguous():
+            # an empty tensor's address may be null, which the library refuses
+            return t.data_ptr() or (0 if r and c else 16), r, c, c
+    except (AttributeError, ValueError):
+        pass
     _on(t, dev, name)
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -491,7 +489,6 @@ def _matrix(t, dev: int, name: str, dtype=None, rows=None, cols=None):
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name} must hold {rows} rows of {cols} channels, got {tuple(shape)}")
     if t.is_contiguous():
-        # an empty tensor's address may be null, which the library refuses
         return t.data_ptr() or (0 if r and c else 16), r, c, c
     if c > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have its channels last and contiguous")
@@ -514,26 +511,30 @@ def _vector(t, dev: int, numel: int, name: str):
     """A contiguous fp32 device tensor of at least `numel` values, or None."""
     if t is None:
         return None
-    import torch
+    try:
+        if t.get_device() == dev and t.dtype is _F32 and t.is_contiguous() and t.numel() >= numel:
+            return t.data_ptr() or 16
+    except AttributeError:
+        pass
     _on(t, dev, name)
-    if t.dtype is not torch.float32:
-        raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
-    if t.numel() < numel or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with at least {numel} elements")
-    return t.data_ptr() or 16
+    if t.dtype is not _F32:
+        raise TypeError(f"{name} must be {_F32}, got {t.dtype}")
+    raise ValueError(f"{name} must be contiguous with at least {numel} elements")
 
 
 def _buffer(t, dev: int, name: str):
     """A uint8 device tensor (checkpoint or workspace), or None."""
     if t is None:
         return None, 0
-    import torch
+    try:
+        if t.get_device() == dev and t.dtype is _U8 and t.is_contiguous():
+            return t.data_ptr(), t.numel()
+    except AttributeError:
+        pass
     _on(t, dev, name)
-    if t.dtype is not torch.uint8:
-        raise TypeError(f"{name} must be {torch.uint8}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr(), t.numel()
+    if t.dtype is not _U8:
+        raise TypeError(f"{name} must be {_U8}, got {t.dtype}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def lags_ckpt_bytes(rows: int, cols: int) -> int:
@@ -542,7 +543,6 @@ def lags_ckpt_bytes(rows: int, cols: int) -> int:
 
 def checkpoint(rows: int, cols: int, device=None):
     """Allocate the 8-bit checkpoint buffer of a [rows, cols] matrix (uint8 device tensor)."""
-    import torch
     nbytes = lags_ckpt_bytes(rows, cols)
     if nbytes == 0 and rows != 0:
         raise ValueError("invalid checkpoint shape")
@@ -555,7 +555,8 @@ def lags_ckpt_pack(x, ckpt, stream=None):
     p, rows, cols, ld = _matrix(x, dev, "x")
     c, nb = _buffer(ckpt, dev, "ckpt")
     rc = lib().lags_ckpt_pack(rows, cols, p, ld, _dtype_code(x.dtype), c, nb, s)
-    _check("lags_ckpt_pack", rc)
+    if rc:
+        raise LagsError("lags_ckpt_pack", rc)
 
 
 def lags_ckpt_unpack(ckpt, x, stream=None):
@@ -564,7 +565,8 @@ def lags_ckpt_unpack(ckpt, x, stream=None):
     p, rows, cols, ld = _matrix(x, dev, "x")
     c, nb = _buffer(ckpt, dev, "ckpt")
     rc = lib().lags_ckpt_unpack(rows, cols, c, nb, p, ld, _dtype_code(x.dtype), s)
-    _check("lags_ckpt_unpack", rc)
+    if rc:
+        raise LagsError("lags_ckpt_unpack", rc)
 
 
 class GroupNorm:
@@ -572,7 +574,6 @@ class GroupNorm:
 
     def __init__(self, samples: int, spatial: int, channels: int, groups: int, dtype=None,
                  act: str = "none", eps: float = 1e-5):
-        import torch
         if act not in ACTS:
             raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
         self.dtype = dtype if dtype is not None else torch.float32
@@ -588,7 +589,6 @@ class GroupNorm:
 
 def gn_workspace(gn: GroupNorm, device=None):
     """Allocate a workspace for lags_gn_forward and lags_gn_backward of this shape."""
-    import torch
     nbytes = gn.workspace_bytes()
     if nbytes == 0:
         raise ValueError("invalid or unsupported group normalisation shape")
@@ -607,7 +607,8 @@ def lags_gn_forward(gn: GroupNorm, x, gamma, beta, y, mean, rstd, ws, ckpt=None,
     rc = lib().lags_gn_forward(
         gn.ref, px, ldx, _vector(gamma, dev, c, "gamma"), _vector(beta, dev, c, "beta"), py, ldy,
         _vector(mean, dev, gn.stats, "mean"), _vector(rstd, dev, gn.stats, "rstd"), pc, nc, pw, nw, s)
-    _check("lags_gn_forward", rc)
+    if rc:
+        raise LagsError("lags_gn_forward", rc)
 
 
 def lags_gn_backward(gn: GroupNorm, dy, gamma, beta, mean, rstd, dx, dgamma, dbeta, ws, x=None,
@@ -627,12 +628,12 @@ def lags_gn_backward(gn: GroupNorm, dy, gamma, beta, mean, rstd, dx, dgamma, dbe
         _vector(beta, dev, c, "beta"), _vector(mean, dev, gn.stats, "mean"),
         _vector(rstd, dev, gn.stats, "rstd"), pdx, lddx, _vector(dgamma, dev, c, "dgamma"),
         _vector(dbeta, dev, c, "dbeta"), LAGS_GRAD_ADD if add else 0, pw, nw, s)
-    _check("lags_gn_backward", rc)
+    if rc:
+        raise LagsError("lags_gn_backward", rc)
 
 
 def wgrad_workspace(rows: int, outs: int, cols: int, dtype, device=None):
     """Allocate a workspace for lags_ckpt_wgrad of these sizes and dY's dtype."""
-    import torch
     nbytes = int(lib().lags_ckpt_wgrad_workspace_bytes(int(rows), int(outs), int(cols), _dtype_code(dtype)))
     if nbytes == 0:
         raise ValueError("invalid weight gradient sizes")
@@ -651,7 +652,8 @@ def lags_ckpt_wgrad(dy, ckpt, dw, ws, add: bool = False, stream=None):
     pc, nc = _buffer(ckpt, dev, "ckpt")
     rc = lib().lags_ckpt_wgrad(rows, outs, dw.shape[1], pdy, lddy, _dtype_code(dy.dtype), pc, nc,
                                _vector(dw, dev, 0, "dw"), LAGS_GRAD_ADD if add else 0, pw, nw, s)
-    _check("lags_ckpt_wgrad", rc)
+    if rc:
+        raise LagsError("lags_ckpt_wgrad", rc)
 
 
 # ---- layer operators ---------------------------------------------------------
@@ -668,7 +670,6 @@ class LayerNorm:
     """A layer normalisation's shape (lags_ln): `rows` rows of `channels`."""
 
     def __init__(self, rows: int, channels: int, dtype=None, eps: float = 1e-5):
-        import torch
         self.dtype = dtype if dtype is not None else torch.float32
         self.shape = LnShape(int(rows), int(channels), _dtype_code(self.dtype), float(eps))
         self.ref = ctypes.byref(self.shape)
@@ -680,7 +681,6 @@ class LayerNorm:
 
 def ln_workspace(ln: LayerNorm, device=None):
     """Allocate a workspace for lags_ln_backward of this shape."""
-    import torch
     nbytes = ln.workspace_bytes()
     if nbytes == 0:
         raise ValueError("invalid or unsupported layer normalisation shape")
@@ -702,7 +702,8 @@ def lags_ln_forward(ln: LayerNorm, x, gamma, beta, y, mean, rstd, res=None, sum=
     rc = lib().lags_ln_forward(
         ln.ref, px, ldx, pr, ldr, _vector(gamma, dev, c, "gamma"), _vector(beta, dev, c, "beta"), ps, lds, py, ldy,
         _vector(mean, dev, r, "mean"), _vector(rstd, dev, r, "rstd"), pc, nc, pk, nk, s)
-    _check("lags_ln_forward", rc)
+    if rc:
+        raise LagsError("lags_ln_forward", rc)
 
 
 def lags_ln_backward(ln: LayerNorm, dy, gamma, mean, rstd, dx, dgamma, dbeta, ws, x=None, ckpt=None, dsum=None,
@@ -721,18 +722,19 @@ def lags_ln_backward(ln: LayerNorm, dy, gamma, mean, rstd, dx, dgamma, dbeta, ws
         ln.ref, pdy, lddy, px, ldx, pc, nc, _vector(gamma, dev, c, "gamma"), _vector(mean, dev, r, "mean"),
         _vector(rstd, dev, r, "rstd"), pd, ldd, pdx, lddx, _vector(dgamma, dev, c, "dgamma"),
         _vector(dbeta, dev, c, "dbeta"), LAGS_GRAD_ADD if add else 0, pw, nw, s)
-    _check("lags_ln_backward", rc)
+    if rc:
+        raise LagsError("lags_ln_backward", rc)
 
 
 def _ids(t, dev: int):
     """(pointer, count, flag) of a contiguous int32 or int64 device tensor of any shape."""
-    import torch
     _on(t, dev, "ids")
-    if t.dtype is not torch.int64 and t.dtype is not torch.int32:
-        raise TypeError(f"ids must be {torch.int64} or {torch.int32}, got {t.dtype}")
+    dtype = t.dtype
+    if dtype is not torch.int64 and dtype is not torch.int32:
+        raise TypeError(f"ids must be {torch.int64} or {torch.int32}, got {dtype}")
     if not t.is_contiguous():
         raise ValueError("ids must be contiguous")
-    return t.data_ptr() or 16, t.numel(), LAGS_IDS64 if t.dtype is torch.int64 else 0
+    return t.data_ptr() or 16, t.numel(), LAGS_IDS64 if dtype is torch.int64 else 0
 
 
 def lags_embed_forward(ids, table, y, scale: float = 1.0, stream=None):
@@ -747,12 +749,12 @@ def lags_embed_forward(ids, table, y, scale: float = 1.0, stream=None):
     py, _, _, ldy = _matrix(y, dev, "y", None, n, cols)
     rc = lib().lags_embed_forward(n, vocab, cols, pi, table.data_ptr(), _dtype_code(table.dtype), scale, py, ldy,
                                   _dtype_code(y.dtype), f, s)
-    _check("lags_embed_forward", rc)
+    if rc:
+        raise LagsError("lags_embed_forward", rc)
 
 
 def embed_workspace(tokens: int, vocab: int, cols: int, device=None):
     """Allocate a workspace for lags_embed_grad of these sizes."""
-    import torch
     nbytes = int(lib().lags_embed_workspace_bytes(int(tokens), int(vocab), int(cols)))
     if nbytes == 0:
         raise ValueError("invalid embedding sizes")
@@ -772,14 +774,14 @@ def lags_embed_grad(ids, dy, dtable, ws, scale: float = 1.0, add: bool = False, 
     pw, nw = _buffer(ws, dev, "ws")
     rc = lib().lags_embed_grad(n, vocab, cols, pi, pdy, lddy, _dtype_code(dy.dtype), scale,
                                _vector(dtable, dev, 0, "dtable"), f | (LAGS_GRAD_ADD if add else 0), pw, nw, s)
-    _check("lags_embed_grad", rc)
+    if rc:
+        raise LagsError("lags_embed_grad", rc)
 
 
 class Linear:
     """A linear layer's shape (lags_linear): [rows, cols] inputs, `outs` outputs."""
 
     def __init__(self, rows: int, cols: int, outs: int, dtype=None, act: str = "none"):
-        import torch
         if act not in LINEAR_ACTS:
             raise ValueError(f"act must be one of {sorted(LINEAR_ACTS)}, got {act!r}")
         self.dtype = dtype if dtype is not None else torch.float32
@@ -793,7 +795,6 @@ class Linear:
 
 def linear_workspace(lin: Linear, device=None):
     """Allocate a workspace for lags_linear_forward and lags_linear_backward of this shape."""
-    import torch
     nbytes = lin.workspace_bytes()
     if nbytes == 0:
         raise ValueError("invalid or unsupported linear layer shape")
@@ -812,7 +813,8 @@ def lags_linear_forward(lin: Linear, x, w, y, ws, bias=None, res=None, z=None, s
     pw, nw = _buffer(ws, dev, "ws")
     rc = lib().lags_linear_forward(lin.ref, px, ldx, pwt, ldw, _vector(bias, dev, n, "bias"), pr, ldr, pz, ldz, py,
                                    ldy, pw, nw, s)
-    _check("lags_linear_forward", rc)
+    if rc:
+        raise LagsError("lags_linear_forward", rc)
 
 
 def lags_linear_backward(lin: Linear, dy, w, dx, ws, z=None, dz=None, dbias=None, add: bool = False, stream=None):
@@ -828,4 +830,5 @@ def lags_linear_backward(lin: Linear, dy, w, dx, ws, z=None, dz=None, dbias=None
     pw, nw = _buffer(ws, dev, "ws")
     rc = lib().lags_linear_backward(lin.ref, pdy, lddy, pz, ldz, pwt, ldw, pdz, lddz, _vector(dbias, dev, n, "dbias"),
                                     pdx, lddx, LAGS_GRAD_ADD if add else 0, pw, nw, s)
-    _check("lags_linear_backward", rc)
+    if rc:
+        raise LagsError("lags_linear_backward", rc)
