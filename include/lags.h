@@ -570,6 +570,8 @@ int lags_ln_forward(const lags_ln *ln, const void *x, int64_t ldx, const void *r
  *                  of res; may be dy or dsum itself;
  *   dgamma, dbeta: device fp32[channels], out; each may be null;
  *   flags:         0 or LAGS_GRAD_ADD (dgamma and dbeta are added to).
+ * The order of dgamma's and dbeta's sums follows from the shape and from whether
+ * rows of 16-bit values start inside words.
  * With rows 0 dgamma and dbeta become 0 (unless added to).
  * Returns as lags_ln_forward, and LAGS_EWORKSPACE for ws.
  */

@@ -300,6 +300,62 @@ __global__ __launch_bounds__(256) void k_embed_join(EmbedArgs a)
         if (j < left) out[j] = a.add ? out[j] + f[j] : f[j];
 }
 
+// Few tokens: one launch.  Every wave holds all ids, kFew / 64 a lane; comparing
+// them with an id of its own gives that id's tokens as bits, in order, and the
+// wave adds up their rows, 64 vectors of them, or writes zeros.
+constexpr int kFewIds = 4;                           // a wave's ids
+template <int D, bool WIDE> __global__ __launch_bounds__(256) void k_embed_few(EmbedArgs a)
+{
+    constexpr int V = Elem<D>::V, E = Elem<D>::E, Q = kFew / 64, U = 8;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    uint32_t id[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) id[q] = q * 64 + lane < a.tokens ? id_of<WIDE>(a, q * 64 + lane) : kNone;
+    const uint32_t unit = blockIdx.x * 4 + wave, v0 = unit / a.nslab * kFewIds;
+    const uint32_t c = (unit % a.nslab * 64 + lane) * V;
+    const int n = (int)a.cols - (int)c;
+    for (uint32_t v = v0; v < min(a.vocab, v0 + kFewIds); ++v) {
+        uint64_t m[Q], any = 0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) any |= m[q] = __ballot(id[q] == v);
+        if (!any && a.add) continue;
+        if (n <= 0) continue;
+        float *out = a.dtable + (size_t)v * a.cols + c;
+        float acc[V] = {};
+        if (any)
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                for (uint64_t left = m[q]; left;) {
+                    u32x4 x[U];
+                    int k = 0;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int t = left ? __builtin_ctzll(left) : 0;
+                        if (left) x[u] = load_vec<D>((const char *)a.dy + ((q * 64 + t) * a.lddy + c) * E, n), ++k;
+                        left &= left - 1;
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        if (u >= k) break;
+                        float f[V];
+                        Elem<D>::unpack(x[u], f);
+                        for (int j = 0; j < V; ++j) acc[j] += f[j];
+                    }
+                }
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            if (i + 4 <= n) {
+                f32x4_u4 s = {acc[i] * a.scale, acc[i + 1] * a.scale, acc[i + 2] * a.scale, acc[i + 3] * a.scale};
+                if (a.add) s += *(f32x4_u4 *)(out + i);
+                *(f32x4_u4 *)(out + i) = s;
+            } else {
+                for (int j = i; j < i + 4; ++j)
+                    if (j < n) out[j] = a.add ? out[j] + acc[j] * a.scale : acc[j] * a.scale;
+            }
+        }
+    }
+}
+
 uint32_t log2_up(uint64_t n, uint32_t lo, uint32_t hi)
 {
     uint32_t l = lo;
@@ -312,6 +368,10 @@ uint32_t log2_up(uint64_t n, uint32_t lo, uint32_t hi)
 EmbedPlan embed_plan(int dtype, int64_t tokens, int64_t vocab, int64_t cols)
 {
     EmbedPlan p = {};
+    // One launch for a few tokens.  us in one and in three: 100 tokens of 100 x 100 fp32 6.5 and 12.2, 200 of 10000
+    // x 1500 13 and 21, 256 of 50304 x 2048 bf16 75 and 93; but 700 of 10000 x 1500 57 and 21, where the rows of a
+    // frequent id come 64 tokens at a time.
+    p.few = tokens <= kFew;
     // ids a workgroup of the sort: 256 workgroups if the counts of 16 waves then stay within 32 KiB
     p.w = (uint32_t)std::min<int64_t>(512, (vocab + 255) / 256);
     // Tokens a chunk: short ones fill the card where there are few.  us for 8, 16 and 32: 700 tokens of 1500
@@ -365,6 +425,20 @@ hipError_t launch_embed(EmbedArgs a, int table, int dtype, bool wide, hipStream_
 hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wide, hipStream_t s)
 {
     a.w = p.w, a.chunk = p.chunk, a.nchunk = p.nchunk, a.tl = p.tl, a.nslab = p.nslab, a.njoin = p.njoin;
+    if (p.few) {
+        const uint32_t V = 16 / elem_bytes(dtype);
+        a.nslab = ((a.cols + V - 1) / V + 63) / 64;
+        const uint64_t units = (uint64_t)((a.vocab + kFewIds - 1) / kFewIds) * a.nslab;
+        const uint32_t g = (uint32_t)((units + 3) / 4);
+        return by_bool(wide, [&](auto w) {
+            switch (dtype) {
+            case kF32: k_embed_few<kF32, w><<<g, 256, 0, s>>>(a); break;
+            case kBF16: k_embed_few<kBF16, w><<<g, 256, 0, s>>>(a); break;
+            default: k_embed_few<kF16, w><<<g, 256, 0, s>>>(a); break;
+            }
+            return hipGetLastError();
+        });
+    }
     a.zl = log2_up(((uint64_t)a.cols + 3) / 4, 2, 10);
     const uint32_t groups = (a.vocab + a.w - 1) / a.w, lds = (kSortWaves + 1) * a.w * 4;
     if (wide)
@@ -372,7 +446,6 @@ hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wi
     else
         k_embed_sort<false><<<groups, 64 * kSortWaves, lds, s>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (!a.nchunk) return hipSuccess;
     const uint32_t sums = (uint32_t)p.sumwgs;
     switch (dtype) {
     case kF32: k_embed_sum<kF32><<<sums, 256, 0, s>>>(a); break;
@@ -380,7 +453,6 @@ hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wi
     default: k_embed_sum<kF16><<<sums, 256, 0, s>>>(a); break;
     }
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (a.nchunk < 2) return hipSuccess;
     k_embed_join<<<(uint32_t)((uint64_t)a.nchunk * a.njoin), 256, 0, s>>>(a);
     return hipGetLastError();
 }

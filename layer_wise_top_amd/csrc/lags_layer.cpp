@@ -281,7 +281,8 @@ int lags_embed_grad(int64_t tokens, int64_t vocab, int64_t cols, const void *ids
     Region r[4];
     if (int rc = matrix(dy, tokens, cols, lddy, dtype, r[0]); rc != LAGS_OK) return rc;
     const EmbedPlan p = embed_plan(dtype, tokens, vocab, cols);
-    // threads of one launch
+    // threads of one launch; few tokens' is 16 a vector of the gradient's rows of 256 bytes or more
+    if (p.few && (u128)vocab * (cols / 256 + 1) * 16 > kMostThreads) return LAGS_ERANGE;
     if ((u128)p.sumwgs * 256 > kMostThreads || (u128)p.nchunk * p.njoin * 256 > kMostThreads)
         return LAGS_ERANGE;
     const EmbedSpace w = embed_space(tokens, vocab, cols);
@@ -382,10 +383,13 @@ int lags_linear_backward(const lags_linear *lin, const void *dy, int64_t lddy, c
     a.M = M, a.act = lin->act;
     if (M && (act || dbias)) {
         a.N = (uint32_t)N, a.dy = dy, a.lddy = lddy, a.zin = z, a.ldz = ldz, a.dz = dz, a.lddz = lddz;
-        a.part = dbias ? (float *)ws : nullptr;
+        if (c.dz.chunks == 1)
+            a.dbias = dbias, a.add = add;
+        else
+            a.part = dbias ? (float *)ws : nullptr;
         if (int rc = hip(launch_slopes(c.dz, a, lin->dtype, s)); rc != LAGS_OK) return rc;
     }
-    if (dbias)
+    if (dbias && (!M || c.dz.chunks > 1))
         if (int rc = hip(launch_dbias((const float *)ws, M ? c.dz.chunks : 0, (uint32_t)N, dbias, add, s)); rc != LAGS_OK)
             return rc;
     if (!M || !dx) return LAGS_OK;

@@ -52,7 +52,9 @@ struct EmbedArgs {
     uint32_t chunk, nchunk, tl, nslab;       // tokens a chunk, chunks, 2^tl lanes a slab, slabs a row
     uint32_t zl, njoin;                      // 2^zl lanes a row of zeros; 256-channel parts
 };
+constexpr int kFew = 256;                    // tokens of a gradient in one launch, at most
 struct EmbedPlan {
+    bool few;
     uint32_t w, chunk, nchunk, tl, nslab, njoin;
     uint64_t sumwgs;
 };
@@ -81,6 +83,8 @@ struct LinArgs {
     void *dz;
     int64_t lddy, lddz, rows_per;
     uint32_t tl, nslab;
+    float *dbias;                            // one chunk of rows: written, or added to, at once
+    uint32_t add;
 };
 // Tiles of the product (rows, columns) and their waves.
 struct LinTile {

@@ -576,7 +576,7 @@ template <int D> __global__ __launch_bounds__(256) void k_linear_dz(LinArgs a)
         with(std::integral_constant<int, kActGelu>());
     else
         with(std::integral_constant<int, kActNone>());
-    if (!a.part) return;
+    if (!a.part && !a.dbias) return;
     for (int j = 0; j < V; ++j) {
         float v = sum[j];
         if (a.tl < 1) v += lane_xor<1>(v);
@@ -590,9 +590,13 @@ template <int D> __global__ __launch_bounds__(256) void k_linear_dz(LinArgs a)
     __syncthreads();
     if (threadIdx.x < T && nv > 0)
         for (int j = 0; j < V; ++j)
-            if (j < nv)
-                a.part[(size_t)chunk * a.N + n + j] =
-                    (sh[0][j][col] + sh[1][j][col]) + (sh[2][j][col] + sh[3][j][col]);
+            if (j < nv) {
+                const float v = (sh[0][j][col] + sh[1][j][col]) + (sh[2][j][col] + sh[3][j][col]);
+                if (a.dbias)
+                    a.dbias[n + j] = a.add ? a.dbias[n + j] + v : v;
+                else
+                    a.part[(size_t)chunk * a.N + n + j] = v;
+            }
 }
 
 // W [N][K] (a.b, a.ldb) turned round: out [K][N].  A workgroup turns 64 x 64

@@ -298,14 +298,22 @@ __global__ __launch_bounds__(MOST ? MOST : 256) void k_ln_backward(LnArgs a)
         }
     }
     if (!a.part) return;
+    // a workgroup's sums go to its place, or, where it is the only one, to the gradients
     float *out = a.part + (size_t)blockIdx.x * 2 * a.C;
+    auto put = [&](int which, uint32_t c, float v) {
+        if (gridDim.x > 1) {
+            out[which * a.C + c] = v;
+        } else if (float *g = which ? a.dgamma : a.dbeta) {
+            g[c] = a.add ? g[c] + v : v;
+        }
+    };
     if constexpr (WIDE) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             for (int j = 0; j < V; ++j)
                 if (j < row.nv[k]) {
-                    out[row.chan(k) + j] = db[k][j];
-                    out[a.C + row.chan(k) + j] = dg[k][j];
+                    put(0, row.chan(k) + j, db[k][j]);
+                    put(1, row.chan(k) + j, dg[k][j]);
                 }
     } else {
         // the rows side by side in a wave, then the four waves
@@ -323,7 +331,7 @@ __global__ __launch_bounds__(MOST ? MOST : 256) void k_ln_backward(LnArgs a)
             __syncthreads();
             for (uint32_t c = threadIdx.x; c < a.C; c += 256) {
                 const uint32_t v = c / V, l = v & (row.T - 1), i = (v >> a.tl) * V + c % V;
-                out[which * a.C + c] = (join[0][i][l] + join[1][i][l]) + (join[2][i][l] + join[3][i][l]);
+                put(which, c, (join[0][i][l] + join[1][i][l]) + (join[2][i][l] + join[3][i][l]));
             }
             __syncthreads();
         }
@@ -401,7 +409,9 @@ LnPlan ln_plan(int dtype, bool backward, int edge, int64_t rows, uint32_t C)
     int64_t groups = 512;
     if (backward && p.threads >= 256 && p.nv == 2 * most) groups = 256;
     if (wide) groups = p.threads == 128 ? 1024 : backward || p.threads > 256 ? 256 : 512;
-    p.groups = (uint32_t)std::max<int64_t>(1, std::min(groups, (rows + per - 1) / per));
+    const int64_t want = (rows + per - 1) / per;
+    // backward: a single workgroup of up to four rounds needs no second launch for its sums
+    p.groups = (uint32_t)(backward && want <= 4 ? 1 : std::max<int64_t>(1, std::min(groups, want)));
     return p;
 }
 
@@ -422,7 +432,7 @@ hipError_t launch_ln_backward(const LnPlan &p, LnArgs a, int dtype, int edge, hi
                                               : backward<kF16>(p, a, edge, s);
         if (e != hipSuccess) return e;
     }
-    if (!a.part) return hipSuccess;
+    if (!a.part || (a.rows && p.groups == 1)) return hipSuccess;
     return launch_params(a.part, a.rows ? p.groups : 0, a.C, a.dgamma, a.dbeta, a.add, s);
 }
 

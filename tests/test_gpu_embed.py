@@ -51,8 +51,9 @@ def _grad(ids, dy, vocab, scale=1.0, dtable=None, add=False):
 
 
 def _check_grad(tag, got, ids, dy, vocab, scale):
-    """A row's sum: at most 16 additions in a chunk (of 8 tokens or more), then chains of a quarter of
-    its chunks and three more; the scale is one product."""
+    """A row's sum: its tokens one after the other up to 256 in all; else at most 16 additions in a
+    chunk (of 8 tokens or more), then chains of a quarter of its chunks and three more; the scale is
+    one product."""
     d, a = dy.double().cpu().numpy(), np.asarray(ids)
     ok = (a >= 0) & (a < vocab)
     want, mag, n = (np.zeros((vocab, d.shape[1])) for _ in range(3))
@@ -60,7 +61,8 @@ def _check_grad(tag, got, ids, dy, vocab, scale):
     np.add.at(mag, a[ok], np.abs(d[ok]))
     np.add.at(n, a[ok], 1)
     s32 = float(np.float32(scale))
-    bound = (16 + n / 32 + 8) * R.U * mag * abs(s32)
+    chain = n + 2 if d.shape[0] <= 256 else 16 + n / 32 + 8
+    bound = chain * R.U * mag * abs(s32)
     R.check(tag, got.double().cpu().numpy(), want * s32, bound)
 
 

@@ -168,7 +168,12 @@ def test_slices_pitches_and_places(m, c, dtype):
         assert torch.equal(yv, y) and torch.equal(got[3], s) and torch.equal(got[1], mean)
         assert torch.isnan(wy[:, :off]).all() and torch.isnan(wy[:, off + c:]).all()
         _, g2, b2 = _backward(dyv, gamma, mean, rstd, x=sv, dsum=dsv, dx=dyv)
-        assert torch.equal(dyv, dx) and torch.equal(g2, dg) and torch.equal(b2, db)
+        assert torch.equal(dyv, dx)
+        # rows that start inside a word are dealt to the workgroups otherwise: another order of the sums,
+        # each off by at most a rounding a row
+        xh = (s.double() - mean.double()[:, None]) * rstd.double()[:, None]
+        for got, want, mag in ((g2, dg, (dy.double() * xh).abs().sum(0)), (b2, db, dy.double().abs().sum(0))):
+            assert ((got.double() - want.double()).abs() <= 2 * (m + 4) * R.U * mag).all()
         assert torch.isnan(wd[:, :off]).all() and torch.isnan(wd[:, off + c:]).all()
     xi, ri = x.clone(), res.clone()
     _forward(xi, gamma, beta, ri, y=xi, sum_=ri)
