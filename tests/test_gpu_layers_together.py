@@ -1,0 +1,238 @@
+"""Embedding, layer norms and linear layers as a training step runs them: a block with a residual
+stream whose output layer shares the embedding's table, its gradient in one flat buffer, from 8-bit
+checkpoints, and the sparsification of that buffer; eager, in a replayed graph, and against float64."""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": "float32", "bf16": "bfloat16", "f16": "float16"}
+SCALE = 3.0
+
+
+class Block:
+    """ids -> x0 = SCALE table[ids] -> y1 = ln(x0) -> a = gelu(y1 w1^T + c1) -> s = x0 + (a w2^T + c2)
+    -> y2 = ln(s) -> y2 table^T.  Parameters and gradient lie in one flat fp32 buffer each; the first
+    layer has three values, so that most slices start at odd places."""
+
+    def __init__(self, tokens, vocab, cols, hidden, dtype, seed):
+        import torch
+        from layer_wise_top_amd import lags
+        self.m, self.v, self.c, self.h, self.dtype = tokens, vocab, cols, hidden, dtype
+        self.shapes = {"lead": (3,), "table": (vocab, cols), "g1": (cols,), "b1": (cols,), "w1": (hidden, cols),
+                       "c1": (hidden,), "w2": (cols, hidden), "c2": (cols,), "g2": (cols,), "b2": (cols,)}
+        rng = np.random.default_rng(seed)
+        off = [0]
+        for sh in self.shapes.values():
+            off.append(off[-1] + math.prod(sh))
+        self.at = {name: (off[i], off[i + 1]) for i, name in enumerate(self.shapes)}
+        flat = np.zeros(off[-1], np.float32)
+        for name, sh in self.shapes.items():
+            lo, hi = self.at[name]
+            r = rng.standard_normal(hi - lo)
+            flat[lo:hi] = r / np.sqrt(sh[-1]) if len(sh) == 2 else (1 + 0.3 * r if name[0] == "g" else 0.3 * r)
+        self.flat = torch.from_numpy(flat).cuda()
+        self.grad = torch.full((off[-1],), float("nan"), device="cuda")
+        self.grad[:3] = 1
+        off = np.array(off, np.uint64)
+        self.layout = lags.Layout(off, lags.k_table(off, 1, 20))
+        self.residual = torch.zeros(self.layout.n, device="cuda")
+        self.idx = torch.zeros(self.layout.K, dtype=torch.int32, device="cuda")
+        self.val = torch.zeros(self.layout.K, device="cuda")
+        self.sws = lags.workspace(self.layout)
+
+        new = lambda r, c: torch.full((r, c), 7, dtype=dtype, device="cuda")
+        vec = lambda n: torch.full((n,), 7., device="cuda")
+        m, c, h, v = tokens, cols, hidden, vocab
+        ids = rng.integers(0, vocab, tokens)
+        ids[4::5] = -1                          # padding
+        ids[1::7] = ids[tokens // 2]            # one id many times
+        self.ids = torch.from_numpy(ids).cuda()
+        self.dout = torch.from_numpy(rng.standard_normal((m, v)) / 8 * (ids >= 0)[:, None]).to(dtype).cuda()
+        self.ln = lags.LayerNorm(m, c, dtype=dtype)
+        self.up = lags.Linear(m, c, h, dtype=dtype, act="gelu")
+        self.down = lags.Linear(m, h, c, dtype=dtype)
+        self.head = lags.Linear(m, c, v, dtype=dtype)
+        self.ws = {"ln": lags.ln_workspace(self.ln), "up": lags.linear_workspace(self.up),
+                   "down": lags.linear_workspace(self.down), "head": lags.linear_workspace(self.head),
+                   "embed": lags.embed_workspace(m, v, c), "w1": lags.wgrad_workspace(m, h, c, dtype),
+                   "w2": lags.wgrad_workspace(m, c, h, dtype), "table": lags.wgrad_workspace(m, v, c, dtype)}
+        self.x0, self.y1, self.u, self.s, self.y2, self.out = new(m, c), new(m, c), new(m, c), new(m, c), new(m, c), new(m, v)
+        self.z, self.a, self.da, self.dz = (new(m, h) for _ in range(4))
+        self.dy2, self.ds, self.dy1, self.dx0 = (new(m, c) for _ in range(4))
+        self.st = [vec(m) for _ in range(4)]
+        self.ck = {"y1": lags.checkpoint(m, c), "a": lags.checkpoint(m, h), "s": lags.checkpoint(m, c),
+                   "y2": lags.checkpoint(m, c)}
+
+    def par(self, name, flat=None):
+        lo, hi = self.at[name]
+        t = self.flat if flat is None else flat
+        return t[lo:hi].view(self.shapes[name])
+
+    def step(self):
+        from layer_wise_top_amd import lags
+        p, w, ck = self.par, self.ws, self.ck
+        g = lambda name: p(name, self.grad)
+        low = lambda name: p(name).to(self.dtype)
+        m1, r1, m2, r2 = self.st
+        table, w1, w2 = low("table"), low("w1"), low("w2")
+        lags.lags_embed_forward(self.ids, p("table"), self.x0, SCALE)
+        lags.lags_ln_forward(self.ln, self.x0, p("g1"), p("b1"), self.y1, m1, r1, yckpt=ck["y1"])
+        lags.lags_linear_forward(self.up, self.y1, w1, self.a, w["up"], bias=p("c1"), z=self.z)
+        lags.lags_ckpt_pack(self.a, ck["a"])
+        lags.lags_linear_forward(self.down, self.a, w2, self.u, w["down"], bias=p("c2"))
+        lags.lags_ln_forward(self.ln, self.u, p("g2"), p("b2"), self.y2, m2, r2, res=self.x0, sum=self.s,
+                             ckpt=ck["s"], yckpt=ck["y2"])
+        lags.lags_linear_forward(self.head, self.y2, table, self.out, w["head"])
+
+        lags.lags_linear_backward(self.head, self.dout, table, self.dy2, w["head"])
+        lags.lags_ckpt_wgrad(self.dout, ck["y2"], g("table"), w["table"])
+        lags.lags_ln_backward(self.ln, self.dy2, p("g2"), m2, r2, self.ds, g("g2"), g("b2"), w["ln"], ckpt=ck["s"])
+        lags.lags_linear_backward(self.down, self.ds, w2, self.da, w["down"], dbias=g("c2"))
+        lags.lags_ckpt_wgrad(self.ds, ck["a"], g("w2"), w["w2"])
+        lags.lags_linear_backward(self.up, self.da, w1, self.dy1, w["up"], z=self.z, dz=self.dz, dbias=g("c1"))
+        lags.lags_ckpt_wgrad(self.dz, ck["y1"], g("w1"), w["w1"])
+        lags.lags_ln_backward(self.ln, self.dy1, p("g1"), m1, r1, self.dx0, g("g1"), g("b1"), w["ln"], x=self.x0,
+                              dsum=self.ds)
+        lags.lags_embed_grad(self.ids, self.dx0, g("table"), w["embed"], SCALE, add=True)
+        self.residual.zero_()
+        lags.lags_sparsify_layers(self.layout, self.grad, self.residual, self.idx, self.val, self.sws)
+
+    def results(self):
+        import torch
+        torch.cuda.synchronize()
+        return [t.clone() for t in (self.out, self.grad, self.residual, self.idx, self.val)]
+
+
+def _gelu(z):
+    g = 2 * np.sqrt(2 / np.pi)
+    s = 1 / (1 + np.exp(-g * (z + 0.044715 * z ** 3)))
+    return z * s, s + z * s * (1 - s) * g * (1 + 0.134145 * z ** 2)
+
+
+def _ln(x, g, b):
+    mean = x.mean(axis=1, keepdims=True)
+    rstd = 1 / np.sqrt(((x - mean) ** 2).mean(axis=1, keepdims=True) + 1e-5)
+    return (x - mean) * rstd * g + b, mean, rstd
+
+
+def _ln_back(dy, x, mean, rstd, g):
+    xh = (x - mean) * rstd
+    t = dy * g
+    dx = rstd * (t - t.mean(axis=1, keepdims=True) - xh * (t * xh).mean(axis=1, keepdims=True))
+    return dx, (dy * xh).sum(axis=0), dy.sum(axis=0)
+
+
+def _reference(b, held):
+    """The step in float64, from the block's weights in its dtype; held: the checkpointed tensors that
+    the gradient is taken from, or None for the values themselves."""
+    low = lambda n: b.par(n).to(b.dtype).double().cpu().numpy()
+    full = lambda n: b.par(n).double().cpu().numpy()
+    ids = b.ids.cpu().numpy()
+    table, w1, w2 = low("table"), low("w1"), low("w2")
+    x0 = np.where((ids >= 0)[:, None], SCALE * full("table")[np.maximum(ids, 0)], 0)
+    y1, m1, r1 = _ln(x0, full("g1"), full("b1"))
+    a, da_dz = _gelu(y1 @ w1.T + full("c1"))
+    s = x0 + a @ w2.T + full("c2")
+    y2, m2, r2 = _ln(s, full("g2"), full("b2"))
+    h = held or {"y1": y1, "a": a, "s": s, "y2": y2}
+    out = {}
+    dout = b.dout.double().cpu().numpy()
+    out["table"] = dout.T @ h["y2"]
+    ds, out["g2"], out["b2"] = _ln_back(dout @ table, h["s"], m2, r2, full("g2"))
+    out["c2"], out["w2"] = ds.sum(axis=0), ds.T @ h["a"]
+    dz = (ds @ w2) * da_dz
+    out["c1"], out["w1"] = dz.sum(axis=0), dz.T @ h["y1"]
+    dx0, out["g1"], out["b1"] = _ln_back(dz @ w1, x0, m1, r1, full("g1"))
+    dx0 += ds
+    np.add.at(out["table"], ids[ids >= 0], SCALE * dx0[ids >= 0])
+    return y2 @ table.T, out, {"y1": y1, "a": a, "s": s, "y2": y2}
+
+
+def _off(got, want):
+    return np.linalg.norm(got - want) / max(np.linalg.norm(want), 1e-30)
+
+
+@pytest.mark.parametrize("sizes", [(1, 7, 33, 64), (216, 331, 72, 150), (1300, 1001, 129, 516)], ids=str)
+@pytest.mark.parametrize("dtype", sorted(DT))
+def test_step(sizes, dtype):
+    """A tensor's values are off by at most half a step each, independently, so a product with a random
+    matrix and a normalisation carry that share of its norm on and enlarge it by little: no result has
+    more than 13 stored tensors before it, and 2 of them allow for the enlargement.  fp32 sums of up to
+    1300 terms add 1300 / 2 steps in the worst order.  Sums over tokens that cancel (a row's or a bias's)
+    are relative to the whole gradient of their layer, and one token's few terms to a wider share."""
+    import torch
+    from layer_wise_top_amd import lags
+    print("step", sizes, dtype, flush=True)
+    b = Block(*sizes, getattr(torch, DT[dtype]), 3)
+    b.step()
+    first = b.results()
+    held = {}
+    for name, ck in b.ck.items():
+        t = torch.empty(sizes[0], sizes[3] if name == "a" else sizes[2], device="cuda")
+        lags.lags_ckpt_unpack(ck, t)
+        held[name] = t.double().cpu().numpy()
+    tol = 26 * torch.finfo(b.dtype).eps / 2 + 1300 * 2.0 ** -24
+    out, want, true = _reference(b, held)
+    assert _off(first[0].double().cpu().numpy(), out) < tol
+    for name, t in true.items():                # a run of 32 in 8 bits: half a step of 1/64 at most
+        assert _off(held[name], t) < 2.0 ** -6 + tol, name
+    _, exact, _ = _reference(b, None)
+    for name, w in want.items():
+        got = b.par(name, first[1]).double().cpu().numpy()
+        err, far = _off(got, w), _off(got, exact[name])
+        print(name, "off by", err, "and from the gradient without checkpoints by", far, flush=True)
+        assert err < tol, name
+        assert far < 2.0 ** -5 + tol, name
+    assert torch.equal(first[1][:3], torch.ones(3, device="cuda"))
+
+    # the message holds the gradient's entries, the residual the rest
+    sent = torch.zeros_like(b.grad)
+    sent[first[3].long()] = first[4]
+    assert torch.equal(sent + first[2], first[1]) and int((sent != 0).sum()) <= b.layout.K
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b.step()
+    torch.cuda.current_stream().wait_stream(side)
+    for x, y in zip(b.results(), first):
+        assert torch.equal(x, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.step()
+    for i in range(3):
+        b.grad[3:].fill_(float("nan"))
+        b.out.fill_(7), b.val.zero_()
+        graph.replay()
+        for x, y in zip(b.results(), first):
+            assert torch.equal(x, y), i
+        b.step()
+        torch.cuda.synchronize()
+
+
+def test_differences():
+    """The gradient against central differences of the fp32 step's loss sum(out * dout) along random
+    directions: the loss is read with an error near 2^-24 of its terms' norm times a few, the step of
+    2^-6 of a parameter's norm leaves a share of 2^-10 of the third derivative, and the checkpoints' share
+    is 2^-6 of the gradient's norm at most (halves of steps at random, far less along one direction)."""
+    import torch
+    b = Block(96, 101, 64, 128, torch.float32, 11)
+    b.step()
+    grad = b.results()[1]
+    rng = np.random.default_rng(2)
+    for name in ("table", "g1", "b1", "w1", "c1", "w2", "c2", "g2", "b2"):
+        g, p = b.par(name, grad), b.par(name)
+        d = torch.from_numpy(rng.standard_normal(g.shape)).float().cuda() + g * (g.numel() ** 0.5 / g.norm())
+        d *= 2.0 ** -6 * p.norm() / d.norm()
+        keep, loss = p.clone(), []
+        for sign in (1, -1):
+            p.copy_(keep + sign * d)
+            b.step()
+            torch.cuda.synchronize()
+            loss.append((b.out.double() * b.dout.double()).sum())
+        p.copy_(keep)
+        got, want = float((g.double() * d.double()).sum()), float((loss[0] - loss[1]) / 2)
+        print(name, got, want, flush=True)
+        assert abs(got - want) < 2.0 ** -5 * float(g.norm() * d.norm()), name
