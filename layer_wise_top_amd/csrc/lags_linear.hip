@@ -33,34 +33,40 @@ __global__ __launch_bounds__(64 * kBiasWaves) void k_linear_dbias(const float *p
 namespace {
 // Microseconds that a tile takes a step of 128 bytes of k on a compute unit that is full of them
 // (`alone`: when it is the only one on an idle card), and for its results, and how many a compute unit
-// holds; 16-bit values and fp32, whose steps are half as long.  Measured with 512 x 512 to 8192 x 4096 outputs over 2048 to 8192 of k; the backward product
-// takes 1.17 times as long, but as long with 32 x 128.
+// holds: 16-bit values, the same with W as it comes (backward), and fp32, whose steps are half as long.
+// Fitted to 620 products of 16 to 16384 rows and 64 to 8192 columns and outputs, each in every tile and up to 27
+// slices: the plan's time is 1.015, 1.03 and 1.016 of the best measured one, geometric mean.  Up to 64 rows of 16
+// bits take W from memory, not from a cache that others' reads have filled, and `alone` is 2 (backward 1.5)
+// times that: over 107 products of 1 to 64 rows with W not in any cache 1.05 and 1.07 of the best, without it 1.15 and
+// 1.10.
 struct Cost {
     float full, alone, out;
     int held;
 };
-constexpr Cost kCost[2][4] = {
-    {{1.75f, 1.25f, 4.0f, 1}, {0.52f, 0.60f, 1.0f, 2}, {0.198f, 0.47f, 0.3f, 5}, {0.23f, 0.47f, 0.3f, 4}},
-    {{7.7f, 7.5f, 4.0f, 1}, {2.0f, 2.05f, 1.0f, 2}, {0.53f, 0.68f, 0.3f, 5}, {0.54f, 0.70f, 0.3f, 4}}};
+constexpr Cost kCost[3][4] = {
+    {{1.60f, 0.94f, 3.4f, 1}, {0.46f, 0.67f, 1.2f, 2}, {0.246f, 0.342f, 0.31f, 4}, {0.56f, 0.37f, 0.25f, 3}},
+    {{2.00f, 0.95f, 3.5f, 1}, {0.54f, 0.92f, 1.2f, 2}, {0.232f, 0.593f, 0.26f, 5}, {0.23f, 0.60f, 0.29f, 4}},
+    {{7.7f, 7.2f, 10.9f, 1}, {1.98f, 2.15f, 2.0f, 2}, {0.556f, 0.736f, 0.20f, 4}, {0.577f, 0.727f, 0.34f, 3}}};
 }  // namespace
 
 // The tile and the slices of k with the least time by a model of it (`least`): the rounds of workgroups on 256
 // compute units, or the bytes of the operands; then the slices' sums, written and read again.
-//   700 x 6000 x 1500 fp32   127 us (64 x 64, 8 slices; 128 x 128 in 6: 138), the library's product 132
-//   1 x 2048 x 8192 bf16     9.9 us (64 x 64, 4 slices; whole 12)
+//   700 x 6000 x 1500 fp32   116 us (128 x 128, 7 slices; 64 x 64 in 6: 121, whole 193), the library's product 132
+//   1 x 2048 x 8192 bf16     11.1 us (64 x 64, 3 slices; whole 15)
 static LinPlan plan_of(int dtype, bool backward, int64_t M, int64_t N, int64_t K, double &least)
 {
     const int64_t e = elem_bytes(dtype), ks = 128 / e, steps = (K + ks - 1) / ks;
-    const double in = (double)(M * K + N * K) * e / 4.5e6, sums = (double)M * N * 4 / 4.5e6;
+    const double in = (double)(M * K + N * K) * e / 5e6, sums = (double)M * N * 4 / 5e6;
+    const double far = dtype == kF32 || M > 64 ? 1 : backward ? 1.5 : 2;
     LinPlan best = {};
     least = 0;
     for (uint32_t t = 0; t < 4; ++t) {
-        const Cost &c = kCost[dtype == kF32][t];
+        const Cost &c = kCost[dtype == kF32 ? 2 : backward][t];
         LinPlan p = {};
         p.tile = t;
         p.tm = (uint32_t)((M + kLinTiles[t].bm - 1) / kLinTiles[t].bm);
         p.tn = (uint32_t)((N + kLinTiles[t].bn - 1) / kLinTiles[t].bn);
-        const double tiles = (double)p.tm * p.tn, slow = backward && dtype != kF32 && t != 3 ? 1.17 : 1;
+        const double tiles = (double)p.tm * p.tn;
         int64_t last = 0;
         for (int64_t want = 1; want <= 32 && want <= steps; want += want < 4 ? 1 : want / 4) {
             const int64_t per = (steps + want - 1) / want;
@@ -71,10 +77,11 @@ static LinPlan plan_of(int dtype, bool backward, int64_t M, int64_t N, int64_t K
             // whole rounds of all the card holds, and the rest; a card that is part idle runs faster
             const double units = tiles * p.split / 256, whole = std::floor(units / c.held) * c.held;
             const double rest = units - whole, some = rest > 1 ? 1 : rest * rest;
-            const double step = whole * c.full + (rest ? std::fmax(std::ceil(rest) * c.full, c.alone) * some +
-                                                             c.alone * (1 - some) : 0);
-            double us = std::fmax(per * slow * step, in) + std::ceil(units) * c.out;
-            if (p.split > 1) us += 4.5 + 0.2 * p.split + sums * (p.split + 1);     // another launch, loads in turn
+            const double alone = c.alone * far;
+            const double step = whole * c.full + (rest ? std::fmax(std::ceil(rest) * c.full, alone) * some +
+                                                             alone * (1 - some) : 0);
+            double us = std::fmax(per * step, in) + std::ceil(units) * c.out;
+            if (p.split > 1) us += 4.5 + 0.22 * p.split + sums * (p.split + 1);     // another launch, loads in turn
             if (!least || us < least) least = us, best = p;
         }
     }

@@ -11,19 +11,19 @@ TILES = ((256, 256), (128, 128), (64, 64), (32, 128))
 # (rows, cols, outs) whose product, forward or backward, is made of ragged tiles of each kind, whole and in
 # slices; of 16-bit values and of fp32.  Keys: backward, tile, sliced, W turned round.
 SHAPES = {
-    "f32": {(0, 0, 0, 0): (3022, 19, 4742), (0, 0, 1, 0): (1681, 2239, 1164), (0, 1, 0, 0): (6353, 16, 454),
-            (0, 1, 1, 0): (1160, 837, 865), (0, 2, 0, 0): (1, 16, 66), (0, 2, 1, 0): (2, 322, 66),
-            (0, 3, 0, 0): (67, 17, 8685), (0, 3, 1, 0): (201, 394, 605), (1, 0, 0, 0): (1688, 8479, 8),
-            (1, 0, 1, 0): (2858, 731, 2240), (1, 1, 0, 0): (7059, 386, 11), (1, 1, 1, 0): (4366, 72, 877),
-            (1, 2, 0, 0): (1, 65, 8), (1, 2, 1, 0): (1, 65, 328), (1, 3, 0, 0): (66, 8393, 11),
-            (1, 3, 1, 0): (643, 207, 355)},
-    "bf16": {(0, 0, 0, 0): (8311, 19, 1410), (0, 0, 1, 0): (1538, 6546, 1219), (0, 1, 0, 0): (6353, 16, 456),
-             (0, 1, 1, 0): (1194, 1800, 530), (0, 2, 0, 0): (1, 16, 66), (0, 2, 1, 0): (2, 907, 67),
-             (0, 3, 0, 0): (67, 17, 8685), (0, 3, 1, 0): (195, 1035, 688), (1, 0, 0, 0): (5439, 2177, 8),
-             (1, 0, 0, 1): (8390, 910, 1976), (1, 0, 1, 0): (1701, 1158, 5326), (1, 0, 1, 1): (8365, 387, 5496),
-             (1, 1, 0, 0): (7059, 386, 11), (1, 1, 0, 1): (8351, 602, 2128), (1, 1, 1, 0): (1474, 461, 1896),
-             (1, 1, 1, 1): (6197, 273, 7536), (1, 2, 0, 0): (8202, 17, 8), (1, 2, 0, 1): (6630, 583, 2600),
-             (1, 2, 1, 0): (679, 129, 1288), (1, 3, 0, 0): (33, 16, 8), (1, 3, 1, 0): (34, 17, 927)},
+    "f32": {(0, 0, 0, 0): (7187, 340, 1991), (0, 0, 1, 0): (1367, 2886, 1483), (0, 1, 0, 0): (1700, 514, 1862),
+            (0, 1, 1, 0): (716, 1564, 1470), (0, 2, 0, 0): (1, 16, 66), (0, 2, 1, 0): (1, 295, 68),
+            (0, 3, 0, 0): (67, 17, 8685), (0, 3, 1, 0): (137, 413, 778), (1, 0, 0, 0): (3600, 4032, 359),
+            (1, 0, 1, 0): (1228, 2438, 1896), (1, 1, 0, 0): (1968, 1546, 528), (1, 1, 1, 0): (1713, 592, 1561),
+            (1, 2, 0, 0): (1, 65, 8), (1, 2, 1, 0): (1, 66, 304), (1, 3, 0, 0): (66, 8393, 11),
+            (1, 3, 1, 0): (129, 778, 414)},
+    "bf16": {(0, 0, 0, 0): (8196, 16, 963), (0, 0, 1, 0): (2692, 3279, 920), (0, 1, 0, 0): (321, 26, 8299),
+             (0, 1, 1, 0): (579, 2889, 797), (0, 2, 0, 0): (1, 70, 65), (0, 2, 1, 0): (1, 700, 65),
+             (0, 3, 0, 0): (33, 16, 8), (0, 3, 1, 0): (2, 643, 2744), (1, 0, 0, 0): (1036, 8701, 8),
+             (1, 0, 0, 1): (8719, 1607, 1192), (1, 0, 1, 0): (3207, 432, 4151), (1, 0, 1, 1): (7553, 300, 5232),
+             (1, 1, 0, 0): (6582, 929, 9), (1, 1, 0, 1): (5680, 519, 1376), (1, 1, 1, 0): (581, 1720, 2233),
+             (1, 1, 1, 1): (8351, 277, 5096), (1, 2, 0, 0): (1, 65, 8), (1, 2, 0, 1): (1825, 323, 1288),
+             (1, 2, 1, 0): (1, 65, 520), (1, 3, 0, 0): (66, 8393, 11), (1, 3, 1, 0): (792, 202, 919)},
 }
 SHAPES["f16"] = SHAPES["bf16"]
 CASES = [(dtype, key, shape) for dtype, t in SHAPES.items() for key, shape in t.items()]
