@@ -101,6 +101,44 @@ def test_gradient(tokens, vocab, cols, kind, dtype):
     _check_grad(f"{tokens} {vocab} {cols} {kind} {dtype}", got, a, dy, vocab, scale)
 
 
+@pytest.mark.parametrize("kind", ["one", "text", "holes"])
+@pytest.mark.parametrize("tokens", [63, 64, 128, 192, 193, 255, 256, 257])
+def test_where_one_launch_ends(tokens, kind):
+    """Up to 256 tokens and above, written and added at an odd place, all columns of a vector used and not."""
+    import torch
+    rng = np.random.default_rng(tokens)
+    for dtype, vocab, cols in (("bf16", 41, 520), ("f32", 300, 261)):
+        a = _draw(rng, tokens, vocab, kind)
+        dy = _dev(rng.standard_normal((tokens, cols)), dtype)
+        flat = torch.full((vocab * cols + 7,), 0.5, device="cuda")
+        at = flat[3:3 + vocab * cols].view(vocab, cols)
+        _check_grad(f"{tokens} {kind} {dtype}", _grad(_ids(a, True), dy, vocab, 1.5, at), a, dy, vocab, 1.5)
+        once = at.clone()
+        _grad(_ids(a, False), dy, vocab, 1.5, at, add=True)
+        assert torch.equal(at, 2 * once)
+        assert (flat[:3] == 0.5).all() and (flat[3 + vocab * cols:] == 0.5).all()
+
+
+@pytest.mark.parametrize("tokens", [40, 400])
+def test_ids_whose_low_half_is_in_the_table(tokens):
+    """64-bit ids outside the table, in each 32-bit half."""
+    import torch
+    from layer_wise_top_amd import lags
+    rng = np.random.default_rng(1)
+    vocab, cols = 30, 24
+    a = rng.integers(0, vocab, tokens)
+    far = a.copy()
+    far[::3] = np.resize([2 ** 32 + 3, -2 ** 32 + 3, 2 ** 63 - 1, -2 ** 63, 2 ** 32, 2 ** 40 + 7], len(far[::3]))
+    a[::3] = -1
+    dy, w = _dev(rng.standard_normal((tokens, cols)), "bf16"), _dev(rng.standard_normal((vocab, cols)), "f32")
+    y = torch.full((tokens, cols), 7, dtype=dy.dtype, device="cuda")
+    want = torch.full_like(y, 7)
+    lags.lags_embed_forward(_ids(far, True), w, y)
+    lags.lags_embed_forward(_ids(a, True), w, want)
+    assert torch.equal(y, want) and (y[::3] == 0).all()
+    assert torch.equal(_grad(_ids(far, True), dy, vocab), _grad(_ids(a, True), dy, vocab))
+
+
 @pytest.mark.parametrize("vocab", [511, 512, 131072, 131073, 300000])
 def test_large_vocabularies(vocab):
     """From one id a workgroup of the sort to its 512 at most, and a last group of any size."""

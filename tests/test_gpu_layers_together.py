@@ -236,3 +236,23 @@ def test_differences():
         got, want = float((g.double() * d.double()).sum()), float((loss[0] - loss[1]) / 2)
         print(name, got, want, flush=True)
         assert abs(got - want) < 2.0 ** -5 * float(g.norm() * d.norm()), name
+
+
+def test_two_streams_at_once():
+    """Two blocks, each with its own buffers, on two streams: what each gives alone."""
+    import torch
+    blocks = [Block(700, 501, 136, 264, torch.bfloat16, 5), Block(190, 77, 65, 130, torch.float32, 6)]
+    alone = []
+    for b in blocks:
+        b.step()
+        alone.append(b.results())
+    streams = [torch.cuda.Stream() for _ in blocks]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i in range(5):
+        for b, s in zip(blocks, streams):
+            with torch.cuda.stream(s):
+                b.step()
+    for b, want in zip(blocks, alone):
+        for x, y in zip(b.results(), want):
+            assert torch.equal(x, y)

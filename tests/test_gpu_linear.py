@@ -200,7 +200,8 @@ def test_epilogues(act, has_res, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(DT))
-@pytest.mark.parametrize("m,k,n", [(37, 70, 45), (300, 136, 264), (70, 64, 129), (25, 3000, 40), (1100, 200, 1064)])
+@pytest.mark.parametrize("m,k,n", [(37, 70, 45), (300, 136, 264), (70, 64, 129), (25, 3000, 40), (1100, 200, 1064),
+                                   (1825, 323, 1288)])
 def test_slices_and_pitches(m, k, n, dtype):
     """Operands and results as column slices of wider matrices at odd, even and whole-vector offsets: the
     contiguous call's bits, neighbours (NaN) untouched and unread."""
