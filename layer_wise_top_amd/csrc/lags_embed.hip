@@ -82,6 +82,7 @@ template <int TD, int D, bool WIDE, int U> __global__ __launch_bounds__(256) voi
 // ids still sort (16384 tokens whose frequencies fall as 1 / rank: half of them in the first
 // of 256 workgroups).
 constexpr int kSortWaves = 16, kHeld = 16;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <bool WIDE> __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(EmbedArgs a)
 {
     extern __shared__ uint32_t cnt[];               // [wave][a.w], then each id's count
@@ -181,24 +182,28 @@ template <bool WIDE> __global__ __launch_bounds__(64 * kSortWaves) void k_embed_
         }
     }
     if (a.add) return;
-    const uint32_t T = 1u << a.zl;                   // lanes a row of zeros
-    const f32x4_u4 zero = {0, 0, 0, 0};
+    // Rows of a flat buffer's slice start anywhere: vectors from the first whole line of 128 bytes on, single
+    // values before and behind them.  With zeros of more than 128 MB, which the cache would only have to write
+    // back, past it: 700 tokens of 60000 x 1501 fp32 121 -> 92 us, 16384 of 50304 x 2048 bf16 one value off 136 -> 122
+    // (lines of their own 120 -> 117); 700 of 10000 x 1500 (60 MB) stays at 21, past the cache 26.
+    const uint32_t T = 1u << a.zl, lane0 = threadIdx.x & (T - 1);
+    const f32x4 zero = {0, 0, 0, 0};
     for (uint32_t v = threadIdx.x >> a.zl; v < w; v += 64 * kSortWaves >> a.zl) {
         if (count[v]) continue;
         float *p = a.dtable + (size_t)(lo + v) * a.cols;
-        for (uint32_t c = (threadIdx.x & (T - 1)) * 4; c < a.cols; c += T * 4) {
-            if (c + 4 <= a.cols)
-                *(f32x4_u4 *)(p + c) = zero;
-            else
-                for (uint32_t j = c; j < a.cols; ++j) p[j] = 0;
-        }
+        const uint32_t head = min(a.cols, (uint32_t)(-(uintptr_t)p >> 2) & 31), body = head + ((a.cols - head) & ~3u);
+        for (uint32_t c = lane0; c < head; c += T) p[c] = 0;
+        if (a.past)
+            for (uint32_t c = head + lane0 * 4; c < body; c += T * 4) __builtin_nontemporal_store(zero, (f32x4 *)(p + c));
+        else
+            for (uint32_t c = head + lane0 * 4; c < body; c += T * 4) *(f32x4 *)(p + c) = zero;
+        if (body + lane0 < a.cols) p[body + lane0] = 0;
     }
 }
 
-// Sums of one chunk's tokens for each id in it.  2^tl lanes span a slab of a row's
+// Sums of one chunk's C tokens for each id in it.  2^tl lanes span a slab of a row's
 // vectors, 64 of them at most.
-constexpr uint32_t kAhead = 8;
-template <int D> __global__ __launch_bounds__(256) void k_embed_sum(EmbedArgs a)
+template <int D, uint32_t C> __global__ __launch_bounds__(256) void k_embed_sum(EmbedArgs a)
 {
     constexpr int V = Elem<D>::V, E = Elem<D>::E;
     const uint32_t T = 1u << a.tl;
@@ -206,12 +211,23 @@ template <int D> __global__ __launch_bounds__(256) void k_embed_sum(EmbedArgs a)
     const uint32_t chunk = (uint32_t)(unit / a.nslab), slab = (uint32_t)(unit % a.nslab);
     const uint32_t c = (slab * T + (threadIdx.x & (T - 1))) * V;
     const int n = (int)a.cols - (int)c;
-    const uint32_t total = a.start[a.vocab], p0 = chunk * a.chunk;
-    if (chunk >= a.nchunk || p0 >= total || n <= 0) return;
-    const uint32_t p1 = min(p0 + a.chunk, total);
-    const uint32_t before = p0 ? a.keys[p0 - 1] : kNone, after = p1 < total ? a.keys[p1] : kNone;
+    if (chunk >= a.nchunk || n <= 0) return;
+    // All places of the chunk and its neighbours' at once, not one after the other; those past the
+    // last token's are read (the workspace goes on behind them) and not looked at.
+    const uint32_t p0 = chunk * C, total = a.start[a.vocab];
+    u32x4 v[C / 8][8], t[C / 4], key[C / 4];
+#pragma unroll
+    for (uint32_t h = 0; h < C / 4; ++h) t[h] = *(const u32x4 *)(a.order + p0 + 4 * h), key[h] = *(const u32x4 *)(a.keys + p0 + 4 * h);
+    const uint32_t before = p0 ? a.keys[p0 - 1] : kNone, next = a.keys[p0 + C];
+    if (p0 >= total) return;
+    const uint32_t p1 = min(p0 + C, total), after = p1 < total ? next : kNone;
+#pragma unroll
+    for (uint32_t k = 0; k < C; ++k) {
+        const uint32_t token = p0 + k < p1 ? t[k / 4][k % 4] : t[0][0];
+        v[k / 8][k % 8] = load_vec<D>((const char *)a.dy + ((size_t)token * a.lddy + c) * E, n);
+    }
     float acc[V] = {};
-    uint32_t cur = a.keys[p0];
+    uint32_t cur = key[0][0];
     bool first = cur == before;                    // the id began in an earlier chunk
     auto leave = [&](bool goes_on) {
         float *out = first ? a.part + (size_t)chunk * 2 * a.cols
@@ -233,28 +249,23 @@ template <int D> __global__ __launch_bounds__(256) void k_embed_sum(EmbedArgs a)
             }
         }
     };
-    for (uint32_t p = p0; p < p1; p += kAhead) {
-        // eight places at a time; those past the last token's are not looked at
-        u32x4 v[kAhead], t[2], key[2];
-        for (int h = 0; h < 2; ++h) t[h] = *(const u32x4 *)(a.order + p + 4 * h), key[h] = *(const u32x4 *)(a.keys + p + 4 * h);
+    auto take = [&](const u32x4(&w)[8], uint32_t k0) __attribute__((always_inline)) {
 #pragma unroll
-        for (uint32_t k = 0; k < kAhead; ++k) {
-            const uint32_t token = p + k < p1 ? t[k / 4][k % 4] : t[0][0];
-            v[k] = load_vec<D>((const char *)a.dy + ((size_t)token * a.lddy + c) * E, n);
-        }
-#pragma unroll
-        for (uint32_t k = 0; k < kAhead; ++k) {
-            if (p + k >= p1) break;
+        for (uint32_t i = 0; i < 8; ++i) {
+            const uint32_t k = k0 + i;
+            if (p0 + k >= p1) break;
             if (key[k / 4][k % 4] != cur) {
                 leave(false);
                 cur = key[k / 4][k % 4], first = false;
                 for (int j = 0; j < V; ++j) acc[j] = 0;
             }
             float f[V];
-            Elem<D>::unpack(v[k], f);
+            Elem<D>::unpack(w[i], f);
             for (int j = 0; j < V; ++j) acc[j] += f[j];
         }
-    }
+    };
+    take(v[0], 0);
+    if constexpr (C > 8) take(v[1], 8);
     leave(cur == after);
 }
 
@@ -440,6 +451,7 @@ hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wi
         });
     }
     a.zl = log2_up(((uint64_t)a.cols + 3) / 4, 2, 10);
+    a.past = (uint64_t)a.vocab * a.cols * 4 > (uint64_t)128 << 20;
     const uint32_t groups = (a.vocab + a.w - 1) / a.w, lds = (kSortWaves + 1) * a.w * 4;
     if (wide)
         k_embed_sort<true><<<groups, 64 * kSortWaves, lds, s>>>(a);
@@ -447,12 +459,16 @@ hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wi
         k_embed_sort<false><<<groups, 64 * kSortWaves, lds, s>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const uint32_t sums = (uint32_t)p.sumwgs;
-    switch (dtype) {
-    case kF32: k_embed_sum<kF32><<<sums, 256, 0, s>>>(a); break;
-    case kBF16: k_embed_sum<kBF16><<<sums, 256, 0, s>>>(a); break;
-    default: k_embed_sum<kF16><<<sums, 256, 0, s>>>(a); break;
-    }
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    const hipError_t e = by_bool(p.chunk == 8, [&](auto few) {
+        constexpr uint32_t C = few ? 8 : 16;
+        switch (dtype) {
+        case kF32: k_embed_sum<kF32, C><<<sums, 256, 0, s>>>(a); break;
+        case kBF16: k_embed_sum<kBF16, C><<<sums, 256, 0, s>>>(a); break;
+        default: k_embed_sum<kF16, C><<<sums, 256, 0, s>>>(a); break;
+        }
+        return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
     k_embed_join<<<(uint32_t)((uint64_t)a.nchunk * a.njoin), 256, 0, s>>>(a);
     return hipGetLastError();
 }
