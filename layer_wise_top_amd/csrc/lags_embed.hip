@@ -10,9 +10,9 @@
 // leave a sum for each chunk, which are then added up in the order of the chunks.
 // No atomics on floats: results repeat bit for bit.
 //   lookup, 16384 tokens of 50304 x 2048, fp32 to bf16   26 us (3.4 TB/s with each row read once)
-//   gradient of the same                                 118 us (4.0 TB/s): 72 sorting beside 350 MB of
-//                                                        zeros, 40 the sums, 6 joining them
-//   gradient, 700 tokens of 10000 x 1500 fp32            22 us: 15, 4, 4
+//   gradient of the same                                 117 us (4.1 TB/s): 71 sorting beside 350 MB of
+//                                                        zeros, 39 the sums, 7 joining them
+//   gradient, 700 tokens of 10000 x 1500 fp32            21 us: 14, 4, 3
 // Many more tokens are bound by the sort of the most frequent ids in one workgroup: 200000 tokens of 50304 x
 // 512 take 333 us.
 #include "lags_gn.h"
@@ -25,6 +25,7 @@ namespace {
 
 // The id of token t; `none` (never below vocab) where it is outside the vocabulary.
 constexpr uint32_t kNone = 0xffffffffu;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <bool WIDE> __device__ inline uint32_t id_of(const EmbedArgs &a, int64_t t)
 {
     if constexpr (WIDE) {
@@ -72,6 +73,23 @@ template <int TD, int D, bool WIDE, int U> __global__ __launch_bounds__(256) voi
     }
 }
 
+// n zeros from p on, by T lanes.  Rows of a flat buffer's slice start anywhere: vectors from the first whole line
+// of 128 bytes on, single values before and behind them.  `past`: zeros of more than 128 MB, which the cache would
+// only have to write back, go past it: 700 tokens of 60000 x 1501 fp32 121 -> 92 us, 16384 of 50304 x 2048 bf16 one
+// value off 136 -> 122 (rows of whole lines 120 -> 117), 256 of 50304 x 2001 96 -> 79; 700 of 10000 x 1500 (60 MB) stays at 21, past the
+// cache 26.
+__device__ inline void zeros(float *p, uint32_t n, uint32_t lane, uint32_t T, uint32_t past)
+{
+    const f32x4 zero = {0, 0, 0, 0};
+    const uint32_t head = min(n, (uint32_t)(-(uintptr_t)p >> 2) & 31), body = head + ((n - head) & ~3u);
+    for (uint32_t c = lane; c < head; c += T) p[c] = 0;
+    if (past)
+        for (uint32_t c = head + lane * 4; c < body; c += T * 4) __builtin_nontemporal_store(zero, (f32x4 *)(p + c));
+    else
+        for (uint32_t c = head + lane * 4; c < body; c += T * 4) *(f32x4 *)(p + c) = zero;
+    if (body + lane < n) p[body + lane] = 0;
+}
+
 // Tokens sorted by id: order[], their ids keys[], and start[v], the first place
 // of id v (start[vocab]: how many tokens have an id); and (not adding) zeros in the
 // rows of ids without tokens.  A workgroup owns a.w ids.  Its 16 waves each read a
@@ -82,7 +100,6 @@ template <int TD, int D, bool WIDE, int U> __global__ __launch_bounds__(256) voi
 // ids still sort (16384 tokens whose frequencies fall as 1 / rank: half of them in the first
 // of 256 workgroups).
 constexpr int kSortWaves = 16, kHeld = 16;
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 template <bool WIDE> __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(EmbedArgs a)
 {
     extern __shared__ uint32_t cnt[];               // [wave][a.w], then each id's count
@@ -182,23 +199,9 @@ template <bool WIDE> __global__ __launch_bounds__(64 * kSortWaves) void k_embed_
         }
     }
     if (a.add) return;
-    // Rows of a flat buffer's slice start anywhere: vectors from the first whole line of 128 bytes on, single
-    // values before and behind them.  With zeros of more than 128 MB, which the cache would only have to write
-    // back, past it: 700 tokens of 60000 x 1501 fp32 121 -> 92 us, 16384 of 50304 x 2048 bf16 one value off 136 -> 122
-    // (lines of their own 120 -> 117); 700 of 10000 x 1500 (60 MB) stays at 21, past the cache 26.
-    const uint32_t T = 1u << a.zl, lane0 = threadIdx.x & (T - 1);
-    const f32x4 zero = {0, 0, 0, 0};
-    for (uint32_t v = threadIdx.x >> a.zl; v < w; v += 64 * kSortWaves >> a.zl) {
-        if (count[v]) continue;
-        float *p = a.dtable + (size_t)(lo + v) * a.cols;
-        const uint32_t head = min(a.cols, (uint32_t)(-(uintptr_t)p >> 2) & 31), body = head + ((a.cols - head) & ~3u);
-        for (uint32_t c = lane0; c < head; c += T) p[c] = 0;
-        if (a.past)
-            for (uint32_t c = head + lane0 * 4; c < body; c += T * 4) __builtin_nontemporal_store(zero, (f32x4 *)(p + c));
-        else
-            for (uint32_t c = head + lane0 * 4; c < body; c += T * 4) *(f32x4 *)(p + c) = zero;
-        if (body + lane0 < a.cols) p[body + lane0] = 0;
-    }
+    const uint32_t T = 1u << a.zl;
+    for (uint32_t v = threadIdx.x >> a.zl; v < w; v += 64 * kSortWaves >> a.zl)
+        if (!count[v]) zeros(a.dtable + (size_t)(lo + v) * a.cols, a.cols, threadIdx.x & (T - 1), T, a.past);
 }
 
 // Sums of one chunk's C tokens for each id in it.  2^tl lanes span a slab of a row's
@@ -329,30 +332,33 @@ template <int D, bool WIDE> __global__ __launch_bounds__(256) void k_embed_few(E
         uint64_t m[Q], any = 0;
 #pragma unroll
         for (int q = 0; q < Q; ++q) any |= m[q] = __ballot(id[q] == v);
-        if (!any && a.add) continue;
+        if (!any) {
+            const uint32_t s0 = unit % a.nslab * 64 * V;
+            if (!a.add) zeros(a.dtable + (size_t)v * a.cols + s0, min(64u * V, a.cols - s0), lane, 64, a.past);
+            continue;
+        }
         if (n <= 0) continue;
         float *out = a.dtable + (size_t)v * a.cols + c;
         float acc[V] = {};
-        if (any)
 #pragma unroll
-            for (int q = 0; q < Q; ++q)
-                for (uint64_t left = m[q]; left;) {
-                    u32x4 x[U];
-                    int k = 0;
+        for (int q = 0; q < Q; ++q)
+            for (uint64_t left = m[q]; left;) {
+                u32x4 x[U];
+                int k = 0;
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int t = left ? __builtin_ctzll(left) : 0;
-                        if (left) x[u] = load_vec<D>((const char *)a.dy + ((q * 64 + t) * a.lddy + c) * E, n), ++k;
-                        left &= left - 1;
-                    }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (u >= k) break;
-                        float f[V];
-                        Elem<D>::unpack(x[u], f);
-                        for (int j = 0; j < V; ++j) acc[j] += f[j];
-                    }
+                for (int u = 0; u < U; ++u) {
+                    const int t = left ? __builtin_ctzll(left) : 0;
+                    if (left) x[u] = load_vec<D>((const char *)a.dy + ((q * 64 + t) * a.lddy + c) * E, n), ++k;
+                    left &= left - 1;
                 }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (u >= k) break;
+                    float f[V];
+                    Elem<D>::unpack(x[u], f);
+                    for (int j = 0; j < V; ++j) acc[j] += f[j];
+                }
+            }
 #pragma unroll
         for (int i = 0; i < V; i += 4) {
             if (i + 4 <= n) {
@@ -436,6 +442,7 @@ hipError_t launch_embed(EmbedArgs a, int table, int dtype, bool wide, hipStream_
 hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wide, hipStream_t s)
 {
     a.w = p.w, a.chunk = p.chunk, a.nchunk = p.nchunk, a.tl = p.tl, a.nslab = p.nslab, a.njoin = p.njoin;
+    a.past = (uint64_t)a.vocab * a.cols * 4 > (uint64_t)128 << 20;
     if (p.few) {
         const uint32_t V = 16 / elem_bytes(dtype);
         a.nslab = ((a.cols + V - 1) / V + 63) / 64;
@@ -451,7 +458,6 @@ hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wi
         });
     }
     a.zl = log2_up(((uint64_t)a.cols + 3) / 4, 2, 10);
-    a.past = (uint64_t)a.vocab * a.cols * 4 > (uint64_t)128 << 20;
     const uint32_t groups = (a.vocab + a.w - 1) / a.w, lds = (kSortWaves + 1) * a.w * 4;
     if (wide)
         k_embed_sort<true><<<groups, 64 * kSortWaves, lds, s>>>(a);

@@ -74,7 +74,7 @@ EmbedSpace embed_space(int64_t tokens, int64_t vocab, int64_t cols)
 {
     auto up = [](size_t n) { return (n + 15) / 16 * 16; };
     EmbedSpace w;
-    w.order = 0;                     // read eight at a time: what follows is the workspace's too
+    w.order = 0;                     // read a chunk at a time: what follows is the workspace's too
     w.keys = up((size_t)tokens * 4);
     w.start = w.keys + up((size_t)tokens * 4);
     w.part = w.start + up(((size_t)vocab + 1) * 4);
