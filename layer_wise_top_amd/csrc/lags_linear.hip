@@ -51,7 +51,7 @@ constexpr Cost kCost[3][4] = {
 
 // The tile and the slices of k with the least time by a model of it (`least`): the rounds of workgroups on 256
 // compute units, or the bytes of the operands; then the slices' sums, written and read again.
-//   700 x 6000 x 1500 fp32   116 us (128 x 128, 7 slices; 64 x 64 in 6: 121, whole 193), the library's product 132
+//   700 x 6000 x 1500 fp32   116 us (128 x 128, 7 slices; 64 x 64 in 6: 121, whole 193), the library's product 113
 //   1 x 2048 x 8192 bf16     11.1 us (64 x 64, 3 slices; whole 15)
 static LinPlan plan_of(int dtype, bool backward, int64_t M, int64_t N, int64_t K, double &least)
 {
