@@ -273,8 +273,11 @@ __global__ __launch_bounds__(MOST ? MOST : 256) void k_ln_backward(LnArgs a)
             } else {
                 row.values(x[k], k, xh[k]);
             }
+            // Columns past the last channel hold s = 0 and no mean: xh stays 0 there, where -mean * rstd may be
+            // infinite (a constant row far from zero) and would make the row's second sum 0 * inf.
+            const float mu = row.nv[k] > 0 ? mean : 0.0f;
             for (int j = 0; j < V; ++j) {
-                xh[k][j] = (xh[k][j] - mean) * rs;
+                xh[k][j] = (xh[k][j] - (EDGE == kWhole || j < row.nv[k] ? mu : 0.0f)) * rs;
                 db[k][j] += d[j];
                 dg[k][j] = __builtin_fmaf(d[j], xh[k][j], dg[k][j]);
                 g[k][j] = d[j] * gamma[k][j];

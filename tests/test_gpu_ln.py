@@ -357,3 +357,39 @@ def test_past_2_31_elements():
     dx, dg, db = _backward(y, gamma, mean, rstd, ckpt=ck[0])
     assert torch.equal(dx[-5:], dx[:5]) and torch.equal(dx[1 << 19:(1 << 19) + 1024], dx[:1024])
     assert torch.isfinite(dg).all() and torch.isfinite(db).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,c", [(1, 40), (5, 100), (9, 104), (6, 1500), (4, 1501), (3, 2500), (3, 5000)])
+def test_backward_of_constant_rows_far_from_zero(m, c, dtype):
+    """A constant row whose mean times rstd is past fp32's range has xh = 0 in every channel, so
+    dx = rstd (g - <g>) + dsum; the lanes past its last channel, where s is not the mean, add nothing.  From s,
+    from s in a slice that starts off a word, and from its checkpoint; the rows beside it are as without it."""
+    import torch
+    from layer_wise_top_amd import lags
+    rng = np.random.default_rng(m * 13 + c)
+    x, dy, ds = _dev(_rows(rng, m, c), dtype), _dev(rng.standard_normal((m, c)), dtype), _dev(rng.standard_normal((m, c)), dtype)
+    gamma, beta = _par(rng, c)
+    x[0] = 2.0 ** 122                    # held exactly by every type here and by a checkpoint
+    _, mean, rstd, _, _ = _forward(x, gamma, beta)
+    mean[0], rstd[0] = 2.0 ** 122, 1e-5 ** -0.5
+    assert torch.isinf(mean[0] * rstd[0])
+    wide = torch.full((m, c + 3), float("nan"), dtype=x.dtype, device="cuda")
+    wide[:, 1:1 + c] = x
+    ck = lags.checkpoint(m, c)
+    lags.lags_ckpt_pack(x, ck)
+    r, g = float(rstd[0]), _np(dy)[0] * _np(gamma)
+    want = r * (g - g.mean()) + _np(ds)[0]
+    # products and differences round once each, the mean's sum in chains below R.CHAIN
+    err = r * ((R.CHAIN + 4) * R.U * np.abs(g).mean() + 4 * R.U * np.abs(g)) + 4 * R.U * (np.abs(want) + np.abs(_np(ds)[0]))
+    for tag, kw in (("s", dict(x=x)), ("slice", dict(x=wide[:, 1:1 + c])), ("checkpoint", dict(ckpt=ck))):
+        dx, dg, db = _backward(dy, gamma, mean, rstd, dsum=ds, **kw)
+        R.check(f"{m}x{c} {dtype} {tag}", _np(dx)[0], want, err, dtype)
+        assert torch.isfinite(dg).all() and torch.isfinite(db).all()
+        if m > 1 and tag != "slice":
+            y, ck1 = x.clone(), lags.checkpoint(m, c)
+            y[0] = 0
+            lags.lags_ckpt_pack(y, ck1)
+            zero = torch.cat([mean[:1] * 0, mean[1:]])
+            beside, dg0, _ = _backward(dy, gamma, zero, rstd, dsum=ds, **({"x": y} if "x" in kw else {"ckpt": ck1}))
+            assert torch.equal(dx[1:], beside[1:]) and torch.equal(dg, dg0)
