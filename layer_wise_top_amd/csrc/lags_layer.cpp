@@ -101,10 +101,9 @@ int plan_anew(const lags_linear *l, LinearCall &c)
     c.fwd = linear_plan(l->dtype, false, M, l->outs, l->cols);
     c.bwd = linear_plan(l->dtype, true, M, l->cols, l->outs);
     c.dz = dz_plan(l->dtype, M, l->outs);
-    // threads of one launch: the product's, and those that join its slices
+    // Tiles are counted in 32 bits; outputs of so many fit no memory.
     for (const LinPlan *p : {&c.fwd, &c.bwd})
-        if ((u128)p->tm * p->tn * p->split * 512 > kMostThreads) return LAGS_ERANGE;
-    if ((u128)M * std::max(l->outs, l->cols) > kMostThreads && (c.fwd.split > 1 || c.bwd.split > 1)) return LAGS_ERANGE;
+        if ((u128)p->tm * p->tn * p->split > 0xffffffffu) return LAGS_ERANGE;
     const u128 f = c.fwd.split > 1 ? (u128)c.fwd.split * M * l->outs * 4 : 0;
     const u128 b = c.bwd.split > 1 ? (u128)c.bwd.split * M * l->cols * 4 : 0;
     // dbias is done before the product's sums are written

@@ -12,6 +12,7 @@
 #include "lags_gn.h"
 #include "lags_layer.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace lags {
@@ -669,13 +670,28 @@ template <int D> hipError_t product(const LinPlan &p, LinArgs a, bool nn, int ho
             if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
             a.b = a.turned, a.ldb = a.K, nn = false;
         }
-    a.tm = p.tm, a.tn = p.tn, a.split = p.split, a.k_per = p.k_per;
-    const hipError_t e = nn ? run_tile<D, true>(p.tile, a, how, s) : run_tile<D, false>(p.tile, a, how, s);
-    if (e != hipSuccess || a.split == 1) return e;
-    constexpr uint32_t V = Elem<D>::V;
-    const uint64_t threads = (uint64_t)a.M * ((a.N + V - 1) / V);
-    k_linear_join<D><<<(uint32_t)((threads + 255) / 256), 256, 0, s>>>(a);
-    return hipGetLastError();
+    a.tn = p.tn, a.split = p.split, a.k_per = p.k_per;
+    constexpr int64_t V = Elem<D>::V, E = Elem<D>::E;
+    const LinTile &t = kLinTiles[p.tile];
+    const uint64_t vecs = (a.N + V - 1) / V;
+    // A launch takes so many rows at most: tiles, and threads that join their slices.  Rows beyond are launches
+    // of their own, which take the workspace one after the other; an output's sums do not depend on the cut.
+    int64_t most = (int64_t)(kMostThreads / ((uint64_t)64 * t.wm * t.wn * p.tn * p.split)) * t.bm;
+    if (a.split > 1) most = std::min(most, (int64_t)((kMostThreads - 255) / vecs));
+    for (int64_t left = a.M;;) {
+        a.M = std::min(left, most);
+        a.tm = (uint32_t)((a.M + t.bm - 1) / t.bm);
+        hipError_t e = nn ? run_tile<D, true>(p.tile, a, how, s) : run_tile<D, false>(p.tile, a, how, s);
+        if (e == hipSuccess && a.split > 1) {
+            k_linear_join<D><<<(uint32_t)(((uint64_t)a.M * vecs + 255) / 256), 256, 0, s>>>(a);
+            e = hipGetLastError();
+        }
+        left -= a.M;
+        if (e != hipSuccess || !left) return e;
+        a.a = (const char *)a.a + a.M * a.lda * E, a.y = (char *)a.y + a.M * a.ldy * E;
+        if (a.z) a.z = (char *)a.z + a.M * a.ldz * E;
+        if (a.res) a.res = (const char *)a.res + a.M * a.ldr * E;
+    }
 }
 template <int D> hipError_t slopes(const DzPlan &p, LinArgs a, hipStream_t s)
 {

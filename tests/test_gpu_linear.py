@@ -407,3 +407,46 @@ def test_past_2_31_elements():
     assert torch.equal(y2[-7:], y2[:7]) and torch.equal(z2[1 << 20:(1 << 20) + 4096], z2[:4096])
     dz2, _, dx2 = _backward(y2, w2, "relu", z2)
     assert torch.equal(dz2[-7:], dz2[:7]) and torch.equal(dx2[-7:], dx2[:7])
+
+
+@pytest.mark.parametrize("m,k,n", [(16448, 72, 262152), (5546, 9, 774729)])
+def test_outputs_of_a_large_vocabulary(m, k, n):
+    """More than 2^32 outputs, and a backward whose sums over them are split: columns at both ends and past
+    2^31 entries, dx whole."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.Generator(device="cuda").manual_seed(m)
+    x, w = (torch.randn(r, k, generator=g, device="cuda").bfloat16() for r in (m, n))
+    bias = torch.randn(n, generator=g, device="cuda")
+    y, _ = _forward(x, w, "none", bias)
+    _, db, dx = _backward(y, w)
+    for c in (slice(0, 130), slice(n // 2, n // 2 + 70), slice(n - 133, n)):
+        _check_forward(f"{m}x{k}x{n} {c}", x, w[c], "none", bias[c], None, y[:, c], None, "bf16")
+        d = _np(y[:, c])
+        # rows of a lane, waves and chunks, as in _check_backward
+        R.check("dbias", _np(db[c]), d.sum(0), 256 * R.U * np.abs(d).sum(0))
+    want, mag = (torch.zeros(m, k, dtype=torch.float64, device="cuda") for _ in range(2))
+    for i in range(0, n, 16384):
+        d, v = y[:, i:i + 16384].double(), w[i:i + 16384].double()
+        want += d @ v
+        mag += d.abs() @ v.abs()
+    R.check("dx", _np(dx), _np(want), _sum_bound(n, "bf16") * _np(mag), "bf16")
+
+
+def test_rows_of_several_launches():
+    """Tiles of more threads than a launch has: x, z, res and y go on where the first launch ends."""
+    import torch
+    m = (1 << 30) + 77
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, res = (torch.empty(m, 1, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    w = torch.full((1, 1), -1.5, dtype=torch.bfloat16, device="cuda")
+    y, z = _forward(x, w, "relu", res=res, keep=True)
+    _, _, dx = _backward(res, w, bias=False)
+    for i in range(0, m, 1 << 26):
+        c = slice(i, i + (1 << 26))
+        f = x[c].float() * -1.5                       # exact in fp32
+        assert torch.equal(z[c], f.bfloat16()) and torch.equal(y[c], (f.clamp(min=0) + res[c].float()).bfloat16()), i
+        assert torch.equal(dx[c], (res[c].float() * -1.5).bfloat16()), i

@@ -67,3 +67,19 @@ def test_tiles_and_slices_cover_the_product():
             sums = 4 * p.split * rows * n if p.split > 1 else 0
             assert need >= sums + (2 * cols * outs if p.turn else 0)
             assert not p.turn or (back and dtype != "f32" and outs % 8 == 0)
+
+
+# (rows, cols, outs): a large vocabulary's logits, sums split where an operand has more than 2^32 entries, and
+# products whose tiles need more threads than one launch has
+LARGE = [(16384, 1500, 262144), (32000, 2048, 151936), (20000, 8192, 262144), (65664, 512, 128256), (5546, 9, 774729),
+         (11749, 368010, 1), (1 << 29, 8, 8), ((1 << 30) + 77, 1, 1), ((1 << 31) - 1, 2, 3)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_large_layers_are_taken(shape, dtype):
+    code = {"f32": 0, "bf16": 1, "f16": 2}[dtype]
+    for rows in (shape[0], shape[0] - 1, 0):
+        of = lags.LinearShape(rows, shape[1], shape[2], code, 0)
+        need = int(lags.lib().lags_linear_workspace_bytes(ctypes.byref(of)))
+        assert 16 <= need < 1 << 37, (rows, need)
