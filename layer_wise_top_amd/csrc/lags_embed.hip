@@ -388,15 +388,17 @@ EmbedPlan embed_plan(int dtype, int64_t tokens, int64_t vocab, int64_t cols)
     // One launch for a few tokens.  us in one and in three: 100 tokens of 100 x 100 fp32 6.5 and 12.2, 200 of 10000
     // x 1500 13 and 21, 256 of 50304 x 2048 bf16 75 and 93; but 700 of 10000 x 1500 57 and 21, where the rows of a
     // frequent id come 64 tokens at a time.
-    p.few = tokens <= kFew;
+    // (a wave writes 64 vectors of four ids' rows; a table that needs more threads than a launch has takes three)
+    const uint32_t V = 16 / elem_bytes(dtype);
+    const uint64_t vecs = (cols + V - 1) / V;
+    p.fewwgs = ((uint64_t)((vocab + kFewIds - 1) / kFewIds) * ((vecs + 63) / 64) + 3) / 4;
+    p.few = tokens <= kFew && p.fewwgs * 256 <= kMostThreads;
     // ids a workgroup of the sort: 256 workgroups if the counts of 16 waves then stay within 32 KiB
     p.w = (uint32_t)std::min<int64_t>(512, (vocab + 255) / 256);
     // Tokens a chunk: short ones fill the card where there are few.  us for 8, 16 and 32: 700 tokens of 1500
     // fp32 22, 24, 28; 16384 of 2048 bf16 124, 118, 118 (1000 ids: 44, 40, 39).
     p.chunk = tokens < 8192 ? 8 : 16;
     p.nchunk = (uint32_t)((tokens + p.chunk - 1) / p.chunk);
-    const uint32_t V = 16 / elem_bytes(dtype);
-    const uint64_t vecs = (cols + V - 1) / V;
     p.tl = log2_up(vecs, 2, 6);
     p.nslab = (uint32_t)((vecs + (1u << p.tl) - 1) >> p.tl);
     const uint64_t units = (uint64_t)p.nchunk * p.nslab, per = 256 >> p.tl;
@@ -444,10 +446,8 @@ hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wi
     a.w = p.w, a.chunk = p.chunk, a.nchunk = p.nchunk, a.tl = p.tl, a.nslab = p.nslab, a.njoin = p.njoin;
     a.past = (uint64_t)a.vocab * a.cols * 4 > (uint64_t)128 << 20;
     if (p.few) {
-        const uint32_t V = 16 / elem_bytes(dtype);
+        const uint32_t V = 16 / elem_bytes(dtype), g = (uint32_t)p.fewwgs;
         a.nslab = ((a.cols + V - 1) / V + 63) / 64;
-        const uint64_t units = (uint64_t)((a.vocab + kFewIds - 1) / kFewIds) * a.nslab;
-        const uint32_t g = (uint32_t)((units + 3) / 4);
         return by_bool(wide, [&](auto w) {
             switch (dtype) {
             case kF32: k_embed_few<kF32, w><<<g, 256, 0, s>>>(a); break;
@@ -464,6 +464,7 @@ hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wi
     else
         k_embed_sort<false><<<groups, 64 * kSortWaves, lds, s>>>(a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (!a.nchunk) return hipSuccess;
     const uint32_t sums = (uint32_t)p.sumwgs;
     const hipError_t e = by_bool(p.chunk == 8, [&](auto few) {
         constexpr uint32_t C = few ? 8 : 16;

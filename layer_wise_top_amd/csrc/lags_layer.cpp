@@ -280,8 +280,7 @@ int lags_embed_grad(int64_t tokens, int64_t vocab, int64_t cols, const void *ids
     Region r[4];
     if (int rc = matrix(dy, tokens, cols, lddy, dtype, r[0]); rc != LAGS_OK) return rc;
     const EmbedPlan p = embed_plan(dtype, tokens, vocab, cols);
-    // threads of one launch; few tokens' is 16 a vector of the gradient's rows of 256 bytes or more
-    if (p.few && (u128)vocab * (cols / 256 + 1) * 16 > kMostThreads) return LAGS_ERANGE;
+    // threads of one launch
     if ((u128)p.sumwgs * 256 > kMostThreads || (u128)p.nchunk * p.njoin * 256 > kMostThreads)
         return LAGS_ERANGE;
     const EmbedSpace w = embed_space(tokens, vocab, cols);

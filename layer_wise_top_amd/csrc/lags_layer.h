@@ -57,7 +57,7 @@ constexpr int kFew = 256;                    // tokens of a gradient in one laun
 struct EmbedPlan {
     bool few;
     uint32_t w, chunk, nchunk, tl, nslab, njoin;
-    uint64_t sumwgs;
+    uint64_t sumwgs, fewwgs;                 // workgroups of the sums; of the gradient in one launch
 };
 EmbedPlan embed_plan(int dtype, int64_t tokens, int64_t vocab, int64_t cols);
 hipError_t launch_embed(EmbedArgs a, int table, int dtype, bool wide, hipStream_t s);

@@ -294,3 +294,21 @@ def test_past_2_31_elements():
     got = _grad(ids, y, v, dtable=w)
     assert torch.equal(got[v - 1], y[1] + y[4]) and torch.equal(got[v - 2], y[2]) and torch.equal(got[0], y[0])
     assert not got[6:v - 2].any() and not got[1:5].any()
+
+
+@pytest.mark.parametrize("tokens", [0, 100, 300])
+def test_largest_vocabulary(tokens):
+    """2^26 ids, in one launch and in three; small whole numbers, so that sums are exact."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 10 << 30:
+        pytest.skip("needs 10 GB")
+    v, c = 1 << 26, 5
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    ids = torch.randint(0, v, (tokens,), generator=g, device="cuda")
+    if tokens:
+        ids[:6] = torch.tensor([0, v - 1, v - 2, v - 1, v, -1])
+    dy = torch.randint(-9, 10, (tokens, c), generator=g, device="cuda").float()
+    real = (ids >= 0) & (ids < v)
+    want = torch.zeros(v, c, device="cuda").index_add_(0, ids[real], dy[real])
+    assert torch.equal(_grad(ids, dy, v), want)
+    assert torch.equal(_grad(ids, dy, v, scale=2.0, dtable=want.clone(), add=True), 3 * want)

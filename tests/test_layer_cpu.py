@@ -240,3 +240,32 @@ def test_binding_refuses_host_tensors():
         lags.Linear(4, 8, 8, act="tanh")
     with pytest.raises(ValueError):
         lags.linear_workspace(lags.Linear(4, 0, 8))
+
+
+class EmbedPlan(ctypes.Structure):
+    _fields_ = ([("few", ctypes.c_bool)] +
+                [(k, ctypes.c_uint32) for k in ("w", "chunk", "nchunk", "tl", "nslab", "njoin")] +
+                [(k, ctypes.c_uint64) for k in ("sumwgs", "fewwgs")])
+
+
+def test_embedding_gradient_in_one_launch_has_its_threads():
+    """A gradient that is written by one launch needs a wave for 64 vectors of four rows, four waves a
+    workgroup: fewer than 2^32 threads, or it is not taken.  (With 2^32 nothing would be launched.)  No
+    table of up to 2^26 rows is refused for its size."""
+    import random
+    L = lags.lib()
+    plan = L._ZN4lags10embed_planEilll
+    plan.restype, plan.argtypes = EmbedPlan, [ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]
+    rng = random.Random(1)
+    cases = [(d, 100, v, c) for d in (0, 1, 2) for v in (1 << 26, (1 << 26) - 1, (1 << 26) - 4) for c in (
+        256, 512, 513, 768, 769, 1000, 1023, 1024, 1025, 2048, 2049)]
+    cases += [(rng.randrange(3), rng.randrange(257), int(2 ** rng.uniform(0, 26)), int(2 ** rng.uniform(0, 12)))
+              for _ in range(3000)]
+    for dtype, tokens, vocab, cols in cases:
+        p = plan(dtype, tokens, vocab, cols)
+        waves = -(-vocab // 4) * -(-cols // (256 if dtype == 0 else 512))
+        assert p.fewwgs == -(-waves // 4), (dtype, tokens, vocab, cols)
+        assert not p.few or -(-waves // 4) * 256 < 1 << 32, (dtype, tokens, vocab, cols)
+        assert p.few or tokens > 256 or vocab * cols > 1 << 34, (dtype, tokens, vocab, cols)
+        rc = L.lags_embed_grad(tokens, vocab, cols, P(0), P(1), cols, dtype, 1.0, P(2), 2, None, 0, None)
+        assert rc == EWS, (rc, dtype, tokens, vocab, cols)
