@@ -277,7 +277,7 @@ template <int D, uint32_t C> __global__ __launch_bounds__(256) void k_embed_sum(
 __global__ __launch_bounds__(256) void k_embed_join(EmbedArgs a)
 {
     __shared__ float4 sh[4][64];
-    const uint32_t chunk = blockIdx.x / a.njoin, c = (blockIdx.x % a.njoin * 64 + (threadIdx.x & 63)) * 4;
+    const uint32_t chunk = a.first + blockIdx.x / a.njoin, c = (blockIdx.x % a.njoin * 64 + (threadIdx.x & 63)) * 4;
     const uint32_t total = a.start[a.vocab], p0 = chunk * a.chunk, p1 = p0 + a.chunk;
     if (p1 >= total) return;
     const uint32_t v = a.keys[p1 - 1];
@@ -476,8 +476,13 @@ hipError_t launch_embed_grad(const EmbedPlan &p, EmbedArgs a, int dtype, bool wi
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    k_embed_join<<<(uint32_t)((uint64_t)a.nchunk * a.njoin), 256, 0, s>>>(a);
-    return hipGetLastError();
+    // chunks of one launch, at most
+    const uint32_t most = (uint32_t)(kMostThreads / 256 / a.njoin);
+    for (a.first = 0; a.first < a.nchunk; a.first += most) {
+        k_embed_join<<<std::min(most, a.nchunk - a.first) * a.njoin, 256, 0, s>>>(a);
+        if (hipError_t j = hipGetLastError(); j != hipSuccess) return j;
+    }
+    return hipSuccess;
 }
 
 }  // namespace lags

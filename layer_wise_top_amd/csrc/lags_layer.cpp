@@ -280,9 +280,8 @@ int lags_embed_grad(int64_t tokens, int64_t vocab, int64_t cols, const void *ids
     Region r[4];
     if (int rc = matrix(dy, tokens, cols, lddy, dtype, r[0]); rc != LAGS_OK) return rc;
     const EmbedPlan p = embed_plan(dtype, tokens, vocab, cols);
-    // threads of one launch
-    if ((u128)p.sumwgs * 256 > kMostThreads || (u128)p.nchunk * p.njoin * 256 > kMostThreads)
-        return LAGS_ERANGE;
+    // threads of the sums' launch
+    if ((u128)p.sumwgs * 256 > kMostThreads) return LAGS_ERANGE;
     const EmbedSpace w = embed_space(tokens, vocab, cols);
     if (!ws || !aligned(ws, 16) || ws_bytes < w.bytes) return LAGS_EWORKSPACE;
     r[1] = flat(ids, (size_t)tokens * (wide ? 8 : 4)), r[2] = flat(dtable, (size_t)vocab * cols * 4), r[3] = flat(ws, w.bytes);

@@ -50,7 +50,7 @@ struct EmbedArgs {
     float *part;
     uint32_t w;                              // ids a workgroup of the sort
     uint32_t chunk, nchunk, tl, nslab;       // tokens a chunk, chunks, 2^tl lanes a slab, slabs a row
-    uint32_t zl, njoin;                      // 2^zl lanes a row of zeros; 256-channel parts
+    uint32_t zl, njoin, first;               // 2^zl lanes a row of zeros; 256-channel parts; a join's first chunk
     uint32_t past;                           // zeros go past the caches
 };
 constexpr int kFew = 256;                    // tokens of a gradient in one launch, at most

@@ -312,3 +312,22 @@ def test_largest_vocabulary(tokens):
     want = torch.zeros(v, c, device="cuda").index_add_(0, ids[real], dy[real])
     assert torch.equal(_grad(ids, dy, v), want)
     assert torch.equal(_grad(ids, dy, v, scale=2.0, dtable=want.clone(), add=True), 3 * want)
+
+
+def test_chunks_of_several_joins():
+    """More chunks of 16 tokens than one launch of the join has workgroups.  Sums of small whole numbers are
+    exact, below 2^24."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    v, n, c = 1000, (1 << 28) + (1 << 20) + 5, 2
+    ids = torch.arange(n, dtype=torch.int32, device="cuda") % v
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dy = torch.randint(0, 16, (n, c), generator=g, device="cuda", dtype=torch.int8).float()
+    got = _grad(ids, dy, v)
+    whole = n // v * v
+    want = torch.zeros(v, c, dtype=torch.float64, device="cuda")
+    for i in range(0, whole, v << 14):
+        want += dy[i:min(whole, i + (v << 14))].view(-1, v, c).sum(0, dtype=torch.float64)
+    want[:n - whole] += dy[whole:].double()
+    assert torch.equal(got.double(), want)

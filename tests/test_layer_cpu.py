@@ -269,3 +269,14 @@ def test_embedding_gradient_in_one_launch_has_its_threads():
         assert p.few or tokens > 256 or vocab * cols > 1 << 34, (dtype, tokens, vocab, cols)
         rc = L.lags_embed_grad(tokens, vocab, cols, P(0), P(1), cols, dtype, 1.0, P(2), 2, None, 0, None)
         assert rc == EWS, (rc, dtype, tokens, vocab, cols)
+
+
+@pytest.mark.parametrize("tokens,cols,dtype", [((1 << 28) + 5, 1, 0), ((1 << 28) + 5, 8, 1), (1 << 30, 4, 2),
+                                               (70000000, 1024, 1), ((1 << 31) - 1, 1, 0), (1 << 27, 520, 1)])
+def test_embedding_gradient_of_many_tokens_is_taken(tokens, cols, dtype):
+    """Joining the chunks' sums takes a workgroup a chunk, and as many launches as that needs."""
+    L = lags.lib()
+    need = L.lags_embed_workspace_bytes(tokens, 1000, cols)
+    assert 8 * tokens < need < 1 << 36
+    rc = L.lags_embed_grad(tokens, 1000, cols, P(0), P(16), cols, dtype, 1.0, P(32), 0, None, 0, None)
+    assert rc == EWS
