@@ -11,7 +11,6 @@ import ctypes
 import os
 
 import numpy as np
-import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblags.so")
@@ -78,13 +77,34 @@ class LinearShape(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
+class _Unloaded:
+    """What `torch` is until its first use, which imports it: this file's constants and the
+    structures of its arguments need none."""
+
+    def __getattr__(self, name):
+        return getattr(_load_torch(), name)
+
+
+torch, _C, _F32, _U8 = _Unloaded(), None, None, None
+_DTYPES = {}
+
+
+def _load_torch():
+    global torch, _C, _F32, _U8
+    if _C is None:
+        import torch as t
+        _DTYPES.update({t.float32: LAGS_F32, t.bfloat16: LAGS_BF16, t.float16: LAGS_F16})
+        torch, _F32, _U8, _C = t, t.float32, t.uint8, t._C       # _C last: other threads ask for it
+    return torch
+
+
 _lib = None
 
 
 def lib():
     """Load liblags.so (raises if it has not been built).
 
-    torch is imported first (above): its HIP runtime (torch/lib/libamdhip64.so, soname
+    torch is imported first: its HIP runtime (torch/lib/libamdhip64.so, soname
     libamdhip64.so.7) must be the one the library binds to, since the device
     pointers and streams passed in come from torch.  Loaded the other way
     round, the library would pull the system runtime under its soname and
@@ -95,6 +115,7 @@ def lib():
         return _lib
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is not built; run `python -m layer_wise_top_amd.build`")
+    _load_torch()       # binds the library to torch's HIP runtime
     L = ctypes.CDLL(LIB_PATH)
     i32, i64, u32, vp, sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32,
                              ctypes.c_void_p, ctypes.c_size_t)
@@ -430,11 +451,10 @@ def kernel_names():
 # arguments costs more than the kernels.  Each check asks torch once, and
 # pointers go to ctypes as plain integers.
 
-_C, _F32, _U8 = torch._C, torch.float32, torch.uint8
-_DTYPES = {torch.float32: LAGS_F32, torch.bfloat16: LAGS_BF16, torch.float16: LAGS_F16}
-
 
 def _dtype_code(dtype) -> int:
+    if _C is None:
+        _load_torch()
     code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
@@ -449,6 +469,8 @@ def _place(first, name: str, stream):
             raise TypeError(f"{name} must be a device tensor")
     except AttributeError:
         raise TypeError(f"{name} must be a device tensor") from None
+    if _C is None:
+        _load_torch()
     dev = _C._cuda_getDevice()
     return dev, _C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 

@@ -4,6 +4,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -207,3 +208,25 @@ def test_static_sparsify_size_limit_without_a_device():
                                                 base + (17 << 30), 0, None)
     assert rc == lags.LAGS_ESTATIC
     assert lags.lib().lags_sparsify_layers_static(None, base, base, base, base, 0, None) == -1
+
+
+@pytest.mark.parametrize("first", [
+    "assert lags.strerror(0)",
+    "assert lags.LayerNorm(2, 3).dtype is __import__('torch').float32",
+    "import torch; assert lags.Linear(1, 2, 3, dtype=torch.bfloat16).shape.dtype == lags.LAGS_BF16",
+    "import torch; assert lags._dtype_code(torch.float16) == lags.LAGS_F16"])
+def test_binding_is_imported_without_torch(first):
+    """The binding's names and structures need no torch, which its first use brings."""
+    code = f"""
+import sys
+from layer_wise_top_amd import lags
+lags.LnShape(3, 4, lags.LAGS_BF16, 1e-5), lags.LinearShape(1, 2, 3, lags.LAGS_F32, lags.LINEAR_ACTS["gelu"])
+assert "torch" not in sys.modules
+{first}
+import torch
+assert lags.torch.float32 is torch.float32 and lags.GroupNorm(1, 2, 4, 2).dtype is torch.float32
+assert lags.lags_ckpt_bytes(1, 1) == 32
+print("import ok")
+"""
+    out = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "import ok" in out.stdout, out.stdout + out.stderr

@@ -48,3 +48,21 @@ def test_library_loaded_before_torch():
                          timeout=300)
     assert out.returncode == 0, out.stdout + out.stderr
     assert "load order ok" in out.stdout
+
+
+FIRST = """
+import torch
+from layer_wise_top_amd import lags
+x = torch.arange(-8.0, 8.0, device="cuda").reshape(2, 8)
+ck, y = torch.zeros(64, dtype=torch.uint8, device="cuda"), torch.empty_like(x)
+lags.lags_ckpt_pack(x, ck)                       # the first use of the binding: its tensors are checked
+lags.lags_ckpt_unpack(ck, y)
+assert torch.equal(x, y)
+print("first use ok", flush=True)
+"""
+
+
+def test_first_use_is_an_operator():
+    out = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stdout + out.stderr
+    assert "first use ok" in out.stdout
