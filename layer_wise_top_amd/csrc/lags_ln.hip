@@ -57,12 +57,12 @@ template <int D, int NV, bool WIDE, int EDGE> struct Row {
             }
         }
     }
-    // the values of a vector; those past the last channel are zero
-    __device__ void values(u32x4 v, int k, float (&f)[V]) const
+    // the values of a vector; those past the last channel are `past`
+    __device__ void values(u32x4 v, int k, float (&f)[V], float past = 0.0f) const
     {
         Elem<D>::unpack(v, f);
         if constexpr (EDGE != kWhole)
-            for (int j = 0; j < V; ++j) f[j] = j < nv[k] ? f[j] : 0.0f;
+            for (int j = 0; j < V; ++j) f[j] = j < nv[k] ? f[j] : past;
     }
     __device__ void store(void *base, int64_t row, int64_t ld, int k, u32x4 v) const
     {
@@ -268,16 +268,18 @@ __global__ __launch_bounds__(MOST ? MOST : 256) void k_ln_backward(LnArgs a)
         for (int k = 0; k < NV; ++k) {
             float d[V];
             row.values(dy[k], k, d);
+            // Columns past the last channel have s = mean and xh = 0: with s = 0, as loaded, -mean * rstd may be
+            // infinite (a constant row far from zero) and would make the row's second sum 0 * inf.
             if constexpr (CK) {
                 for (int i = 0; i < V / 4; ++i) run_values(q[k][i], run_step(sc[k]), xh[k] + 4 * i);
+                if constexpr (EDGE != kWhole)
+                    for (int j = 0; j < V; ++j) xh[k][j] = j < row.nv[k] ? xh[k][j] : mean;
             } else {
-                row.values(x[k], k, xh[k]);
+                row.values(x[k], k, xh[k], mean);
             }
-            // Columns past the last channel hold s = 0 and no mean: xh stays 0 there, where -mean * rstd may be
-            // infinite (a constant row far from zero) and would make the row's second sum 0 * inf.
-            const float mu = row.nv[k] > 0 ? mean : 0.0f;
+            const float mu = EDGE == kWhole && row.nv[k] <= 0 ? 0.0f : mean;
             for (int j = 0; j < V; ++j) {
-                xh[k][j] = (xh[k][j] - (EDGE == kWhole || j < row.nv[k] ? mu : 0.0f)) * rs;
+                xh[k][j] = (xh[k][j] - mu) * rs;
                 db[k][j] += d[j];
                 dg[k][j] = __builtin_fmaf(d[j], xh[k][j], dg[k][j]);
                 g[k][j] = d[j] * gamma[k][j];
