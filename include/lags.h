@@ -610,6 +610,7 @@ size_t lags_embed_workspace_bytes(int64_t tokens, int64_t vocab, int64_t cols);
  *           flat gradient;
  *   flags:  LAGS_IDS64 and LAGS_GRAD_ADD (dtable is added to, and only the rows of
  *           ids that occur are touched).
+ * Sizes as lags_embed_forward's; 2^37 values of dy and more may be LAGS_ERANGE.
  * Returns LAGS_OK, LAGS_EINVAL, LAGS_ERANGE, LAGS_EWORKSPACE, LAGS_EHIP.
  */
 int lags_embed_grad(int64_t tokens, int64_t vocab, int64_t cols, const void *ids, const void *dy,
@@ -624,7 +625,8 @@ int lags_embed_grad(int64_t tokens, int64_t vocab, int64_t cols, const void *ids
  * and sums are held in fp32; z and y are each rounded to dtype once, from fp32.  The
  * weight's gradient is lags_ckpt_wgrad's (from dz and x's checkpoint).
  * rows in [0, 2^31), cols, outs and every ld in [1, LAGS_LINEAR_MAX]; act any
- * LAGS_ACT_*, LAGS_ACT_GELU among them.
+ * LAGS_ACT_*, LAGS_ACT_GELU among them.  (Products of 2^32 tiles are LAGS_ERANGE: 2^40
+ * outputs and more.)
  */
 typedef struct lags_linear {
     int64_t rows, cols, outs;
@@ -655,8 +657,8 @@ int lags_linear_forward(const lags_linear *lin, const void *x, int64_t ldx, cons
 /*
  * Gradients of the forward call for the gradient dy of y (which is also that of
  * res):
- *   dz = dy * act'(z), rounded to dtype;  dbias = its sum over the rows before the
- *   rounding;  dx = dz W.
+ *   dz = dy * act'(z), rounded to dtype (an infinite dy where relu's slope is 0 gives
+ *   NaN);  dbias = its sum over the rows before the rounding;  dx = dz W.
  *   dy:    device matrix [rows, outs] (lddy);
  *   z:     as the forward left it (ldz); null for LAGS_ACT_NONE;
  *   w, dx: device matrices (ldw, lddx), or both null (the first layer's input

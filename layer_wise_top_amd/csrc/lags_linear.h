@@ -25,7 +25,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ---- activations -----------------------------------------------------------
 // s = 1 / (1 + exp(-u)) and 1 - s.  16-bit types: the hardware's exponential and
-// reciprocal, good to a few units of 2^-23.
+// reciprocal, good to a few units of 2^-23 and, since u / ln 2 is rounded first, |u| 2^-24 of the
+// result (5e-6 where |u| is 87).  That is far below dz's rounding; the fp32 sums of dbias take it as it is.
 template <int D> __device__ inline float sigmoid(float u, float &rest)
 {
     if constexpr (D == kF32) {
@@ -176,10 +177,13 @@ __device__ inline uint32_t deal(uint32_t b, uint32_t n)
 // come after them, a step ahead of need.  One barrier a step, before its last quarter.
 //   8192 x 8192 x 8192 bf16     772 us, 1.42 PFLOP/s (the library's product 674 to 714; operands of zeros, which
 //                               hold the clock up, 550)
-//   16384 x 2048 to 8192 bf16   416 us, 1.32 (373 to 392); with gelu and z 496: the results of a compute unit's one
-//                               workgroup are written between its products, not beside them.  The
-//                               matrix units are busy 62 % of that, 80 % of 16384 x 8192 to 2048
+//   16384 x 2048 to 8192 bf16   416 to 422 us, 1.3 (373 to 392); with gelu and z 482 to 518: the results of a compute
+//                               unit's one workgroup are written between its products, not beside them.  The
+//                               matrix units are busy 62 % of that, 78 to 80 % of 16384 x 8192 to 2048
 //   8192 x 8192 x 8192 fp32     7310 us, 150 TFLOP/s (7160)
+// Products that do not fill whole rounds of 256 tiles, or whose operands are staged through registers, take 1.5 to
+// 2.4 times what their operations need: 3230 x 6224 to 5400 bf16 279 us (136 at 1.6 PFLOP/s; the library's 219);
+// 16384 x 2048 to 8192 with W one word off a vector 497, one value off 622, of 2049 columns 641.
 // NN: B is [k][n].  HOW a tile gets into LDS: kDirect, loads that write it themselves
 // (operands of whole, aligned 16-byte vectors); kWords and kHalves, through
 // registers, rows that start on any word, or on any half of one (five words are
@@ -607,7 +611,7 @@ template <int D> __global__ __launch_bounds__(256) void k_linear_dz(LinArgs a)
 }
 
 // W [N][K] (a.b, a.ldb) turned round: out [K][N].  A workgroup turns 64 x 64
-// values in LDS.  8192 x 2048 bf16: see linear_plan.
+// values in LDS.  8192 x 2048 bf16 17 us, 3.9 TB/s.
 template <int D> __global__ __launch_bounds__(256) void k_linear_turn(LinArgs a, void *out)
 {
     static_assert(Elem<D>::E == 2, "");

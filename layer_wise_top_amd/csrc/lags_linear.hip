@@ -37,8 +37,9 @@ namespace {
 // Fitted to 620 products of 16 to 16384 rows and 64 to 8192 columns and outputs, each in every tile and up to 27
 // slices: the plan's time is 1.015, 1.03 and 1.016 of the best measured one, geometric mean.  Up to 64 rows of 16
 // bits take W from memory, not from a cache that others' reads have filled, and `alone` is 2 (backward 1.5)
-// times that: over 107 products of 1 to 64 rows with W not in any cache 1.05 and 1.07 of the best, without it 1.15 and
-// 1.10.
+// times that: over 107 products of 1 to 64 rows with W not in any cache 1.05 and 1.07 of the best of these tiles,
+// without it 1.15 and 1.10.  Their tiles are mostly empty there, and reading W once would take 1.2 to 2.9 times less.
+// Operands staged through registers take the same plan, so that sums have the same order, though not the same times.
 struct Cost {
     float full, alone, out;
     int held;
@@ -51,8 +52,10 @@ constexpr Cost kCost[3][4] = {
 
 // The tile and the slices of k with the least time by a model of it (`least`): the rounds of workgroups on 256
 // compute units, or the bytes of the operands; then the slices' sums, written and read again.
-//   700 x 6000 x 1500 fp32   116 us (128 x 128, 7 slices; 64 x 64 in 6: 121, whole 193), the library's product 113
-//   1 x 2048 x 8192 bf16     11.1 us (64 x 64, 3 slices; whole 15)
+//   700 x 6000 to 1500 fp32   114 to 119 us (128 x 128, 7 slices; 64 x 64 in 6: 121, whole 193), the library's
+//                             product 113
+//   1 x 2048 to 8192 bf16     9.5 us with W in the caches, 13.6 with W from memory (32 x 128, 4 slices; W's bytes at
+//                             the rate of a copy 6.5; the library's product 17 and 13)
 static LinPlan plan_of(int dtype, bool backward, int64_t M, int64_t N, int64_t K, double &least)
 {
     const int64_t e = elem_bytes(dtype), ks = 128 / e, steps = (K + ks - 1) / ks;

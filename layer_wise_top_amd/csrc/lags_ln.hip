@@ -9,11 +9,16 @@
 // rows are a workgroup's.  Workgroups walk the rows with gamma and beta, and
 // backward the channel sums, in registers; the next rows are requested before
 // this one's sums.
-//   16384 x 2048 bf16, forward with a residual   49 us, 5.4 TB/s (a large copy reaches 5.0)
+//   16384 x 2048 bf16, forward with a residual   50 us, 5.3 TB/s (a large copy reaches 5.1)
 //   the same, backward from a checkpoint         54 us, 4.4 TB/s, 5 of it the parameters' last sum
-//   4000 x 8190 bf16                             forward 52 us, backward 61
-//   2000 x 16384 bf16                            forward 53 us, backward 122: 1024 threads have 128
-//                                                registers, and some spill
+//   16384 x 2048 fp32                            forward 101 us, backward 106, 5.2 TB/s
+//   700 x 1500 fp32, backward                    12 us: 10 for 175 workgroups, a row a wave and less than a
+//                                                wave a SIMD, then the parameters' last sum
+//   4000 x 8190 bf16                             forward 46 us, backward 53 (45 from a checkpoint at a copy's rate)
+//   2000 x 16384 bf16                            forward 47 us, backward 119 (45)
+//   2000 x 16384 fp32                            forward 114 us, backward 215 (102 each)
+// 8193 channels and more: 1024 threads have 128 registers, and the fp32 forward spills 19 of them, the
+// backward 23 to 44 (16 bits) and 81 to 86 (fp32).
 #include "lags_layer.h"
 #include "lags_gn.h"
 
@@ -412,7 +417,7 @@ LnPlan ln_plan(int dtype, bool backward, int edge, int64_t rows, uint32_t C)
     // 55, 43, 44; backward 2048 from a checkpoint 55, 61, 75; 65536 rows of 512: 70, 53, 54; 6000 of 4096: 43,
     // 49, 63.
     int64_t groups = 512;
-    if (backward && p.threads >= 256 && p.nv == 2 * most) groups = 256;
+    if (backward && p.nv == 2 * most) groups = 256;
     if (wide) groups = p.threads == 128 ? 1024 : backward || p.threads > 256 ? 256 : 512;
     const int64_t want = (rows + per - 1) / per;
     // backward: a single workgroup of up to four rounds needs no second launch for its sums
